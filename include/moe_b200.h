@@ -79,7 +79,10 @@ typedef struct {
   int32_t M, H, I, E, top_k, block_size;
 } moe_shape_t;
 
-typedef enum { MOE_W_BF16 = 0, MOE_W_NVFP4 = 1 } moe_wdtype_t;
+typedef enum { MOE_W_BF16 = 0, MOE_W_NVFP4 = 1, MOE_W_INT8 = 2 } moe_wdtype_t;
+
+/* Element type of the tensors that come in more than one. */
+typedef enum { MOE_DT_F32 = 0, MOE_DT_BF16 = 1 } moe_dtype_t;
 
 /* Expert weights.
  * MOE_W_BF16:  gate, up: bf16 [E, I, H]; down: bf16 [E, H, I] (the contraction
@@ -87,7 +90,14 @@ typedef enum { MOE_W_BF16 = 0, MOE_W_NVFP4 = 1 } moe_wdtype_t;
  * MOE_W_NVFP4: gate, up, down: blobs written by moe_prepare_nvfp4_weights
  *              (from moe_quantize_nvfp4 of W_gate/W_up as E matrices [I,H] and
  *              W_down as E matrices [H,I]); gate_gs, up_gs, down_gs: the device
- *              fp32 [E] per-expert global scales that moe_quantize_nvfp4 wrote. */
+ *              fp32 [E] per-expert global scales that moe_quantize_nvfp4 wrote.
+ * MOE_W_INT8:  gate, up: int8 codes [E, I, H]; down: int8 codes [E, H, I];
+ *              gate_gs, up_gs: device fp32 [E, I] and down_gs: fp32 [E, H], the
+ *              scale of every weight row (output channel), as moe_quantize_int8
+ *              writes them for the matrices as E*I (E*H) rows.  Codes are in
+ *              [-127, 127]; -128 is taken as it stands.  A call that does not
+ *              use a matrix (the up projection: down; the down projection:
+ *              gate and up) ignores its pointers. */
 typedef struct {
   moe_wdtype_t dtype;
   const void* gate;
@@ -147,6 +157,51 @@ MOE_API moe_status_t moe_route_ex(const moe_bf16_t* x, const moe_bf16_t* w_route
                                   const moe_route_opts_t* opts, int32_t* topk_ids, float* topk_w, void* ws,
                                   size_t ws_bytes, moe_stream_t stream);
 
+/* ------------------------------------------------- routing with groups --
+ * Top-k routing from given logits, with the experts in groups.  The E experts
+ * form n_group groups of E / n_group neighbours.  For token t:
+ *   p_e   = 1 / (1 + exp(-z_e)) (SIGMOID), or the softmax of z[t,:] over all E
+ *   key_e = p_e + bias_e: the bias (balancing) shifts the selection only
+ *   s_g   = the largest key of group g (MOE_GROUP_MAX), or the sum of its two
+ *           largest (MOE_GROUP_TOP2; of a one-expert group, its key)
+ *   the topk_group groups with the largest s_g stay, ties -> lower group;
+ *   topk_ids[t,0..K) = the K largest keys among their experts, descending, ties
+ *           -> lower id;  topk_w[t,k] = w_k * routed_scale with w_k = p_k, or
+ *           p_k / sum_j p_j over the K selected (renormalize; 0 if that sum is 0).
+ * p, keys and group scores are those of fp64 arithmetic; weights are rounded
+ * to fp32 once.  A NaN logit counts as -inf, a NaN key or group score ranks as
+ * -inf; with +inf among softmax logits the +inf entries share the scores, and
+ * a row of -inf only has scores 0.  The ids are always K different experts of
+ * the chosen groups, also where keys are -inf.
+ * logits: fp32 or bf16 (dtype) [M, E], row t at logits + t * ld elements, ld >= E;
+ * bias: fp32 [E] (nullable -> 0); topk_ids: int32 [M,K]; topk_w: fp32 [M,K].
+ * Logits and bias need the alignment of their type only.  opts is a host
+ * pointer, read during the call.
+ * Accepted: M >= 1; 1 <= E <= 1024; 1 <= n_group <= 32, E % n_group == 0;
+ * 1 <= topk_group <= n_group; 1 <= top_k <= min(32, topk_group * E / n_group);
+ * M * top_k < 2^31; else UNSUPPORTED.  INVALID_ARG for a null pointer, an
+ * unknown dtype, scoring or group_score, ld < E, or a routed_scale that is not
+ * finite and > 0. */
+typedef enum { MOE_GROUP_MAX = 0, MOE_GROUP_TOP2 = 1 } moe_group_score_t;
+typedef struct {
+  int32_t scoring;      /* moe_score_t */
+  int32_t renormalize;  /* nonzero: renormalise over the K selected */
+  int32_t n_group;      /* groups of E / n_group neighbouring experts; 1: no groups */
+  int32_t topk_group;   /* groups that stay */
+  int32_t group_score;  /* moe_group_score_t */
+  float routed_scale;   /* multiplies every weight */
+} moe_group_opts_t;
+MOE_API moe_status_t moe_route_logits(const void* logits, moe_dtype_t dtype, int64_t ld, const float* bias, int32_t M,
+                                      int32_t E, int32_t top_k, const moe_group_opts_t* opts, int32_t* topk_ids,
+                                      float* topk_w, moe_stream_t stream);
+
+/* The same from x and w_router: the logits of moe_route (its z without a bias,
+ * fp32, in that fixed order) followed by moe_route_logits.  x, w_router, shape
+ * and workspace as moe_route; bias and opts as moe_route_logits. */
+MOE_API moe_status_t moe_route_group(const moe_bf16_t* x, const moe_bf16_t* w_router, const float* bias, moe_shape_t s,
+                                     const moe_group_opts_t* opts, int32_t* topk_ids, float* topk_w, void* ws,
+                                     size_t ws_bytes, moe_stream_t stream);
+
 /* ---------------------------------------------------------------- align --
  * Expert-major block plan (flashinfer PR #6511 analysis, §5).
  *   expert_counts[e]      = #{f : topk_ids[f] == e}, f = t*K + k
@@ -179,7 +234,9 @@ MOE_API size_t moe_align_capacity(moe_shape_t s); /* M*top_k + E*(block_size-1) 
  * scaled by gs_gate[e] * gs_x and gs_up[e] * gs_x before SwiGLU; the block-
  * scaled GEMM runs on 2-SM pairs (cta_group::2) when I % 256 == 0 and on
  * single SMs otherwise or with MOE_NVFP4_PAIR=0 in the environment, with the
- * same bits either way. */
+ * same bits either way.  MOE_W_INT8: every token's x is quantised on the fly
+ * (moe_quantize_int8's codes and scale) into ws (required); g and u are the
+ * exact integer products times the token's and the channel's scale. */
 MOE_API moe_status_t moe_grouped_up_swiglu(const moe_bf16_t* x, const moe_weights_t* w, const moe_plan_t* plan,
                                    moe_shape_t s, moe_bf16_t* h, void* ws, size_t ws_bytes, int32_t* err_flag,
                                    moe_stream_t stream);
@@ -216,7 +273,9 @@ MOE_API moe_status_t moe_grouped_up_swiglu_routed(const moe_bf16_t* x, const moe
  * MOE_W_NVFP4: h is quantised on the fly (global scale from the amax over the
  * real plan rows of h) into ws, moe_down_workspace_size(s, MOE_W_NVFP4) bytes
  * (required); the accumulators are scaled by gs_down[e] * gs_h; 2-SM pairs
- * when H % 512 == 0 (MOE_NVFP4_PAIR=0: single SMs), the same bits either way. */
+ * when H % 512 == 0 (MOE_NVFP4_PAIR=0: single SMs), the same bits either way.
+ * MOE_W_INT8: the real plan rows of h are quantised on the fly, each with its
+ * own scale, into ws, moe_down_workspace_size(s, MOE_W_INT8) bytes (required). */
 MOE_API moe_status_t moe_grouped_down(const moe_bf16_t* h, const moe_weights_t* w, const moe_plan_t* plan,
                               moe_shape_t s, moe_bf16_t* y, void* ws, size_t ws_bytes, int32_t* err_flag,
                               moe_stream_t stream);
@@ -299,6 +358,38 @@ MOE_API size_t moe_nvfp4_quantize_workspace_size(int64_t n_mats);
 MOE_API moe_status_t moe_prepare_nvfp4_weights(const uint8_t* codes, const uint8_t* scales, moe_shape_t s, int which,
                                        void* blob, size_t blob_bytes, moe_stream_t stream);
 MOE_API size_t moe_nvfp4_blob_bytes(moe_shape_t s, int which);
+
+/* ---------------------------------------------------------------- int8 ---
+ * Rows of bf16 as symmetric 8-bit codes with one fp32 scale per row:
+ *   a = max |v| of the row;  scale = a / 127;  code = rint(127 v / a), ties to
+ *   even (a = 0: scale 0, codes 0)
+ * the codes are those of exact arithmetic.  A row that holds an infinity or a
+ * NaN gets codes 0 and the scale NaN: every product with it is NaN.
+ * src: bf16, row r at src + r * ld elements; codes: int8, row r at codes +
+ * r * pitch (bytes from cols to the pitch are left as they were); scales: fp32
+ * [rows].  Any alignment.  rows, cols >= 1, ld >= cols, pitch >= cols; rows < 2^31,
+ * cols <= MOE_INT8_MAX_K. */
+#define MOE_INT8_MAX_K 131072 /* 131072 * 127 * 127 < 2^31: the sums are exact */
+MOE_API moe_status_t moe_quantize_int8(const moe_bf16_t* src, int64_t ld, int64_t rows, int64_t cols, int8_t* codes,
+                                       int64_t pitch, float* scales, moe_stream_t stream);
+
+/* Dense product with 8-bit weights (a projection that every token takes, such
+ * as a shared expert's):
+ *   out[m,n] = sx[m] * w_scale[n] * sum_k xq[m,k] * w[n,k]
+ * with xq, sx of x as moe_quantize_int8 (on the fly into ws), the sum exact in
+ * int32, the scaling in fp32, rounded to out_dtype (bf16 or fp32) at the end.
+ * x: bf16, row m at x + m * ldx elements (any alignment, ldx >= K); w: int8
+ * [N, K] codes, row n at w + n * ldw, w 16-byte aligned, ldw >= K a multiple of
+ * 16 (codes between K and ldw are not read as values); w_scale: fp32 [N]; out:
+ * row m at out + m * ldo elements, ldo >= N; ws: moe_linear_int8_workspace_size
+ * bytes, 16-byte aligned; err_flag (nullable) as everywhere.
+ * Accepted: 1 <= M, N <= 2^30 with (M/32 + 1) * (N/128 + 1) < 2^31;
+ * 1 <= K <= MOE_INT8_MAX_K; else UNSUPPORTED. */
+MOE_API moe_status_t moe_linear_int8(const moe_bf16_t* x, int64_t ldx, const int8_t* w, int64_t ldw,
+                                     const float* w_scale, int64_t M, int64_t N, int64_t K, void* out, int64_t ldo,
+                                     moe_dtype_t out_dtype, void* ws, size_t ws_bytes, int32_t* err_flag,
+                                     moe_stream_t stream);
+MOE_API size_t moe_linear_int8_workspace_size(int64_t M, int64_t N, int64_t K);
 
 /* ---------------------------------------------------------------- route, no allocation
  * No counterpart on the pages: this entry point exists for callers that cannot

@@ -8,6 +8,7 @@ cannot be loaded, every call raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import threading
@@ -20,7 +21,9 @@ __all__ = [
     "finalize_rmsnorm", "layer", "layer_workspace_size", "up_workspace_size", "layer_workspace_layout", "align_capacity",
     "route_workspace_size", "get_device_error", "status_string", "STATUS", "NVFP4Weights", "quantize_nvfp4",
     "prepare_nvfp4_weights", "nvfp4_weights", "nvfp4_blob_bytes", "grouped_up_swiglu_nvfp4", "grouped_down_nvfp4",
-    "layer_nvfp4", "down_workspace_size",
+    "layer_nvfp4", "down_workspace_size", "route_logits", "route_group", "GROUP_MAX", "GROUP_TOP2", "Int8Weights",
+    "quantize_int8", "int8_weights", "linear_int8", "linear_int8_workspace_size", "grouped_up_swiglu_int8",
+    "grouped_down_int8", "layer_int8",
 ]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -30,7 +33,7 @@ _lib = None
 
 STATUS = {0: "MOE_OK", 1: "MOE_ERR_INVALID_ARG", 2: "MOE_ERR_UNSUPPORTED", 3: "MOE_ERR_WORKSPACE",
           4: "MOE_ERR_INVALID_INPUT", 5: "MOE_ERR_TIMEOUT", 6: "MOE_ERR_CUDA"}
-MOE_W_BF16, MOE_W_NVFP4 = 0, 1
+MOE_W_BF16, MOE_W_NVFP4, MOE_W_INT8 = 0, 1, 2
 
 
 class MoEError(RuntimeError):
@@ -61,7 +64,14 @@ class _RouteOpts(ctypes.Structure):
                 ("routed_scale", ctypes.c_float)]
 
 
+class _GroupOpts(ctypes.Structure):
+    _fields_ = [("scoring", ctypes.c_int32), ("renormalize", ctypes.c_int32), ("n_group", ctypes.c_int32),
+                ("topk_group", ctypes.c_int32), ("group_score", ctypes.c_int32), ("routed_scale", ctypes.c_float)]
+
+
 SCORE_SOFTMAX, SCORE_SIGMOID = 0, 1
+GROUP_MAX, GROUP_TOP2 = 0, 1
+_DTYPES = {torch.float32: 0, torch.bfloat16: 1}  # moe_dtype_t
 
 _LAYOUT_FIELDS = ["err_flag", "logits", "topk_ids", "topk_w", "sorted_ids", "block_expert", "expert_counts",
                   "expert_offsets", "num_tokens_post_padded", "h", "y", "act_scratch", "sync", "total"]
@@ -91,6 +101,13 @@ def _declare(L):
         "moe_route": (st, [vp, vp, vp, _Shape, vp, vp, vp, sz, vp]),
         "moe_route_workspace_size": (sz, [_Shape]),
         "moe_route_ex": (st, [vp, vp, vp, _Shape, ctypes.POINTER(_RouteOpts), vp, vp, vp, sz, vp]),
+        "moe_route_logits": (st, [vp, st, ctypes.c_int64, vp, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32,
+                                  ctypes.POINTER(_GroupOpts), vp, vp, vp]),
+        "moe_route_group": (st, [vp, vp, vp, _Shape, ctypes.POINTER(_GroupOpts), vp, vp, vp, sz, vp]),
+        "moe_quantize_int8": (st, [vp, ctypes.c_int64, ctypes.c_int64, ctypes.c_int64, vp, ctypes.c_int64, vp, vp]),
+        "moe_linear_int8": (st, [vp, ctypes.c_int64, vp, ctypes.c_int64, vp, ctypes.c_int64, ctypes.c_int64,
+                                 ctypes.c_int64, vp, ctypes.c_int64, st, vp, sz, vp, vp]),
+        "moe_linear_int8_workspace_size": (sz, [ctypes.c_int64, ctypes.c_int64, ctypes.c_int64]),
         "moe_align_block_size": (st, [vp, _Shape, vp, vp, vp, vp, vp, vp, vp]),
         "moe_align_capacity": (sz, [_Shape]),
         "moe_grouped_up_swiglu": (st, [vp, ctypes.POINTER(_Weights), ctypes.POINTER(_Plan), _Shape, vp, vp, sz,
@@ -230,6 +247,80 @@ def route_ex(x, w_router, bias, top_k, scoring=SCORE_SIGMOID, renormalize=True, 
     _check(library().moe_route_ex(_ptr(_bf16(x)), _ptr(_bf16(w_router)), _ptr(bias), shape.c(), ctypes.byref(opts),
                                   _ptr(topk_ids), _ptr(topk_w), _ptr(ws), ws.numel(), _stream()), "moe_route_ex")
     return topk_ids, topk_w
+
+
+def _same_device(*ts):
+    """All the given CUDA tensors lie on one device; makes it current for the rest of the call if it is not."""
+    _need_cuda(*ts)
+    dev = ts[0].device
+    for t in ts[1:]:
+        if t is not None and t.device != dev:
+            raise ValueError("tensors on different devices")
+    return _AS_IS if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
+
+
+_AS_IS = contextlib.nullcontext()
+
+
+def _want(t, dtype, shape, what):
+    if t is not None and (t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous()):
+        raise ValueError(f"{what}: expected a contiguous {dtype} tensor of shape {tuple(shape)}")
+    return t
+
+
+def _group_opts(n_group, topk_group, group_score, scoring, renormalize, routed_scale):
+    return _GroupOpts(int(scoring), int(bool(renormalize)), int(n_group), int(topk_group), int(group_score),
+                      float(routed_scale))
+
+
+def route_logits(logits, bias, top_k, n_group=1, topk_group=1, group_score=GROUP_TOP2, scoring=SCORE_SIGMOID,
+                 renormalize=True, routed_scale=1.0, topk_ids=None, topk_w=None):
+    """Top-k routing from logits [M,E] (fp32 or bf16, rows may be strided) with the experts in ``n_group``
+    groups of which ``topk_group`` stay -> (topk_ids int32 [M,K], topk_w fp32 [M,K]).  The selection key is the
+    score (sigmoid or softmax) plus ``bias`` [E]; the weights come from the scores without it."""
+    if logits.dim() != 2 or logits.dtype not in _DTYPES or (logits.shape[1] > 1 and logits.stride(1) != 1):
+        raise ValueError("logits: expected an fp32 or bf16 [M, E] tensor with contiguous rows")
+    M, E = logits.shape
+    with _same_device(logits, bias, topk_ids, topk_w):
+        _want(bias, torch.float32, (E,), "bias")
+        topk_ids, topk_w = _routing_out(M, top_k, logits.device, topk_ids, topk_w)
+        opts = _group_opts(n_group, topk_group, group_score, scoring, renormalize, routed_scale)
+        _check(library().moe_route_logits(_ptr(logits), _DTYPES[logits.dtype], _row_stride(logits), _ptr(bias), M, E,
+                                          int(top_k), ctypes.byref(opts), _ptr(topk_ids), _ptr(topk_w), _stream()),
+               "moe_route_logits")
+    return topk_ids, topk_w
+
+
+def route_group(x, w_router, bias, top_k, n_group=1, topk_group=1, group_score=GROUP_TOP2, scoring=SCORE_SIGMOID,
+                renormalize=True, routed_scale=1.0, topk_ids=None, topk_w=None, ws=None):
+    """route_logits of the router's logits x . w_router^T (the canonical fp32 logits of route)."""
+    M, H = x.shape
+    E = w_router.shape[0]
+    shape = Shape(M, H, 128, E, top_k, 16)
+    with _same_device(x, w_router, bias, topk_ids, topk_w, ws):
+        _want(w_router, torch.bfloat16, (E, H), "w_router")
+        _want(bias, torch.float32, (E,), "bias")
+        topk_ids, topk_w = _routing_out(M, top_k, x.device, topk_ids, topk_w)
+        if ws is None:
+            ws = torch.empty(max(route_workspace_size(shape), 1), dtype=torch.uint8, device=x.device)
+        opts = _group_opts(n_group, topk_group, group_score, scoring, renormalize, routed_scale)
+        _check(library().moe_route_group(_ptr(_bf16(x)), _ptr(w_router), _ptr(bias), shape.c(), ctypes.byref(opts),
+                                         _ptr(topk_ids), _ptr(topk_w), _ptr(ws), ws.numel(), _stream()),
+               "moe_route_group")
+    return topk_ids, topk_w
+
+
+def _row_stride(t):
+    """Elements between rows (any value fits a single row)."""
+    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+
+
+def _routing_out(M, top_k, device, topk_ids, topk_w):
+    if topk_ids is None:
+        topk_ids = torch.empty(M, top_k, dtype=torch.int32, device=device)
+    if topk_w is None:
+        topk_w = torch.empty(M, top_k, dtype=torch.float32, device=device)
+    return _want(topk_ids, torch.int32, (M, top_k), "topk_ids"), _want(topk_w, torch.float32, (M, top_k), "topk_w")
 
 
 def align_block_size(topk_ids, E, block_size, err_flag=None, out=None):
@@ -453,6 +544,139 @@ def layer_nvfp4(x, w_router, bias, nw: NVFP4Weights, gamma, eps, top_k, block_si
     _check(library().moe_layer(_ptr(_bf16(x)), _ptr(_bf16(w_router)), _ptr(bias), ctypes.byref(w),
                                _ptr(_bf16(gamma)), float(eps), shape.c(), _ptr(out), _ptr(residual_out),
                                _ptr(topk_ids), _ptr(topk_w), _ptr(ws), ws.numel(), _stream()), "moe_layer")
+    return out
+
+
+# ------------------------------------------------------------------ int8
+@dataclass
+class Int8Weights:
+    """Expert weights as 8-bit codes with one fp32 scale per output channel: gate/up int8 [E,I,H] with scales
+    [E,I], down int8 [E,H,I] with scales [E,H].  A projection alone needs its own matrices only."""
+    gate: torch.Tensor | None = None
+    up: torch.Tensor | None = None
+    down: torch.Tensor | None = None
+    gate_scales: torch.Tensor | None = None
+    up_scales: torch.Tensor | None = None
+    down_scales: torch.Tensor | None = None
+
+    def check(self, shape: Shape, *names):
+        """The named matrices are there, with the shapes of ``shape``; returns them and their scales."""
+        found = []
+        for n in names:
+            rows, cols = (shape.H, shape.I) if n == "down" else (shape.I, shape.H)
+            codes, scales = getattr(self, n), getattr(self, n + "_scales")
+            if codes is None or scales is None:
+                raise ValueError(f"Int8Weights without {n}")
+            found += [_want(codes, torch.int8, (shape.E, rows, cols), n),
+                      _want(scales, torch.float32, (shape.E, rows), n + "_scales")]
+        return found
+
+    def c(self) -> _Weights:
+        p = [None if t is None else t.data_ptr() for t in (self.gate, self.up, self.down, self.gate_scales,
+                                                           self.up_scales, self.down_scales)]
+        return _Weights(MOE_W_INT8, *p)
+
+
+def quantize_int8(w):
+    """w bf16 [..., cols] -> (codes int8 of the same shape, scales fp32 [...]): code = rint(127 v / amax of the
+    row), scale = amax / 127.  The codes' rows lie a multiple of 16 bytes apart (a view of a wider buffer where
+    cols is not one), as linear_int8 takes them."""
+    with _same_device(w):
+        cols = w.shape[-1]
+        _want(w, torch.bfloat16, w.shape, "w")
+        rows = w.numel() // cols if cols else 0
+        pitch = (cols + 15) // 16 * 16
+        buf = torch.empty(*w.shape[:-1], pitch, dtype=torch.int8, device=w.device)
+        scales = torch.empty(w.shape[:-1], dtype=torch.float32, device=w.device)
+        _check(library().moe_quantize_int8(_ptr(w), cols, rows, cols, _ptr(buf), pitch, _ptr(scales), _stream()),
+               "moe_quantize_int8")
+    return buf[..., :cols], scales
+
+
+def int8_weights(w_gate, w_up, w_down) -> Int8Weights:
+    """8-bit codes and channel scales of bf16 expert weights (w_gate/w_up [E,I,H], w_down [E,H,I])."""
+    (g, gs), (u, us), (d, ds) = (quantize_int8(w) for w in (w_gate, w_up, w_down))
+    return Int8Weights(g, u, d, gs, us, ds)
+
+
+def linear_int8_workspace_size(M: int, N: int, K: int) -> int:
+    return int(library().moe_linear_int8_workspace_size(M, N, K))
+
+
+def linear_int8(x, codes, scales, out=None, out_dtype=torch.bfloat16, ws=None, err_flag=None):
+    """out[M,N] = x . W^T with W given as 8-bit codes [N,K] (rows a multiple of 16 bytes apart) and channel
+    scales [N]; x bf16 [M,K] (rows may be strided) is quantised per row on the fly.  out: bf16 or fp32."""
+    if x.dim() != 2 or x.dtype != torch.bfloat16 or (x.shape[1] > 1 and x.stride(1) != 1):
+        raise ValueError("x: expected a bf16 [M, K] tensor with contiguous rows")
+    M, K = x.shape
+    N = codes.shape[0]
+    if codes.dtype != torch.int8 or tuple(codes.shape) != (N, K) or (K > 1 and codes.stride(1) != 1):
+        raise ValueError("codes: expected an int8 [N, K] tensor with contiguous rows")
+    with _same_device(x, codes, scales, out, ws, err_flag):
+        _want(scales, torch.float32, (N,), "scales")
+        if out is None:
+            out = torch.empty(M, N, dtype=out_dtype, device=x.device)
+        elif out.dtype not in _DTYPES or tuple(out.shape) != (M, N) or (N > 1 and out.stride(1) != 1):
+            raise ValueError("out: expected a bf16 or fp32 [M, N] tensor with contiguous rows")
+        if out.dtype not in _DTYPES:
+            raise ValueError("out_dtype: expected torch.bfloat16 or torch.float32")
+        ldw = codes.stride(0) if N > 1 else (max(codes.stride(0), K) + 15) // 16 * 16
+        if ws is None:
+            ws = torch.empty(max(linear_int8_workspace_size(M, N, K), 1), dtype=torch.uint8, device=x.device)
+        _check(library().moe_linear_int8(_ptr(x), _row_stride(x), _ptr(codes), ldw, _ptr(scales), M, N, K, _ptr(out),
+                                         _row_stride(out), _DTYPES[out.dtype], _ptr(ws), ws.numel(), _ptr(err_flag),
+                                         _stream()), "moe_linear_int8")
+    return out
+
+
+def grouped_up_swiglu_int8(x, iw: Int8Weights, plan, shape: Shape, h=None, err_flag=None, ws=None):
+    """int8 form of grouped_up_swiglu (every token's x quantised on the fly into ws)."""
+    ts = iw.check(shape, "gate", "up")
+    with _same_device(x, *ts, plan["sorted_ids"], h, err_flag, ws):
+        _want(x, torch.bfloat16, (shape.M, shape.H), "x")
+        if h is None:
+            h = torch.empty(align_capacity(shape), shape.I, dtype=torch.bfloat16, device=x.device)
+        if ws is None:
+            ws = torch.empty(max(up_workspace_size(shape, MOE_W_INT8), 1), dtype=torch.uint8, device=x.device)
+        w, p = iw.c(), _plan_struct(plan)
+        _check(library().moe_grouped_up_swiglu(_ptr(x), ctypes.byref(w), ctypes.byref(p), shape.c(), _ptr(_bf16(h)),
+                                               _ptr(ws), ws.numel(), _ptr(err_flag), _stream()),
+               "moe_grouped_up_swiglu")
+    return h
+
+
+def grouped_down_int8(h, iw: Int8Weights, plan, shape: Shape, y=None, err_flag=None, ws=None):
+    """int8 form of grouped_down (the real plan rows of h quantised on the fly into ws)."""
+    ts = iw.check(shape, "down")
+    with _same_device(h, *ts, plan["sorted_ids"], y, err_flag, ws):
+        if y is None:
+            y = torch.empty(shape.M * shape.top_k, shape.H, dtype=torch.bfloat16, device=h.device)
+        if ws is None:
+            ws = torch.empty(max(down_workspace_size(shape, MOE_W_INT8), 1), dtype=torch.uint8, device=h.device)
+        w, p = iw.c(), _plan_struct(plan)
+        _check(library().moe_grouped_down(_ptr(_bf16(h)), ctypes.byref(w), ctypes.byref(p), shape.c(), _ptr(_bf16(y)),
+                                          _ptr(ws), ws.numel(), _ptr(err_flag), _stream()), "moe_grouped_down")
+    return y
+
+
+def layer_int8(x, w_router, bias, iw: Int8Weights, gamma, eps, top_k, block_size, ws=None, out=None,
+               residual_out=None, topk_ids=None, topk_w=None):
+    """The whole layer with int8 expert weights; returns out [M,H] bf16."""
+    if iw.gate is None:
+        raise ValueError("Int8Weights without gate")
+    M, H = x.shape
+    E, I = iw.gate.shape[0], iw.gate.shape[1]
+    shape = Shape(M, H, I, E, top_k, block_size)
+    ts = iw.check(shape, "gate", "up", "down")
+    with _same_device(x, w_router, bias, *ts, gamma, ws, out, residual_out, topk_ids, topk_w):
+        if ws is None:
+            ws = torch.empty(max(layer_workspace_size(shape, MOE_W_INT8), 1), dtype=torch.uint8, device=x.device)
+        if out is None:
+            out = torch.empty_like(x)
+        w = iw.c()
+        _check(library().moe_layer(_ptr(_bf16(x)), _ptr(_bf16(w_router)), _ptr(bias), ctypes.byref(w),
+                                   _ptr(_bf16(gamma)), float(eps), shape.c(), _ptr(out), _ptr(residual_out),
+                                   _ptr(topk_ids), _ptr(topk_w), _ptr(ws), ws.numel(), _stream()), "moe_layer")
     return out
 
 

@@ -84,6 +84,21 @@ bool make_map_u8(CUtensorMap* map, const void* base, uint64_t rows, uint64_t col
   return r == CUDA_SUCCESS;
 }
 
+// 2-D int8 tensor [rows, cols] with rows of `ld` bytes (a multiple of 16), read in boxes of box_rows x 128
+// codes with the 128-byte swizzle; codes past the last column or row read as 0.
+bool make_map_i8(CUtensorMap* map, const void* base, uint64_t rows, uint64_t cols, uint64_t ld, uint32_t box_rows) {
+  auto fn = encode_fn();
+  if (fn == nullptr) return false;
+  cuuint64_t dims[2] = {cols, rows};
+  cuuint64_t strides[1] = {ld};
+  cuuint32_t box[2] = {128, box_rows};
+  cuuint32_t estr[2] = {1, 1};
+  CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS;
+}
+
 // NVFP4 scale atoms ([blocks][kdim/64][512 bytes]) as a 2-D byte tensor of
 // 256-byte rows, read in boxes of 8 rows (one stage's four atoms, 2 KB) with
 // no swizzle: the shared-memory copy is the global bytes in order.
@@ -213,7 +228,7 @@ moe_status_t check_plan(const moe_plan_t* p) {
 
 moe_status_t check_weights(const moe_weights_t* w, const moe_shape_t& s) {
   if (w == nullptr) return MOE_ERR_INVALID_ARG;
-  if (w->dtype != MOE_W_BF16 && w->dtype != MOE_W_NVFP4) return MOE_ERR_UNSUPPORTED;
+  if (w->dtype != MOE_W_BF16 && w->dtype != MOE_W_NVFP4 && w->dtype != MOE_W_INT8) return MOE_ERR_UNSUPPORTED;
   if (w->dtype == MOE_W_NVFP4) {
     if (!w->gate_gs || !w->up_gs || !w->down_gs) return MOE_ERR_INVALID_ARG;
     if (s.I % 256 != 0) return MOE_ERR_UNSUPPORTED;  // the NVFP4 kernels step 256 elements along I
@@ -553,6 +568,119 @@ moe_status_t run_down_nvfp4(const moe_bf16_t* h, const moe_weights_t* w, const m
   return cuda_status(moe::launch_nvfp4_down(md, mh, a, num_sms(), stream));
 }
 
+// ---------------------------------------------------------------- int8 rows
+// Workspace of an int8 projection: row scales, then codes of the activation rows (pitch bytes each).
+struct Int8Layout {
+  size_t scales, codes, total;
+};
+Int8Layout int8_layout(size_t rows, size_t pitch) {
+  Int8Layout L{};
+  L.codes = align_up(rows * sizeof(float));
+  L.total = align_up(L.codes + rows * pitch);
+  return L;
+}
+Int8Layout int8_up_layout(const moe_shape_t& s) { return int8_layout(s.M, s.H); }
+Int8Layout int8_down_layout(const moe_shape_t& s) { return int8_layout(cap_rows(s), s.I); }
+
+moe::Int8GemmArgs int8_plan_args(const moe_plan_t* plan, const moe_shape_t& s, int32_t* err) {
+  moe::Int8GemmArgs a{};
+  a.sorted_ids = plan->sorted_ids;
+  a.counts = plan->expert_counts;
+  a.offsets = plan->expert_offsets;
+  a.err = err;
+  a.M = s.M;
+  a.E = s.E;
+  a.top_k = s.top_k;
+  return a;
+}
+
+// int8 up: x -> codes and scale of every token -> GEMM with the rows gathered by token.
+moe_status_t run_up_int8(const moe_bf16_t* x, const moe_weights_t* w, const moe_plan_t* plan, const moe_shape_t& s,
+                         moe_bf16_t* h, void* ws, int32_t* err, cudaStream_t stream) {
+  const Int8Layout L = int8_up_layout(s);
+  auto* base = static_cast<uint8_t*>(ws);
+  moe::Int8RowsArgs q{};
+  q.src = x;
+  q.ld = s.H;
+  q.rows = s.M;
+  q.cols = s.H;
+  q.codes = reinterpret_cast<int8_t*>(base + L.codes);
+  q.pitch = s.H;
+  q.scales = reinterpret_cast<float*>(base + L.scales);
+  if (moe::launch_quantize_int8(q, stream) != cudaSuccess) return MOE_ERR_CUDA;
+  CUtensorMap mg, mu, mx;
+  const uint64_t wrows = static_cast<uint64_t>(s.E) * s.I;
+  if (!make_map_i8(&mg, w->gate, wrows, s.H, s.H, 128) || !make_map_i8(&mu, w->up, wrows, s.H, s.H, 128) ||
+      !make_map_i8(&mx, q.codes, s.M, s.H, s.H, 1))
+    return MOE_ERR_CUDA;
+  moe::Int8GemmArgs a = int8_plan_args(plan, s, err);
+  a.row_scale = q.scales;
+  a.ch_scale0 = w->gate_gs;
+  a.ch_scale1 = w->up_gs;
+  a.out = h;
+  a.out_ld = s.I;
+  a.rows_per_expert = s.I;
+  a.kdim = s.H;
+  return cuda_status(moe::launch_int8_up(mg, mu, mx, a, choose_nmax(s), stream));
+}
+
+// int8 down: the real plan rows of h -> codes and scales -> GEMM scattered to slots.
+moe_status_t run_down_int8(const moe_bf16_t* h, const moe_weights_t* w, const moe_plan_t* plan, const moe_shape_t& s,
+                           moe_bf16_t* y, void* ws, int32_t* err, cudaStream_t stream) {
+  const Int8Layout L = int8_down_layout(s);
+  auto* base = static_cast<uint8_t*>(ws);
+  moe::Int8RowsArgs q{};
+  q.src = h;
+  q.ld = s.I;
+  q.rows = static_cast<int64_t>(cap_rows(s));
+  q.cols = s.I;
+  q.codes = reinterpret_cast<int8_t*>(base + L.codes);
+  q.pitch = s.I;
+  q.scales = reinterpret_cast<float*>(base + L.scales);
+  q.sorted_ids = plan->sorted_ids;
+  q.ntpp = plan->num_tokens_post_padded;
+  q.nslots = s.M * s.top_k;
+  if (moe::launch_quantize_int8(q, stream) != cudaSuccess) return MOE_ERR_CUDA;
+  CUtensorMap md, mh;
+  if (!make_map_i8(&md, w->down, static_cast<uint64_t>(s.E) * s.H, s.I, s.I, 128) ||
+      !make_map_i8(&mh, q.codes, cap_rows(s), s.I, s.I, 16))
+    return MOE_ERR_CUDA;
+  moe::Int8GemmArgs a = int8_plan_args(plan, s, err);
+  a.row_scale = q.scales;
+  a.ch_scale0 = w->down_gs;
+  a.ch_scale1 = w->down_gs;
+  a.out = y;
+  a.out_ld = s.H;
+  a.rows_per_expert = s.H;
+  a.kdim = s.I;
+  return cuda_status(moe::launch_int8_down(md, mh, a, choose_nmax(s), stream));
+}
+
+// moe_linear_int8's arguments that its workspace size depends on.
+bool linear_int8_shape_ok(int64_t M, int64_t N, int64_t K) {
+  return M >= 1 && N >= 1 && K >= 1 && M <= (1ll << 30) && N <= (1ll << 30) && K <= MOE_INT8_MAX_K &&
+         (M / 32 + 1) * (N / 128 + 1) < (1ll << 31);
+}
+int64_t linear_int8_pitch(int64_t K) { return (K + 15) / 16 * 16; }
+
+// moe_route_logits' options, shape and logits: MOE_OK or the status of the call.
+moe_status_t check_group_route(int32_t M, int32_t E, int32_t top_k, const moe_group_opts_t* o) {
+  if (!o) return MOE_ERR_INVALID_ARG;
+  if (o->scoring != MOE_SCORE_SOFTMAX && o->scoring != MOE_SCORE_SIGMOID) return MOE_ERR_INVALID_ARG;
+  if (o->group_score != MOE_GROUP_MAX && o->group_score != MOE_GROUP_TOP2) return MOE_ERR_INVALID_ARG;
+  if (!(o->routed_scale > 0.0f) || !std::isfinite(o->routed_scale)) return MOE_ERR_INVALID_ARG;
+  if (M < 1 || E < 1 || E > 1024 || top_k < 1 || top_k > 32) return MOE_ERR_UNSUPPORTED;
+  if (o->n_group < 1 || o->n_group > 32 || E % o->n_group != 0) return MOE_ERR_UNSUPPORTED;
+  if (o->topk_group < 1 || o->topk_group > o->n_group) return MOE_ERR_UNSUPPORTED;
+  if (top_k > o->topk_group * (E / o->n_group)) return MOE_ERR_UNSUPPORTED;
+  if (static_cast<long long>(M) * top_k >= (1ll << 31)) return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+moe::RouteGroupOpts group_opts(const moe_group_opts_t& o) {
+  return {o.scoring, o.renormalize != 0 ? 1 : 0, o.n_group, o.topk_group, o.group_score, o.routed_scale};
+}
+
 // Counters of the single-launch layer: grid barrier, work counter, finalize
 // count, one up-tile count per expert, and (up to 64 tokens) one slice count
 // and 8 partial sums of squares per token.
@@ -588,9 +716,11 @@ moe_layer_ws_layout_t layer_layout(const moe_shape_t& s, moe_wdtype_t dt) {
   off = align_up(off + cap * s.I * sizeof(uint16_t));
   L.y = off;
   off = align_up(off + mk * s.H * sizeof(uint16_t));
-  L.act_scratch = off;  // bf16: x gathered into plan order; NVFP4: the two tile-aligned activation copies
+  L.act_scratch = off;  // bf16: x gathered into plan order; NVFP4, int8: the two activation copies
   if (dt == MOE_W_NVFP4)
     off = align_up(off + x_act_layout(s).total + h_act_layout(s).total);
+  else if (dt == MOE_W_INT8)
+    off = align_up(off + int8_up_layout(s).total + int8_down_layout(s).total);
   else
     off = align_up(off + pregather_bytes(s));
   L.total = off;
@@ -608,6 +738,7 @@ moe_status_t check_layer_args(const moe_bf16_t* x, const moe_bf16_t* w_router, c
   if (!aligned16(x) || !aligned16(w_router) || !aligned16(gamma) || !aligned16(out) || !aligned16(w->gate) ||
       !aligned16(w->up) || !aligned16(w->down) || (residual_out && !aligned16(residual_out)))
     return MOE_ERR_INVALID_ARG;
+  if (w->dtype == MOE_W_INT8 && (!w->gate_gs || !w->up_gs || !w->down_gs)) return MOE_ERR_INVALID_ARG;
   if (!(eps >= 0.0f)) return MOE_ERR_INVALID_ARG;
   return MOE_OK;
 }
@@ -652,6 +783,11 @@ moe_status_t run_layer_to_y(const moe_bf16_t* x, const moe_bf16_t* w_router, con
     if ((st = cuda_status(cudaMemsetAsync(h_amax, 0, sizeof(unsigned), cs))) != MOE_OK) return st;
     if ((st = run_up_nvfp4(x, w, &plan, s, h, act, err, cs, h_amax)) != MOE_OK) return st;
     return run_down_nvfp4(h, w, &plan, s, y, act_h, err, cs, true);
+  }
+  if (w->dtype == MOE_W_INT8) {
+    uint8_t* act = base + L.act_scratch;
+    if ((st = run_up_int8(x, w, &plan, s, h, act, err, cs)) != MOE_OK) return st;
+    return run_down_int8(h, w, &plan, s, y, act + int8_up_layout(s).total, err, cs);
   }
   if ((st = run_up(x, w, &plan, s, h, base + L.act_scratch, L.total - L.act_scratch, err, cs)) != MOE_OK) return st;
   return run_down(h, w, &plan, s, y, err, cs);
@@ -709,11 +845,13 @@ size_t moe_route_workspace_size(moe_shape_t s) {
 size_t moe_up_workspace_size(moe_shape_t s, moe_wdtype_t dtype) {
   if (check_shape(s) != MOE_OK) return 0;
   if (dtype == MOE_W_NVFP4) return x_act_layout(s).total;
+  if (dtype == MOE_W_INT8) return int8_up_layout(s).total;
   return (want_pregather(s) || want_persistent(s)) ? pregather_bytes(s) : 0;
 }
 
 size_t moe_down_workspace_size(moe_shape_t s, moe_wdtype_t dtype) {
   if (check_shape(s) != MOE_OK) return 0;
+  if (dtype == MOE_W_INT8) return int8_down_layout(s).total;
   return dtype == MOE_W_NVFP4 ? h_act_layout(s).total : 0;
 }
 
@@ -782,6 +920,11 @@ moe_status_t moe_grouped_up_swiglu(const moe_bf16_t* x, const moe_weights_t* w, 
       return MOE_ERR_WORKSPACE;
     return run_up_nvfp4(x, w, plan, s, h, ws, err_flag, static_cast<cudaStream_t>(stream));
   }
+  if (w->dtype == MOE_W_INT8) {
+    if (!w->gate_gs || !w->up_gs) return MOE_ERR_INVALID_ARG;
+    if (!ws || ws_bytes < moe_up_workspace_size(s, MOE_W_INT8) || !aligned16(ws)) return MOE_ERR_WORKSPACE;
+    return run_up_int8(x, w, plan, s, h, ws, err_flag, static_cast<cudaStream_t>(stream));
+  }
   return run_up(x, w, plan, s, h, ws, ws_bytes, err_flag, static_cast<cudaStream_t>(stream));
 }
 
@@ -818,6 +961,11 @@ moe_status_t moe_grouped_down(const moe_bf16_t* h, const moe_weights_t* w, const
     if (!ws || ws_bytes < moe_down_workspace_size(s, MOE_W_NVFP4) || !aligned16(ws) || !plan->num_tokens_post_padded)
       return MOE_ERR_WORKSPACE;
     return run_down_nvfp4(h, w, plan, s, y, ws, err_flag, static_cast<cudaStream_t>(stream));
+  }
+  if (w->dtype == MOE_W_INT8) {
+    if (!w->down_gs || !plan->num_tokens_post_padded) return MOE_ERR_INVALID_ARG;
+    if (!ws || ws_bytes < moe_down_workspace_size(s, MOE_W_INT8) || !aligned16(ws)) return MOE_ERR_WORKSPACE;
+    return run_down_int8(h, w, plan, s, y, ws, err_flag, static_cast<cudaStream_t>(stream));
   }
   return run_down(h, w, plan, s, y, err_flag, static_cast<cudaStream_t>(stream));
 }
@@ -907,11 +1055,12 @@ moe_status_t moe_tp_layer(const moe_bf16_t* x, const moe_bf16_t* w_router, const
 }
 
 int moe_layer_kernel_count(moe_shape_t s, moe_wdtype_t dtype) {
-  if (check_shape(s) != MOE_OK || (dtype != MOE_W_BF16 && dtype != MOE_W_NVFP4)) return -1;
+  if (check_shape(s) != MOE_OK || (dtype != MOE_W_BF16 && dtype != MOE_W_NVFP4 && dtype != MOE_W_INT8)) return -1;
   // routing: logits + top-k, or screened: digits, integer partial logits, candidates + exact logits + top-k
   const int route = route_screens(s) ? 3 : 2;
   if (dtype == MOE_W_NVFP4)  // routing, align, amax x, quantize x, gather tiles, up (+ amax h), quantize h, down, finalize
     return route + 8;
+  if (dtype == MOE_W_INT8) return route + 6;  // routing, align, quantize x, up, quantize h, down, finalize
   if (want_fused_layer(s, dtype)) return 1;      // the whole layer in one launch
   if (want_self_route(s, dtype)) return route + 3;  // routing, up with the plan, down, finalize
   return route + 4 + (up_pregathers(s) ? 1 : 0);   // routing, align, [gather x], up, down, finalize
@@ -952,6 +1101,92 @@ size_t moe_nvfp4_blob_bytes(moe_shape_t s, int which) {
   int64_t rows, cols;
   blob_dims(s, which, &rows, &cols);
   return static_cast<size_t>(rows) * cols / 2 + static_cast<size_t>(rows) * cols / 16;
+}
+
+moe_status_t moe_route_logits(const void* logits, moe_dtype_t dtype, int64_t ld, const float* bias, int32_t M,
+                              int32_t E, int32_t top_k, const moe_group_opts_t* opts, int32_t* topk_ids,
+                              float* topk_w, moe_stream_t stream) {
+  moe_status_t st = check_group_route(M, E, top_k, opts);
+  if (st != MOE_OK) return st;
+  if (!logits || !topk_ids || !topk_w) return MOE_ERR_INVALID_ARG;
+  if ((dtype != MOE_DT_F32 && dtype != MOE_DT_BF16) || ld < E) return MOE_ERR_INVALID_ARG;
+  return cuda_status(moe::launch_route_group(logits, dtype == MOE_DT_BF16, ld, bias, M, E, top_k, group_opts(*opts),
+                                             topk_ids, topk_w, static_cast<cudaStream_t>(stream)));
+}
+
+moe_status_t moe_route_group(const moe_bf16_t* x, const moe_bf16_t* w_router, const float* bias, moe_shape_t s,
+                             const moe_group_opts_t* opts, int32_t* topk_ids, float* topk_w, void* ws, size_t ws_bytes,
+                             moe_stream_t stream) {
+  moe_status_t st = check_shape(s);
+  if (st != MOE_OK) return st;
+  if ((st = check_group_route(s.M, s.E, s.top_k, opts)) != MOE_OK) return st;
+  if (!x || !w_router || !topk_ids || !topk_w) return MOE_ERR_INVALID_ARG;
+  if (!aligned16(x) || !aligned16(w_router)) return MOE_ERR_INVALID_ARG;
+  if (!ws || ws_bytes < moe_route_workspace_size(s)) return MOE_ERR_WORKSPACE;
+  auto cs = static_cast<cudaStream_t>(stream);
+  auto* logits = static_cast<float*>(ws);
+  if ((st = cuda_status(moe::launch_router_logits(x, w_router, nullptr, s.M, s.H, s.E, logits, cs))) != MOE_OK)
+    return st;
+  return cuda_status(moe::launch_route_group(logits, false, s.E, bias, s.M, s.E, s.top_k, group_opts(*opts), topk_ids,
+                                             topk_w, cs));
+}
+
+moe_status_t moe_quantize_int8(const moe_bf16_t* src, int64_t ld, int64_t rows, int64_t cols, int8_t* codes,
+                               int64_t pitch, float* scales, moe_stream_t stream) {
+  if (rows < 1 || cols < 1 || rows >= (1ll << 31) || cols > MOE_INT8_MAX_K) return MOE_ERR_UNSUPPORTED;
+  if (!src || !codes || !scales || ld < cols || pitch < cols) return MOE_ERR_INVALID_ARG;
+  moe::Int8RowsArgs q{};
+  q.src = src;
+  q.ld = ld;
+  q.rows = rows;
+  q.cols = static_cast<int>(cols);
+  q.codes = codes;
+  q.pitch = pitch;
+  q.scales = scales;
+  return cuda_status(moe::launch_quantize_int8(q, static_cast<cudaStream_t>(stream)));
+}
+
+size_t moe_linear_int8_workspace_size(int64_t M, int64_t N, int64_t K) {
+  return linear_int8_shape_ok(M, N, K) ? int8_layout(M, linear_int8_pitch(K)).total : 0;
+}
+
+moe_status_t moe_linear_int8(const moe_bf16_t* x, int64_t ldx, const int8_t* w, int64_t ldw, const float* w_scale,
+                             int64_t M, int64_t N, int64_t K, void* out, int64_t ldo, moe_dtype_t out_dtype, void* ws,
+                             size_t ws_bytes, int32_t* err_flag, moe_stream_t stream) {
+  if (!linear_int8_shape_ok(M, N, K)) return MOE_ERR_UNSUPPORTED;
+  if (!x || !w || !w_scale || !out) return MOE_ERR_INVALID_ARG;
+  if (out_dtype != MOE_DT_F32 && out_dtype != MOE_DT_BF16) return MOE_ERR_INVALID_ARG;
+  if (ldx < K || ldw < K || ldo < N || ldw % 16 != 0 || !aligned16(w)) return MOE_ERR_INVALID_ARG;
+  if (!ws || ws_bytes < moe_linear_int8_workspace_size(M, N, K) || !aligned16(ws)) return MOE_ERR_WORKSPACE;
+  auto cs = static_cast<cudaStream_t>(stream);
+  const int64_t pitch = linear_int8_pitch(K);
+  const Int8Layout L = int8_layout(M, pitch);
+  auto* base = static_cast<uint8_t*>(ws);
+  moe::Int8RowsArgs q{};
+  q.src = x;
+  q.ld = ldx;
+  q.rows = M;
+  q.cols = static_cast<int>(K);
+  q.codes = reinterpret_cast<int8_t*>(base + L.codes);
+  q.pitch = pitch;
+  q.scales = reinterpret_cast<float*>(base + L.scales);
+  if (moe::launch_quantize_int8(q, cs) != cudaSuccess) return MOE_ERR_CUDA;
+  CUtensorMap mw, mx;
+  if (!make_map_i8(&mw, w, N, K, ldw, 128) || !make_map_i8(&mx, q.codes, M, K, pitch, 16)) return MOE_ERR_CUDA;
+  moe::Int8GemmArgs a{};
+  a.row_scale = q.scales;
+  a.ch_scale0 = w_scale;
+  a.ch_scale1 = w_scale;
+  a.out = out;
+  a.out_ld = ldo;
+  a.out_f32 = out_dtype == MOE_DT_F32 ? 1 : 0;
+  a.err = err_flag;
+  a.M = static_cast<int>(M);
+  a.E = 1;
+  a.top_k = 1;
+  a.rows_per_expert = static_cast<int>(N);
+  a.kdim = static_cast<int>(K);
+  return cuda_status(moe::launch_int8_dense(mw, mx, a, M <= 32 ? 32 : 128, cs));
 }
 
 moe_status_t moe_selftest_wait_timeout(int32_t* err_flag, uint32_t limit_us, moe_stream_t stream) {

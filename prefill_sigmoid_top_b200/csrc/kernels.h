@@ -214,4 +214,52 @@ cudaError_t launch_nvfp4_pair_down(const CUtensorMap& down_codes, const CUtensor
                                    const CUtensorMap& down_sf, const CUtensorMap& h_sf, const Nvfp4GemmArgs& args,
                                    int num_sms, cudaStream_t stream);
 
+// router_group.cu: moe_route_logits.
+struct RouteGroupOpts {
+  int scoring, renormalize, n_group, topk_group, group_score;
+  float routed_scale;
+};
+cudaError_t launch_route_group(const void* logits, bool bf16, int64_t ld, const float* bias, int M, int E, int K,
+                               const RouteGroupOpts& o, int32_t* topk_ids, float* topk_w, cudaStream_t stream);
+
+// int8.cu: rows of bf16 -> 8-bit codes and row scales.
+struct Int8RowsArgs {
+  const uint16_t* src;  // [rows, cols], row stride ld (elements)
+  int64_t ld, rows;
+  int cols;
+  int8_t* codes;        // row stride pitch
+  int64_t pitch;
+  float* scales;        // [rows]
+  // plan rows only (null otherwise): padding rows, and rows from *ntpp on, are skipped
+  const int32_t* sorted_ids;
+  const int32_t* ntpp;
+  int nslots;
+};
+cudaError_t launch_quantize_int8(const Int8RowsArgs& a, cudaStream_t stream);
+
+// int8_gemm.cu: products of 8-bit rows.
+struct Int8GemmArgs {
+  const int32_t* sorted_ids;  // the plan (null for the dense product)
+  const int32_t* counts;
+  const int32_t* offsets;
+  const float* row_scale;     // up: [M] by token; down: [cap] by plan row; dense: [M]
+  const float* ch_scale0;     // [E * rows_per_expert]
+  const float* ch_scale1;     // up: of W_up
+  void* out;                  // up: h [cap, I]; down: y [M*K, H]; dense: [M, out_ld]
+  int64_t out_ld;
+  int out_f32;                // dense: fp32 results instead of bf16
+  int32_t* err;
+  int M, E, top_k;
+  int rows_per_expert;        // up: I; down: H; dense: N
+  int kdim;
+};
+// Tensor maps: weights in 128-row boxes of 128 bytes; up: x codes [M, H] in one-row boxes (gathered by token);
+// down / dense: h codes [cap, I] / x codes [M, K] in 16-row boxes.
+cudaError_t launch_int8_up(const CUtensorMap& w_gate, const CUtensorMap& w_up, const CUtensorMap& x_rows,
+                           const Int8GemmArgs& args, int nmax, cudaStream_t stream);
+cudaError_t launch_int8_down(const CUtensorMap& w_down, const CUtensorMap& h_rows, const Int8GemmArgs& args, int nmax,
+                             cudaStream_t stream);
+cudaError_t launch_int8_dense(const CUtensorMap& w, const CUtensorMap& x_rows, const Int8GemmArgs& args, int nmax,
+                              cudaStream_t stream);
+
 }  // namespace moe

@@ -179,23 +179,6 @@ __global__ void __launch_bounds__(kQThreads) screen_quantize_kernel(const uint16
 }
 
 // ---------------------------------------------------------------------------- 2. integer partial logits
-// Instruction descriptor of kind::i8 with signed 8-bit A and B, int32 accumulator, both K-major:
-// D format (2 = s32) at bits [4,6), A format (1 = signed) at [7,10), B format at [10,13),
-// N >> 3 at [17,23), M >> 4 at [24,29).
-__host__ __device__ constexpr uint32_t umma_idesc_s8(uint32_t M, uint32_t N) {
-  return (2u << 4) | (1u << 7) | (1u << 10) | ((N >> 3) << 17) | ((M >> 4) << 24);
-}
-
-__device__ __forceinline__ void umma_s8_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
-                                           uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::i8 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-
 struct ScreenGemmArgs {
   double* partial;  // [slices][M][E]
   int32_t* err;

@@ -1,0 +1,390 @@
+"""The int8 (W8A8) products against plain 64-bit implementations.
+
+The codes are those of exact arithmetic (compared bit for bit) and the integer sums are exact, so what is left is
+the fp32 scaling and the last rounding.  Bars, relative to the exact value v = sx sw sum:
+  linear, down: sx (a / 127 rounded), sx sw, the sum as fp32 and the product are one rounding of at most 2^-24 each:
+      5 * 2^-24 covers them and their products; a bf16 result adds its half step 2^-8.
+  up: h = g sigma(g) u.  g and u carry 5 * 2^-24 each; silu's relative condition is at most 1 + |g|; the hardware
+      exponential is off by 2 ulp plus |g| 2^-23 (its scaled argument), the fast division by 2 ulp:
+      (16 + 16 |g|) 2^-24 covers all of it, plus the half step of bf16.
+"""
+import numpy as np
+import pytest
+import torch
+
+import prefill_sigmoid_top_b200 as moe
+from prefill_sigmoid_top_b200 import inputs
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+STEP = {torch.bfloat16: 2.0 ** -8, torch.float32: 0.0}
+
+
+def gen(seed):
+    return torch.Generator().manual_seed(seed)
+
+
+def quantize_ref(v):
+    """Codes and scales of the rows of v (fp64, bf16 values): 127 v / a is exact up to one rounding of fp64, and a
+    tie is representable, so rint decides as exact arithmetic does."""
+    a = np.abs(v).max(axis=-1, keepdims=True)
+    q = np.divide(127.0 * v, a, out=np.zeros_like(v), where=a > 0)
+    return np.rint(q), a[..., 0] / 127.0
+
+
+def codes_of(rows, cols, seed, pitch=None):
+    g = gen(seed)
+    c = torch.randint(-127, 128, (rows, pitch or cols), generator=g, dtype=torch.int64).to(torch.int8)
+    return c[:, :cols], (torch.rand(rows, generator=g) + 0.5) * 0.01
+
+
+def within(got, want, rel):
+    got = got.detach().cpu().double().numpy()
+    bad = ~(np.abs(got - want) <= rel * np.abs(want) + 1e-37)
+    assert not bad.any(), (np.argwhere(bad)[:4], got[bad][:4], want[bad][:4])
+
+
+# ------------------------------------------------------------------ codes
+@pytest.mark.parametrize("rows,cols", [(1, 1), (3, 5), (7, 127), (4, 128), (5, 1777), (2, 7168), (9, 256), (1, 131072)])
+def test_quantize_codes_exact(rows, cols):
+    w = torch.randn(rows, cols, generator=gen(cols)).to(torch.bfloat16)
+    codes, scales = moe.quantize_int8(w.to(DEV))
+    q, s = quantize_ref(w.double().numpy())
+    assert np.array_equal(codes.cpu().numpy(), q)
+    assert np.array_equal(scales.cpu().numpy(), s.astype(np.float32))
+    assert codes.stride(0) % 16 == 0
+
+
+def test_quantize_every_ratio_and_tie():
+    """Every pair of bf16 significands at several exponent gaps: all quotients 127 v / a there are, ties included."""
+    m = torch.arange(128, 256).double()
+    rows = []
+    for a in m:
+        for gap in (0, 1, 2, 5, 7, 8):
+            v = m * 2.0 ** -gap
+            rows.append(torch.cat([a[None], torch.where(v <= a, v, -v / 2)]))
+    w = torch.stack(rows)
+    for scale in (1.0, 2.0 ** -130, 2.0 ** -60, 2.0 ** 120):
+        b = (w * scale).to(torch.bfloat16)
+        q, s = quantize_ref(b.double().numpy())
+        codes, scales = moe.quantize_int8(b.to(DEV))
+        assert np.array_equal(codes.cpu().numpy(), q)
+        assert np.array_equal(scales.cpu().numpy(), s.astype(np.float32))
+
+
+def test_quantize_special_rows():
+    w = torch.randn(6, 40, generator=gen(1)).to(torch.bfloat16)
+    w[0] = 0
+    w[1, 7] = float("inf")
+    w[2, 9] = float("nan")
+    w[3, 0] = 3.3e38
+    w[4] = 0
+    w[4, 39] = -2.0 ** -133
+    codes, scales = moe.quantize_int8(w.to(DEV))
+    codes, scales = codes.cpu(), scales.cpu()
+    assert scales[0] == 0 and (codes[0] == 0).all()
+    assert scales[1:3].isnan().all() and (codes[1:3] == 0).all()
+    assert codes[3, 0] == 127 and scales[3].isfinite() and (codes[3, 1:] == 0).all()
+    assert codes[4, 39] == -127
+    q, _ = quantize_ref(w[5:].double().numpy())
+    assert np.array_equal(codes[5:].numpy(), q)
+
+
+# ------------------------------------------------------------------ dense
+def linear_case(M, N, K, out=torch.bfloat16, pad=0, off=0, seed=0):
+    x = torch.randn(M, K + pad + off, generator=gen(seed)).to(torch.bfloat16)
+    codes, scales = codes_of(N, K, seed + 1, (K + 15) // 16 * 16)
+    xd = x.to(DEV)[:, off:off + K]
+    cd = torch.empty(N, (K + 15) // 16 * 16, dtype=torch.int8, device=DEV).fill_(99)[:, :K]
+    cd.copy_(codes)
+    y = moe.linear_int8(xd, cd, scales.to(DEV), out_dtype=out)
+    xq, sx = quantize_ref(x[:, off:off + K].double().numpy())
+    want = (xq @ codes.double().numpy().T) * sx[:, None] * scales.double().numpy()
+    assert y.dtype == out and tuple(y.shape) == (M, N)
+    within(y, want, 5 * 2.0 ** -24 + STEP[out])
+
+
+@pytest.mark.parametrize("out", [torch.bfloat16, torch.float32], ids=["bf16", "fp32"])
+@pytest.mark.parametrize("M,N,K", [
+    (1, 1, 1), (1, 128, 128), (1, 2048, 7168), (2, 7168, 2048), (3, 131, 77), (16, 257, 129), (17, 640, 1000),
+    (31, 129, 4097), (32, 512, 512), (33, 513, 511), (100, 300, 260), (128, 128, 128), (129, 1025, 2047),
+    (255, 96, 33), (256, 1024, 640), (300, 1, 50), (513, 2049, 1777), (1000, 33, 7168), (1, 5, 131072),
+])
+def test_linear(M, N, K, out):
+    linear_case(M, N, K, out, seed=M + N + K)
+
+
+@pytest.mark.parametrize("M", [1, 5, 40, 300])
+@pytest.mark.parametrize("pad,off", [(3, 0), (1, 1), (8, 8), (0, 2)])
+def test_linear_strided_rows(M, pad, off):
+    linear_case(M, 200, 264, torch.float32, pad, off, seed=pad + off)
+
+
+def test_linear_large_sums_are_exact():
+    """K = 131072 with all codes at 127: the largest sum that is accepted, 131072 * 127^2 < 2^31."""
+    K = 131072
+    x = torch.ones(2, K, dtype=torch.bfloat16, device=DEV)
+    x[1, ::2] = -1
+    codes = torch.full((3, K), 127, dtype=torch.int8, device=DEV)
+    codes[2] = -127
+    y = moe.linear_int8(x, codes, torch.ones(3, device=DEV), out_dtype=torch.float32)
+    want = np.array([[K * 127.0, K * 127.0, -K * 127.0], [0, 0, 0]])
+    within(y, want, 5 * 2.0 ** -24)
+
+
+def test_linear_special_values():
+    x = torch.randn(5, 256, generator=gen(2)).to(torch.bfloat16)
+    x[1] = 0
+    x[2, 3] = float("inf")
+    x[3, 255] = float("nan")
+    codes, scales = codes_of(70, 256, 3)
+    y = moe.linear_int8(x.to(DEV), codes.to(DEV), scales.to(DEV), out_dtype=torch.float32)
+    assert (y[1] == 0).all() and y[2:4].isnan().all() and y[[0, 1, 4]].isfinite().all()
+
+
+def test_linear_writes_its_rows_only():
+    for M in (3, 40, 300):
+        buf = torch.full((M + 2, 150), -5.0, device=DEV)
+        codes, scales = codes_of(130, 64, 4)
+        x = torch.randn(M, 64, generator=gen(5)).to(torch.bfloat16).to(DEV)
+        out = buf[1:M + 1, 10:140]
+        moe.linear_int8(x, codes.to(DEV), scales.to(DEV), out=out)
+        inner = moe.linear_int8(x, codes.to(DEV), scales.to(DEV), out_dtype=torch.float32)
+        assert torch.equal(out, inner)
+        buf[1:M + 1, 10:140] = -5.0
+        assert (buf == -5.0).all()
+
+
+@pytest.mark.parametrize("M", [1, 24, 200, 1500])
+def test_linear_same_bits_again_on_a_stream_and_replayed(M):
+    codes, scales = (t.to(DEV) for t in codes_of(1500, 1024, 6))
+    x = torch.randn(M, 1024, generator=gen(7)).to(torch.bfloat16).to(DEV)
+    want = moe.linear_int8(x, codes, scales)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        a = moe.linear_int8(x, codes, scales)
+    b = moe.linear_int8(x, codes, scales)  # both at once
+    side.synchronize()
+    assert torch.equal(a, want) and torch.equal(b, want)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y = moe.linear_int8(x, codes, scales)
+    x2 = torch.randn(M, 1024, generator=gen(8)).to(torch.bfloat16).to(DEV)
+    want2 = moe.linear_int8(x2, codes, scales)
+    x.copy_(x2)
+    for _ in range(2):
+        graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(y, want2)
+
+
+# ------------------------------------------------------------------ experts
+def random_ids(M, E, K, seed, skew=0.0):
+    z = torch.randn(M, E, generator=gen(seed)) - skew * torch.arange(1, E + 1).log()
+    return z.topk(K, dim=1).indices.int()
+
+
+def experts_case(shape, seed=0, skew=0.0, ids=None):
+    M, H, I, E, K = shape.M, shape.H, shape.I, shape.E, shape.top_k
+    ids = random_ids(M, E, K, seed, skew) if ids is None else ids
+    plan = moe.align_block_size(ids.to(DEV), E, shape.block_size)
+    x = torch.randn(M, H, generator=gen(seed + 1)).to(torch.bfloat16)
+    mats = {}
+    for i, (n, r, c) in enumerate((("gate", I, H), ("up", I, H), ("down", H, I))):
+        codes, scales = codes_of(E * r, c, seed + 2 + i)
+        mats[n], mats[n + "_scales"] = codes.view(E, r, c), scales.view(E, r) * (1.0 / c ** 0.5)
+    iw = moe.Int8Weights(**{k: v.to(DEV) for k, v in mats.items()})
+    return x, ids, plan, mats, iw
+
+
+def check_up(shape, x, plan, mats, iw):
+    err = torch.zeros(1, dtype=torch.int32, device=DEV)
+    cap = moe.align_capacity(shape)
+    h = torch.full((cap, shape.I), -3.0, dtype=torch.bfloat16, device=DEV)
+    moe.grouped_up_swiglu_int8(x.to(DEV), iw, plan, shape, h=h, err_flag=err)
+    assert moe.get_device_error(err) == 0
+    xq, sx = quantize_ref(x.double().numpy())
+    counts, offs, sid = (plan[k].cpu().numpy() for k in ("expert_counts", "expert_offsets", "sorted_ids"))
+    real = np.zeros(cap, bool)
+    hc = h.cpu()
+    for e in range(shape.E):
+        rows = np.arange(offs[e], offs[e] + counts[e])
+        if not len(rows):
+            continue
+        real[rows] = True
+        t = sid[rows] // shape.top_k
+        g, u = ((xq[t] @ mats[n][e].double().numpy().T) * sx[t][:, None] * mats[n + "_scales"][e].double().numpy()
+                for n in ("gate", "up"))
+        with np.errstate(over="ignore"):
+            want = g / (1.0 + np.exp(-g)) * u
+        within(hc[rows], want, 2.0 ** -8 + (16 + 16 * np.abs(g)) * 2.0 ** -24)
+    assert (hc[~real] == -3.0).all()  # padding rows and rows behind the last block are left as they were
+    return h
+
+
+def check_down(shape, h, plan, mats, iw):
+    err = torch.zeros(1, dtype=torch.int32, device=DEV)
+    y = torch.full((shape.M * shape.top_k, shape.H), -3.0, dtype=torch.bfloat16, device=DEV)
+    moe.grouped_down_int8(h, iw, plan, shape, y=y, err_flag=err)
+    assert moe.get_device_error(err) == 0
+    counts, offs, sid = (plan[k].cpu().numpy() for k in ("expert_counts", "expert_offsets", "sorted_ids"))
+    hc, yc = h.double().cpu().numpy(), y.cpu()
+    seen = 0
+    for e in range(shape.E):
+        rows = np.arange(offs[e], offs[e] + counts[e])
+        if not len(rows):
+            continue
+        hq, sh = quantize_ref(hc[rows])
+        want = (hq @ mats["down"][e].double().numpy().T) * sh[:, None] * mats["down_scales"][e].double().numpy()
+        within(yc[sid[rows]], want, 2.0 ** -8 + 5 * 2.0 ** -24)
+        seen += len(rows)
+    assert seen == shape.M * shape.top_k
+
+
+EXPERT_SHAPES = [  # M, H, I, E, K, B, skew
+    (1, 256, 128, 1, 1, 16, 0), (1, 512, 256, 8, 2, 16, 0), (7, 256, 384, 8, 3, 16, 0), (16, 1024, 128, 4, 4, 32, 0),
+    (40, 512, 256, 16, 2, 16, 1.0), (33, 256, 128, 1, 1, 64, 0), (130, 512, 384, 4, 2, 128, 0.5),
+    (200, 768, 640, 3, 2, 256, 1.0), (513, 512, 512, 4, 2, 64, 1.0), (260, 256, 256, 1, 1, 16, 0),
+    (96, 1280, 128, 64, 8, 16, 0.5), (700, 1024, 256, 2, 1, 16, 2.0),
+]
+
+
+@pytest.mark.parametrize("M,H,I,E,K,B,skew", EXPERT_SHAPES)
+def test_experts(M, H, I, E, K, B, skew):
+    shape = moe.Shape(M, H, I, E, K, B)
+    x, ids, plan, mats, iw = experts_case(shape, seed=M + I, skew=skew)
+    check_up(shape, x, plan, mats, iw)
+    h = torch.randn(moe.align_capacity(shape), I, generator=gen(M)).to(torch.bfloat16).to(DEV)
+    pad = torch.ones(h.shape[0], dtype=torch.bool)
+    off, cnt = plan["expert_offsets"].cpu(), plan["expert_counts"].cpu()
+    for e in range(E):
+        pad[off[e]:off[e] + cnt[e]] = False
+    h[pad.to(DEV)] = float("nan")  # what padding rows hold reaches no result
+    check_down(shape, h, plan, mats, iw)
+
+
+@pytest.mark.parametrize("nmax", ["32", "128"])
+def test_experts_token_tile_widths(nmax, monkeypatch):
+    monkeypatch.setenv("MOE_GEMM_NMAX", nmax)
+    shape = moe.Shape(150, 512, 384, 5, 2, 16)
+    x, ids, plan, mats, iw = experts_case(shape, seed=3, skew=1.0)
+    check_up(shape, x, plan, mats, iw)
+    check_down(shape, torch.randn(moe.align_capacity(shape), 384).to(torch.bfloat16).to(DEV), plan, mats, iw)
+
+
+def test_experts_without_tokens_and_all_tokens_on_one():
+    for ids in (torch.full((70, 1), 3, dtype=torch.int32), torch.tensor([[0], [9]], dtype=torch.int32)):
+        shape = moe.Shape(ids.shape[0], 256, 128, 10, 1, 16)
+        x, ids, plan, mats, iw = experts_case(shape, seed=4, ids=ids)
+        check_up(shape, x, plan, mats, iw)
+        check_down(shape, torch.randn(moe.align_capacity(shape), 128).to(torch.bfloat16).to(DEV), plan, mats, iw)
+
+
+def test_experts_report_a_plan_with_bad_slots():
+    """A slot id outside the plan's range is reported in the error word; the other rows keep their values."""
+    for M in (8, 300):
+        shape = moe.Shape(M, 256, 128, 4, 2, 16)
+        x, ids, plan, mats, iw = experts_case(shape, seed=5)
+        good = moe.grouped_up_swiglu_int8(x.to(DEV), iw, plan, shape)
+        first = int(plan["expert_offsets"][:-1][plan["expert_counts"] > 0][0])
+        bad = dict(plan, sorted_ids=plan["sorted_ids"].clone())
+        for v in (-1, shape.M * shape.top_k + 5, 2 ** 31 - 1):
+            bad["sorted_ids"][first] = v
+            err = torch.zeros(1, dtype=torch.int32, device=DEV)
+            h = torch.zeros_like(good)
+            moe.grouped_up_swiglu_int8(x.to(DEV), iw, bad, shape, h=h, err_flag=err)
+            assert moe.get_device_error(err) == 4
+            assert torch.equal(h[first + 1], good[first + 1]) or int(plan["expert_counts"].max()) == 1
+            err.zero_()
+            moe.grouped_down_int8(good, iw, bad, shape, err_flag=err)
+            assert moe.get_device_error(err) == 4
+
+
+# ------------------------------------------------------------------ together
+def layer_inputs(M, seed):
+    cfg = inputs.WORKLOADS[0].with_(M=M, H=512, I=256, E=16, K=4, B=16, bias="normal", seed=seed)
+    d = inputs.make_inputs(cfg, "cpu")
+    return cfg, d, {k: v.to(DEV) for k, v in d.items()}
+
+
+@pytest.mark.parametrize("M", [1, 8, 130, 600])
+def test_layer_is_its_steps(M):
+    cfg, _, d = layer_inputs(M, 21)
+    iw = moe.int8_weights(d["w_gate"], d["w_up"], d["w_down"])
+    shape = moe.Shape(M, cfg.H, cfg.I, cfg.E, cfg.K, cfg.B)
+    ws = torch.empty(moe.layer_workspace_size(shape, moe.MOE_W_INT8), dtype=torch.uint8, device=DEV)
+    ids = torch.empty(M, cfg.K, dtype=torch.int32, device=DEV)
+    out = moe.layer_int8(d["x"], d["w_router"], d["bias"], iw, d["gamma"], cfg.eps, cfg.K, cfg.B, ws=ws, topk_ids=ids)
+    assert moe.get_device_error(ws) == 0
+    ids2, w = moe.route(d["x"], d["w_router"], d["bias"], cfg.K)
+    plan = moe.align_block_size(ids2, cfg.E, cfg.B)
+    h = moe.grouped_up_swiglu_int8(d["x"], iw, plan, shape)
+    y = moe.grouped_down_int8(h, iw, plan, shape)
+    want = moe.finalize_rmsnorm(d["x"], y.view(M, cfg.K, cfg.H), w, d["gamma"], cfg.eps)
+    assert torch.equal(ids, ids2) and torch.equal(out, want)
+
+
+@pytest.mark.parametrize("M", [1, 37, 300])
+def test_group_routed_layer_with_a_shared_expert(M):
+    """As a user runs them together: group-limited routing, the plan, int8 experts, finalize, and a dense int8
+    projection beside them, against a 64-bit layer that takes the stored codes and the same intermediate roundings."""
+    cfg, c, d = layer_inputs(M, 22)
+    iw = moe.int8_weights(d["w_gate"], d["w_up"], d["w_down"])
+    shape = moe.Shape(M, cfg.H, cfg.I, cfg.E, cfg.K, cfg.B)
+    ids, w = moe.route_group(d["x"], d["w_router"], d["bias"], cfg.K, 4, 2, routed_scale=2.5)
+    plan = moe.align_block_size(ids, cfg.E, cfg.B)
+    h = moe.grouped_up_swiglu_int8(d["x"], iw, plan, shape)
+    y = moe.grouped_down_int8(h, iw, plan, shape)
+    out, res = moe.finalize_rmsnorm(d["x"], y.view(M, cfg.K, cfg.H), w, d["gamma"], cfg.eps, want_residual=True)
+    sc, ss = moe.quantize_int8(d["w_gate"][0])
+    shared = moe.linear_int8(d["x"], sc, ss)
+    # 64 bits
+    mats = {n: getattr(iw, n).cpu().double().numpy() * getattr(iw, n + "_scales").cpu().double().numpy()[..., None]
+            for n in ("gate", "up", "down")}
+    xq, sx = quantize_ref(c["x"].double().numpy())
+    xv = xq * sx[:, None]
+    s = c["x"].double().numpy().copy()
+    for t in range(M):
+        for k in range(cfg.K):
+            e = int(ids[t, k])
+            g, u = mats["gate"][e] @ xv[t], mats["up"][e] @ xv[t]
+            hv = torch.from_numpy(g / (1 + np.exp(-g)) * u).to(torch.bfloat16).double().numpy()
+            hq, sh = quantize_ref(hv[None])
+            yv = torch.from_numpy(mats["down"][e] @ (hq[0] * sh[0])).to(torch.bfloat16).double().numpy()
+            s[t] += float(w[t, k]) * yv
+    want = s / np.sqrt((s * s).mean(1, keepdims=True) + cfg.eps) * c["gamma"].double().numpy()
+    # a bf16 rounding of h or y that falls the other way (fp32 against fp64 before it) moves a value by a step of
+    # its own; the framework's bar for layer outputs covers it: 2e-2 of the RMS
+    assert np.abs(out.cpu().double().numpy() - want).max() <= 2e-2 * np.sqrt((want * want).mean())
+    assert np.abs(res.cpu().double().numpy() - s).max() <= 2e-2 * np.sqrt((s * s).mean())
+    want = (xq @ sc.cpu().double().numpy().T) * sx[:, None] * ss.cpu().double().numpy()
+    within(shared, want, 2.0 ** -8 + 5 * 2.0 ** -24)
+
+
+def test_layer_against_bf16_layer():
+    """8 bits instead of bf16: the layer's output moves by the quantisation error only (two roundings of at most
+    half of 1/127 of a row's largest value in each product: a few percent of the RMS)."""
+    cfg, _, d = layer_inputs(64, 23)
+    iw = moe.int8_weights(d["w_gate"], d["w_up"], d["w_down"])
+    a = moe.layer_int8(d["x"], d["w_router"], d["bias"], iw, d["gamma"], cfg.eps, cfg.K, cfg.B).double()
+    b = moe.layer(d["x"], d["w_router"], d["bias"], d["w_gate"], d["w_up"], d["w_down"], d["gamma"], cfg.eps, cfg.K,
+                  cfg.B).double()
+    assert float((a - b).norm() / b.norm()) < 0.05
+
+
+def test_layer_captured_and_replayed():
+    cfg, _, d = layer_inputs(40, 24)
+    iw = moe.int8_weights(d["w_gate"], d["w_up"], d["w_down"])
+    run = lambda: moe.layer_int8(d["x"], d["w_router"], d["bias"], iw, d["gamma"], cfg.eps, cfg.K, cfg.B)  # noqa: E731
+    run()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = run()
+    x2 = torch.randn(40, cfg.H, generator=gen(25)).to(torch.bfloat16)
+    d["x"].copy_(x2)
+    want = run()
+    for _ in range(2):
+        graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, want)

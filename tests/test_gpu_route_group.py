@@ -1,0 +1,194 @@
+"""Routing from logits with expert groups against a plain fp64 implementation.
+
+Bars: ids equal (keys are defined in fp64, so two experts change places only where their keys differ in the last
+bits of fp64; no test puts different logits that near); weights within 2^-20 relative: the scores may be summed in
+fp32 (a softmax denominator of E <= 1024 terms in E/32 + 5 additions per partial sum, each 2^-24, and a few ulp of
+the exponential), then one rounding to fp32.
+"""
+import numpy as np
+import pytest
+import torch
+
+import oracle
+import prefill_sigmoid_top_b200 as moe
+from prefill_sigmoid_top_b200 import inputs
+from tests._util import bf16_bits
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+RTOL = 2.0 ** -20
+
+
+def reference(z, bias, K, G, TG, group_score, scoring, renorm, scale):
+    z = np.where(np.isnan(z), -np.inf, z.astype(np.float64))
+    M, E = z.shape
+    gs = E // G
+    ids, w = np.zeros((M, K), np.int32), np.zeros((M, K))
+    for t in range(M):
+        with np.errstate(over="ignore", invalid="ignore"):
+            if scoring == moe.SCORE_SIGMOID:
+                p = 1.0 / (1.0 + np.exp(-z[t]))
+            else:
+                top = z[t].max()
+                ex = (z[t] == np.inf) * 1.0 if top == np.inf else np.zeros(E) if top == -np.inf else np.exp(z[t] - top)
+                p = ex / ex.sum() if ex.sum() > 0 else ex
+            key = p + (0.0 if bias is None else bias.astype(np.float64))
+            key = np.where(np.isnan(key), -np.inf, key)
+            gr = np.sort(key.reshape(G, gs), axis=1)
+            s = gr[:, -1] if group_score == moe.GROUP_MAX or gs == 1 else gr[:, -1] + gr[:, -2]
+            s = np.where(np.isnan(s), -np.inf, s)
+        keep = np.argsort(-s, kind="stable")[:TG]
+        cand = [e for e in range(E) if e // gs in set(keep.tolist())]
+        sel = sorted(cand, key=lambda e: (-key[e], e))[:K]
+        ps = p[sel]
+        if renorm:
+            ps = ps / ps.sum() if ps.sum() > 0 else ps * 0
+        ids[t], w[t] = sel, ps * scale
+    return ids, w
+
+
+def check(z, bias, K, G=1, TG=1, group_score=moe.GROUP_TOP2, scoring=moe.SCORE_SIGMOID, renorm=True, scale=1.0):
+    """z: a CPU or CUDA tensor, fp32 or bf16, possibly strided."""
+    zd = z.to(DEV) if not z.is_cuda else z
+    bd = None if bias is None else bias.to(DEV)
+    ids, w = moe.route_logits(zd, bd, K, G, TG, group_score, scoring, renorm, scale)
+    ids_r, w_r = reference(zd.float().cpu().numpy(), None if bias is None else bias.numpy(), K, G, TG, group_score,
+                           scoring, renorm, scale)
+    assert np.array_equal(ids.cpu().numpy(), ids_r)
+    w = w.cpu().numpy().astype(np.float64)
+    assert (np.abs(w - w_r) <= RTOL * np.abs(w_r) + 2.0 ** -149).all()
+    return ids, w
+
+
+def rand(M, E, seed, dtype=torch.float32, spread=1.5):
+    g = torch.Generator().manual_seed(seed)
+    return (torch.randn(M, E, generator=g) * spread).to(dtype), 0.05 * torch.randn(E, generator=g)
+
+
+SHAPES = [  # M, groups, group size, groups kept, K
+    (1, 8, 32, 4, 8), (37, 8, 32, 4, 8), (5, 1, 8, 1, 2), (9, 4, 64, 1, 16), (3, 16, 64, 16, 32), (17, 5, 7, 2, 6),
+    (4, 32, 1, 32, 4), (6, 32, 32, 3, 32), (130, 2, 80, 1, 12), (7, 1, 1, 1, 1), (11, 3, 1, 2, 2), (2, 31, 33, 30, 32),
+]
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["fp32", "bf16"])
+@pytest.mark.parametrize("M,G,gs,TG,K", SHAPES)
+def test_shapes(M, G, gs, TG, K, dtype):
+    z, b = rand(M, G * gs, M + gs, dtype)
+    check(z, b, K, G, TG)
+    check(z, None, K, G, TG, moe.GROUP_MAX, moe.SCORE_SOFTMAX, False, 2.5)
+
+
+@pytest.mark.parametrize("scoring", [moe.SCORE_SIGMOID, moe.SCORE_SOFTMAX])
+@pytest.mark.parametrize("group_score", [moe.GROUP_MAX, moe.GROUP_TOP2])
+@pytest.mark.parametrize("renorm", [True, False])
+@pytest.mark.parametrize("with_bias", [True, False])
+def test_variants(scoring, group_score, renorm, with_bias):
+    z, b = rand(65, 256, 3)
+    check(z, b if with_bias else None, 8, 8, 4, group_score, scoring, renorm, 2.5)
+
+
+def test_no_groups_is_a_flat_top_k():
+    z, b = rand(40, 256, 4)
+    check(z, b, 16)
+
+
+def test_equal_keys_take_the_lower_id():
+    z = torch.zeros(3, 64)
+    ids, _ = check(z, None, 6, 8, 2)
+    assert ids[0].tolist() == [0, 1, 2, 3, 4, 5]
+    # bf16 logits of few values: ties between experts and between groups everywhere
+    g = torch.Generator().manual_seed(5)
+    z = torch.randint(-2, 3, (200, 128), generator=g).to(torch.bfloat16)
+    check(z, None, 8, 8, 3)
+    check(z, torch.randint(0, 2, (128,), generator=g) * 0.25, 8, 8, 3, moe.GROUP_MAX)
+
+
+def test_keys_that_fp32_cannot_tell_apart():
+    """Scores and biases chosen so that the keys differ by less than one step of fp32, in both directions."""
+    g = torch.Generator().manual_seed(6)
+    E = 64
+    z = 0.5 + torch.arange(E).float()[torch.randperm(E, generator=g)] * 2.0 ** -24
+    z = torch.stack([z, z.flip(0)])
+    check(z, None, 16, 4, 2)
+    # sigmoid(z) + b with b cancelling all but about 2^-26 of the difference of the scores
+    z2 = torch.randn(2, E, generator=g)
+    p = 1.0 / (1.0 + torch.exp(-z2[:1].double()))
+    check(z2[:1], (0.75 - p[0]).float(), 16, 4, 2)
+
+
+@pytest.mark.parametrize("scoring", [moe.SCORE_SIGMOID, moe.SCORE_SOFTMAX])
+def test_infinities_and_nan(scoring):
+    inf, nan = float("inf"), float("nan")
+    z, b = rand(8, 64, 7)
+    z[0, 3] = inf
+    z[1, 5] = z[1, 40] = inf
+    z[2, :] = -inf
+    z[3, ::2] = nan
+    z[4, :] = nan
+    z[5, 8:16] = -inf
+    z[6, 1] = 3e38
+    z[7, 2] = -3e38
+    for bias in (None, b):
+        for renorm in (True, False):
+            check(z, bias, 8, 8, 3, moe.GROUP_TOP2, scoring, renorm)
+    bad = b.clone()
+    bad[:50] = -inf                      # only 14 experts may be chosen; the rest of K = 20 by id
+    check(z, bad, 20, 8, 4, moe.GROUP_TOP2, scoring)
+    bad[51], bad[60], bad[61] = nan, inf, inf
+    check(z, bad, 10, 4, 2, moe.GROUP_TOP2, scoring)
+
+
+def test_far_logits():
+    z = torch.tensor([[-100.0, -101.0, -102.0, -103.0] * 4, [100.0, 90.0, 80.0, 70.0] * 4, [-800.0] * 16])
+    check(z, None, 4, 4, 2)
+    check(z, None, 4, 4, 2, scoring=moe.SCORE_SOFTMAX)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("off,pad", [(0, 3), (1, 7), (3, 1), (4, 4)])
+def test_strided_and_unaligned_rows(dtype, off, pad):
+    z, b = rand(21, 256 + off + pad, 8, dtype)
+    check(z.to(DEV)[:, off:off + 256], b[:256], 8, 8, 4)
+
+
+def test_output_buffers_and_rows_beyond_are_kept():
+    z, b = rand(6, 32, 9)
+    ids = torch.full((8, 4), -7, dtype=torch.int32, device=DEV)
+    w = torch.full((8, 4), -7.0, device=DEV)
+    r = moe.route_logits(z.to(DEV), b.to(DEV), 4, 4, 2, topk_ids=ids[:6], topk_w=w[:6])
+    assert r[0].data_ptr() == ids.data_ptr() and r[1].data_ptr() == w.data_ptr()
+    assert (ids[6:] == -7).all() and (w[6:] == -7).all() and (ids[:6] >= 0).all()
+
+
+@pytest.mark.parametrize("M", [1, 40, 300])
+def test_route_group_from_x(M):
+    """From x and w_router: the canonical logits of route (the oracle's) without a bias, then route_logits."""
+    cfg = inputs.WORKLOADS[0].with_(M=M, H=512, E=64, K=6, bias="normal", seed=31)
+    w_r, b, _, x = inputs.router_inputs(cfg)
+    ids, w = moe.route_group(x.to(DEV), w_r.to(DEV), b.to(DEV), 6, 8, 3)
+    z = oracle.router_logits(bf16_bits(x), bf16_bits(w_r), np.zeros(64, np.float32))
+    ids_r, w_r_ = reference(z, b.numpy(), 6, 8, 3, moe.GROUP_TOP2, moe.SCORE_SIGMOID, True, 1.0)
+    assert np.array_equal(ids.cpu().numpy(), ids_r)
+    assert (np.abs(w.cpu().numpy() - w_r_) <= RTOL * w_r_).all()
+
+
+def test_captured_replayed_and_on_another_stream():
+    z, b = rand(33, 256, 10)
+    zd, bd = z.to(DEV), b.to(DEV)
+    want = moe.route_logits(zd, bd, 8, 8, 4)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        got = moe.route_logits(zd, bd, 8, 8, 4)
+    side.synchronize()
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = moe.route_logits(zd, bd, 8, 8, 4)
+    z2, _ = rand(33, 256, 11)
+    zd.copy_(z2)
+    graph.replay()
+    torch.cuda.synchronize()
+    ids_r, _ = reference(z2.numpy(), b.numpy(), 8, 8, 4, moe.GROUP_TOP2, moe.SCORE_SIGMOID, True, 1.0)
+    assert np.array_equal(out[0].cpu().numpy(), ids_r)
