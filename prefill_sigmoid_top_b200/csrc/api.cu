@@ -594,6 +594,10 @@ moe::Int8GemmArgs int8_plan_args(const moe_plan_t* plan, const moe_shape_t& s, i
   return a;
 }
 
+// Token-tile width of the int8 projections on 2-SM pairs, or 0 for the one-tile-per-CTA kernels (decode shapes).
+// MOE_GEMM_PAIR overrides as for bf16.
+int int8_pair_nmax(const moe_shape_t& s) { return want_persistent(s) ? pair_nmax(s) : 0; }
+
 // int8 up: x -> codes and scale of every token -> GEMM with the rows gathered by token.
 moe_status_t run_up_int8(const moe_bf16_t* x, const moe_weights_t* w, const moe_plan_t* plan, const moe_shape_t& s,
                          moe_bf16_t* h, void* ws, int32_t* err, cudaStream_t stream) {
@@ -621,6 +625,8 @@ moe_status_t run_up_int8(const moe_bf16_t* x, const moe_weights_t* w, const moe_
   a.out_ld = s.I;
   a.rows_per_expert = s.I;
   a.kdim = s.H;
+  if (const int n = int8_pair_nmax(s))
+    return cuda_status(moe::launch_int8_pair_up(mg, mu, mx, a, n, true, num_sms(), stream));
   return cuda_status(moe::launch_int8_up(mg, mu, mx, a, choose_nmax(s), stream));
 }
 
@@ -641,9 +647,10 @@ moe_status_t run_down_int8(const moe_bf16_t* h, const moe_weights_t* w, const mo
   q.ntpp = plan->num_tokens_post_padded;
   q.nslots = s.M * s.top_k;
   if (moe::launch_quantize_int8(q, stream) != cudaSuccess) return MOE_ERR_CUDA;
+  const int pairs = int8_pair_nmax(s);
   CUtensorMap md, mh;
   if (!make_map_i8(&md, w->down, static_cast<uint64_t>(s.E) * s.H, s.I, s.I, 128) ||
-      !make_map_i8(&mh, q.codes, cap_rows(s), s.I, s.I, 16))
+      !make_map_i8(&mh, q.codes, cap_rows(s), s.I, s.I, pairs != 0 ? 32 : 16))
     return MOE_ERR_CUDA;
   moe::Int8GemmArgs a = int8_plan_args(plan, s, err);
   a.row_scale = q.scales;
@@ -653,6 +660,7 @@ moe_status_t run_down_int8(const moe_bf16_t* h, const moe_weights_t* w, const mo
   a.out_ld = s.H;
   a.rows_per_expert = s.H;
   a.kdim = s.I;
+  if (pairs != 0) return cuda_status(moe::launch_int8_pair_down(md, mh, a, pairs, num_sms(), stream));
   return cuda_status(moe::launch_int8_down(md, mh, a, choose_nmax(s), stream));
 }
 
@@ -662,6 +670,28 @@ bool linear_int8_shape_ok(int64_t M, int64_t N, int64_t K) {
          (M / 32 + 1) * (N / 128 + 1) < (1ll << 31);
 }
 int64_t linear_int8_pitch(int64_t K) { return (K + 15) / 16 * 16; }
+
+// Tokens per tile of the dense product on pairs (512 channels each), or 0 for the one-tile-per-CTA kernel, which
+// takes the sizes that cannot give every pair a tile.  Of the widths from 128 to 256 the one whose longest pair has
+// the fewest token columns to compute: whole tiles of 256 leave the last round of pairs short.
+int linear_int8_tile(int64_t M, int64_t N) {
+  if (const char* env = std::getenv("MOE_INT8_TILE")) {
+    const int v = std::atoi(env);
+    if (v == 0 || (v >= 32 && v <= 256 && v % 32 == 0)) return v;
+  }
+  const int64_t pairs = num_sms() / 2, W = (N + 511) / 512;
+  int best = 0;
+  int64_t best_cost = 0;
+  for (int t = 256; t >= 128; t -= 32) {
+    const int64_t rounds = (W * ((M + t - 1) / t) + pairs - 1) / pairs;
+    const int64_t cost = rounds * (t + 16);  // a tile's drain costs about 16 columns
+    if (best == 0 || cost < best_cost) {
+      best = t;
+      best_cost = cost;
+    }
+  }
+  return W * ((M + best - 1) / best) >= pairs ? best : 0;
+}
 
 // moe_route_logits' options, shape and logits: MOE_OK or the status of the call.
 moe_status_t check_group_route(int32_t M, int32_t E, int32_t top_k, const moe_group_opts_t* o) {
@@ -1172,7 +1202,9 @@ moe_status_t moe_linear_int8(const moe_bf16_t* x, int64_t ldx, const int8_t* w, 
   q.scales = reinterpret_cast<float*>(base + L.scales);
   if (moe::launch_quantize_int8(q, cs) != cudaSuccess) return MOE_ERR_CUDA;
   CUtensorMap mw, mx;
-  if (!make_map_i8(&mw, w, N, K, ldw, 128) || !make_map_i8(&mx, q.codes, M, K, pitch, 16)) return MOE_ERR_CUDA;
+  const int tile_n = linear_int8_tile(M, N);
+  if (!make_map_i8(&mw, w, N, K, ldw, 128) || !make_map_i8(&mx, q.codes, M, K, pitch, tile_n != 0 ? 32 : 16))
+    return MOE_ERR_CUDA;
   moe::Int8GemmArgs a{};
   a.row_scale = q.scales;
   a.ch_scale0 = w_scale;
@@ -1186,6 +1218,10 @@ moe_status_t moe_linear_int8(const moe_bf16_t* x, int64_t ldx, const int8_t* w, 
   a.top_k = 1;
   a.rows_per_expert = static_cast<int>(N);
   a.kdim = static_cast<int>(K);
+  // 16-byte row stores need whole, aligned vectors of 8 bf16 values
+  a.out_plain = a.out_f32 || N % 8 != 0 || ldo % 8 != 0 || !aligned16(out);
+  a.tile_n = tile_n;
+  if (tile_n != 0) return cuda_status(moe::launch_int8_pair_dense(mw, mx, a, num_sms(), cs));
   return cuda_status(moe::launch_int8_dense(mw, mx, a, M <= 32 ? 32 : 128, cs));
 }
 

@@ -1,56 +1,156 @@
 // Symmetric 8-bit rows: the activation and weight form of the int8 projections.
 //   a = max |v| of the row;  scale = a / 127 (fp32);  code = rint(127 v / a), ties to even;  a = 0: scale 0, codes 0.
-// The codes are those of exact arithmetic: v and a are bf16, so 127 v (15 significant bits) is exact in fp32, and a
-// quotient that is not a tie is at least 1.5e-5 (relative) away from one, far more than the rounding of the
-// division.  A row that holds an infinity or a NaN gets the scale NaN and codes 0: its products are NaN.
+// A row that holds an infinity or a NaN gets the scale NaN and codes 0: its products are NaN.
+//
+// The codes are those of exact arithmetic without a division per element.  v and a are bf16 (8 significant bits), so
+// t = 127 v is exact in fp32.  The quotient t / a is either a tie (k + 1/2 exactly) or at least 1.5e-5 (relative) away
+// from one, so rounding t * (1/a), which is within 2^-22 of it, is right except on ties, and there it lands on one of
+// the two neighbours.  r = t - q a is exact (at most 17 bits): 2 |r| = a says tie, and an odd q moves to the even one.
+//
+// Bound: memory.  A row is read once into registers (16-byte loads, 8 in flight per thread), reduced and written as
+// codes; rows of up to 2048 columns take a warp, up to 8192 four warps, longer or unaligned ones a loop that reads
+// twice.
 #include "common.cuh"
 #include "kernels.h"
 
 namespace moe {
 namespace {
 
-constexpr int kQThreads = 128;  // one CTA per row
+constexpr int kQThreads = 128;
+constexpr int kVecs = 8;  // 16-byte vectors per thread
 
-// |v| as bf16 bits: ordered like the magnitudes, infinity 0x7f80, NaN above.
-__global__ void __launch_bounds__(kQThreads) quantize_int8_kernel(Int8RowsArgs a) {
+// Power of two that brings a row's largest magnitude into a range where 127 v stays finite and 1 / a normal.
+__device__ __forceinline__ float prescale(float a) { return a > 0x1p100f ? 0x1p-32f : (a < 0x1p-60f ? 0x1p64f : 1.0f); }
+
+struct RowScale {
+  float a, inv, pre;  // largest magnitude times pre; its reciprocal (0: all codes are 0)
+};
+
+__device__ __forceinline__ RowScale row_scale_of(uint32_t top) {
+  const float amax = __uint_as_float(top << 16);
+  RowScale s;
+  s.pre = prescale(amax);
+  s.a = amax * s.pre;
+  s.inv = top != 0 && top < 0x7f80u ? __frcp_rn(s.a) : 0.0f;
+  return s;
+}
+
+__device__ __forceinline__ float scale_value(uint32_t top) {
+  return top < 0x7f80u ? __fdiv_rn(__uint_as_float(top << 16), 127.0f) : __uint_as_float(0x7fffffffu);
+}
+
+// The code of v (times pre), as the low byte of the result.
+__device__ __forceinline__ uint32_t code_of(float v, const RowScale& s) {
+  constexpr float kMagic = 12582912.0f;  // 1.5 * 2^23: adding it rounds to an integer, ties to even
+  const float t = 127.0f * v;
+  const float y = fmaf(t, s.inv, kMagic);
+  const float r = fmaf(-(y - kMagic), s.a, t);
+  uint32_t q = __float_as_uint(y);
+  if (fabsf(r) * 2.0f == s.a && (q & 1u)) q += r > 0.0f ? 1 : -1;
+  return q;
+}
+
+// |v| as bf16 bits is ordered like the magnitudes: infinity is 0x7f80, NaN above.
+__device__ __forceinline__ uint32_t max_bits(uint32_t top, uint32_t pair) {
+  return max(top, max(pair & 0x7fffu, (pair >> 16) & 0x7fffu));
+}
+
+// kRowThreads threads per row (32 or 128), kVecs vectors of 8 columns each at most.
+template <int kRowThreads>
+__global__ void __launch_bounds__(kQThreads) quantize_rows_kernel(Int8RowsArgs a) {
   __shared__ uint32_t part[kQThreads / 32];
-  const int tid = threadIdx.x;
-  for (int64_t r = blockIdx.x; r < a.rows; r += gridDim.x) {
-    int64_t src_row = r;
-    if (a.sorted_ids != nullptr) {
-      if (r >= *a.ntpp) return;
+  const int tid = threadIdx.x % kRowThreads;
+  const int64_t r = static_cast<int64_t>(blockIdx.x) * (kQThreads / kRowThreads) + threadIdx.x / kRowThreads;
+  bool live = r < a.rows;
+  if (live && a.sorted_ids != nullptr) {
+    live = r < *a.ntpp;
+    if (live) {
       const int id = a.sorted_ids[r];
-      if (id < 0 || id >= a.nslots) continue;  // padding
+      live = id >= 0 && id < a.nslots;  // not padding
     }
-    const uint16_t* src = a.src + src_row * a.ld;
-    uint32_t top = 0;
-    for (int c = tid; c < a.cols; c += kQThreads) top = max(top, static_cast<uint32_t>(src[c] & 0x7fffu));
-    top = __reduce_max_sync(0xffffffffu, top);
-    if ((tid & 31) == 0) part[tid >> 5] = top;
+  }
+  const uint4* src = reinterpret_cast<const uint4*>(a.src + (live ? r : 0) * a.ld);
+  const int nvec = live ? a.cols / 8 : 0;
+  uint4 v[kVecs];
+#pragma unroll
+  for (int i = 0; i < kVecs; ++i) {
+    const int c = tid + kRowThreads * i;
+    v[i] = c < nvec ? src[c] : make_uint4(0, 0, 0, 0);
+  }
+  uint32_t top = 0;
+#pragma unroll
+  for (int i = 0; i < kVecs; ++i) top = max_bits(max_bits(max_bits(max_bits(top, v[i].x), v[i].y), v[i].z), v[i].w);
+  top = __reduce_max_sync(0xffffffffu, top);
+  if (kRowThreads > 32) {
+    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = top;
     __syncthreads();
-    top = 0;
 #pragma unroll
     for (int q = 0; q < kQThreads / 32; ++q) top = max(top, part[q]);
-    __syncthreads();
-    const float amax = __uint_as_float(top << 16);
-    const bool fin = top < 0x7f80u;
-    if (tid == 0) a.scales[r] = fin ? __fdiv_rn(amax, 127.0f) : __uint_as_float(0x7fffffffu);
-    // rows above 2^100 are divided by 2^32 first, so that 127 v stays finite (what drops below the range is code 0)
-    const float pre = amax > 0x1p100f ? 0x1p-32f : 1.0f;
-    int8_t* dst = a.codes + r * a.pitch;
-    for (int c = tid; c < a.cols; c += kQThreads) {
-      const float v = __uint_as_float(static_cast<uint32_t>(src[c]) << 16) * pre;
-      const float q = fin && top != 0 ? rintf(__fdiv_rn(127.0f * v, amax * pre)) : 0.0f;
-      dst[c] = static_cast<int8_t>(static_cast<int>(q));
+  }
+  if (!live) return;
+  if (tid == 0) a.scales[r] = scale_value(top);
+  const RowScale s = row_scale_of(top);
+  uint2* dst = reinterpret_cast<uint2*>(a.codes + r * a.pitch);
+#pragma unroll
+  for (int i = 0; i < kVecs; ++i) {
+    const int c = tid + kRowThreads * i;
+    if (c >= nvec) break;
+    const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+    uint32_t o[2];
+#pragma unroll
+    for (int p = 0; p < 2; ++p) {
+      uint32_t q[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        q[u] = code_of(((u & 1) ? bf16_hi(w[2 * p + u / 2]) : bf16_lo(w[2 * p + u / 2])) * s.pre, s);
+      o[p] = __byte_perm(__byte_perm(q[0], q[1], 0x0040), __byte_perm(q[2], q[3], 0x0040), 0x5410);
     }
+    // a row with no scale (inv 0) has codes 0 whatever its values
+    dst[c] = s.inv != 0.0f ? make_uint2(o[0], o[1]) : make_uint2(0, 0);
+  }
+}
+
+// Any alignment and length: one CTA per row, two passes over it.
+__global__ void __launch_bounds__(kQThreads) quantize_any_kernel(Int8RowsArgs a) {
+  __shared__ uint32_t part[kQThreads / 32];
+  const int tid = threadIdx.x;
+  const int64_t r = blockIdx.x;
+  if (a.sorted_ids != nullptr) {
+    if (r >= *a.ntpp) return;
+    const int id = a.sorted_ids[r];
+    if (id < 0 || id >= a.nslots) return;
+  }
+  const uint16_t* src = a.src + r * a.ld;
+  uint32_t top = 0;
+  for (int c = tid; c < a.cols; c += kQThreads) top = max(top, static_cast<uint32_t>(src[c] & 0x7fffu));
+  top = __reduce_max_sync(0xffffffffu, top);
+  if ((tid & 31) == 0) part[tid >> 5] = top;
+  __syncthreads();
+#pragma unroll
+  for (int q = 0; q < kQThreads / 32; ++q) top = max(top, part[q]);
+  if (tid == 0) a.scales[r] = scale_value(top);
+  const RowScale s = row_scale_of(top);
+  int8_t* dst = a.codes + r * a.pitch;
+  for (int c = tid; c < a.cols; c += kQThreads) {
+    const float v = __uint_as_float(static_cast<uint32_t>(src[c]) << 16) * s.pre;
+    dst[c] = s.inv != 0.0f ? static_cast<int8_t>(code_of(v, s) & 0xffu) : 0;
   }
 }
 
 }  // namespace
 
 cudaError_t launch_quantize_int8(const Int8RowsArgs& a, cudaStream_t stream) {
-  const int64_t grid = a.rows < (1 << 20) ? a.rows : (1 << 20);
-  quantize_int8_kernel<<<static_cast<unsigned>(grid), kQThreads, 0, stream>>>(a);
+  const bool vectors = a.cols % 8 == 0 && a.ld % 8 == 0 && a.pitch % 8 == 0 &&
+                       (reinterpret_cast<uintptr_t>(a.src) & 15u) == 0 &&
+                       (reinterpret_cast<uintptr_t>(a.codes) & 7u) == 0;
+  if (vectors && a.cols <= 32 * 8 * kVecs) {
+    const int64_t per = kQThreads / 32;
+    quantize_rows_kernel<32><<<static_cast<unsigned>((a.rows + per - 1) / per), kQThreads, 0, stream>>>(a);
+  } else if (vectors && a.cols <= kQThreads * 8 * kVecs) {
+    quantize_rows_kernel<kQThreads><<<static_cast<unsigned>(a.rows), kQThreads, 0, stream>>>(a);
+  } else {
+    quantize_any_kernel<<<static_cast<unsigned>(a.rows), kQThreads, 0, stream>>>(a);
+  }
   return cudaGetLastError();
 }
 

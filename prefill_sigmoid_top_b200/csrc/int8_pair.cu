@@ -1,0 +1,472 @@
+// Products of 8-bit rows on 2-SM pairs (tcgen05 kind::i8 with cta_group::2) for many tokens: the plan's expert
+// projections and the dense product, the int8 form of the bf16 pair kernels (same pair protocol and warp roles).
+//
+// Why pairs: a single SM that computes 128 channels x 128 tokens reads 32 KB of shared-memory operands for every
+// 262 clocks of int8 MMA, twice what L2 delivers to it.  A pair computes 512 channels x 256 tokens: each CTA reads
+// its own 2 x 128 channels and half of the tokens, 48 KB for 1024 clocks.
+//
+// Tile: a weight block w of one expert x up to kNmax tokens; CTA r of the pair holds two boxes of 128 weight rows:
+//   up:          rows 256 w + 128 r.. of W_gate and of W_up (the two accumulators of silu(gate) * up);
+//   down, dense: rows 512 w + 128 r.. and 512 w + 256 + 128 r.. (two accumulators of M = 256 each);
+// and token rows [r N/2, (r + 1) N/2) of the tile's N (its tokens rounded up to 32, the width step of this MMA).
+// Channels past the expert's last row are computed and not stored.
+//
+// Warps (640 threads): 0 = weight producer, 1 = MMA issuer (leader), 2 = token producer, 3 idle, 4..19 = epilogue.
+// Every wait is bounded; a timeout sets the error word and unwinds, and both CTAs still meet at the last cluster
+// barrier.
+#include "common.cuh"
+#include "kernels.h"
+#include "pair_ptx.cuh"
+#include "tile_list.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int kBM = 128;              // weight rows per box
+constexpr int kBK = 128;              // codes per stage
+constexpr int kBoxBytes = kBM * kBK;  // 16 KB
+constexpr int kBRows = 32;            // rows per token box
+constexpr int kEpiWarps = 16;
+constexpr int kThreads = 128 + 32 * kEpiWarps;
+
+enum Mode { kUp = 0, kDown = 1, kDense = 2 };
+
+template <int kNmax, int kStagesA, int kStagesB>
+struct PCfg {
+  static constexpr int kHalf = kNmax / 2;
+  static constexpr int kAStage = 2 * kBoxBytes;
+  static constexpr int kBStage = kHalf * kBK;
+  static constexpr int kAccCols = 2 * kNmax;
+  static constexpr int kAccBufs = 512 / kAccCols;
+  static constexpr int kMisc = 10240;  // barriers, flags, counts and tile prefix over the experts (E <= 1024)
+  static constexpr int kSmem = 1024 + kStagesA * kAStage + kStagesB * kBStage + kMisc;
+  static_assert(kNmax == 128 || kNmax == 256, "token-tile widths");
+  static_assert(kSmem <= 227 * 1024, "shared memory");
+  static_assert(kSmem > 116 * 1024, "one CTA per SM: it owns all 512 tensor-memory columns");
+};
+
+// kGather (up): the token rows are gathered from the codes of x by token id (tile::gather4); otherwise they are
+// consecutive plan rows (or rows of x, dense).
+template <int kMode, bool kGather, int kNmax, int kStagesA, int kStagesB>
+__global__ void __launch_bounds__(kThreads, 1)
+    int8_pair_kernel(const __grid_constant__ CUtensorMap tm_a0, const __grid_constant__ CUtensorMap tm_a1,
+                     const __grid_constant__ CUtensorMap tm_b, const Int8GemmArgs args) {
+  using C = PCfg<kNmax, kStagesA, kStagesB>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* a_ring = smem;
+  uint8_t* b_ring = a_ring + kStagesA * C::kAStage;
+  uint8_t* misc = b_ring + kStagesB * C::kBStage;
+  uint64_t* a_full = reinterpret_cast<uint64_t*>(misc);
+  uint64_t* a_empty = a_full + kStagesA;
+  uint64_t* b_full = a_empty + kStagesA;
+  uint64_t* b_empty = b_full + kStagesB;
+  uint64_t* acc_full = b_empty + kStagesB;  // [2]
+  uint64_t* acc_empty = acc_full + 2;       // [2] (the leader's counts both CTAs' epilogue warps)
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_empty + 2);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  int* cnt = const_cast<int*>(abort_flag + 1);  // [E]
+  int* prefix = cnt + 1024;                     // [E + 1]
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t rank = cta_rank_in_cluster();
+  const bool leader = rank == 0;
+  const int pair = static_cast<int>(blockIdx.x) >> 1;
+  const int npairs = static_cast<int>(gridDim.x) >> 1;
+  const int E = args.E;
+  constexpr int kBlock = kMode == kUp ? 2 * kBM : 4 * kBM;  // channels of a weight block
+  const int W = (args.rows_per_expert + kBlock - 1) / kBlock;
+  const int tw = kMode == kDense ? args.tile_n : kNmax;     // tokens per tile
+  const int dense_tiles = (args.M + tw - 1) / tw;
+
+  if (kMode != kDense)
+    for (int e = tid; e < E; e += kThreads) cnt[e] = args.counts[e];
+  if (tid == 0) *abort_flag = 0;
+  __syncthreads();
+  if (kMode != kDense && warp == 0) build_tile_prefix<kNmax>(cnt, prefix, E, W, lane);
+  if (tid == 0) {
+    for (int s = 0; s < kStagesA; ++s) {
+      mbar_init(&a_full[s], 1);
+      mbar_init(&a_empty[s], 1);
+    }
+    for (int s = 0; s < kStagesB; ++s) {
+      mbar_init(&b_full[s], 1);
+      mbar_init(&b_empty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&acc_full[b], 1);
+      mbar_init(&acc_empty[b], 2 * kEpiWarps);
+    }
+    fence_mbar_init();
+  }
+  __syncthreads();
+  const int total = kMode == kDense ? W * dense_tiles : prefix[E];
+  if (pair >= total) return;  // both CTAs of a pair see the same count
+  if (warp == 1) {
+    tmem_alloc_pair(tmem_slot, 512);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before_sync();
+  cluster_sync_all();  // the peer's barriers are initialised and both CTAs hold tensor memory
+  tc_fence_after_sync();
+  const uint32_t tmem = *tmem_slot;
+  const int nk = (args.kdim + kBK - 1) / kBK;
+  const int nslots = args.M * args.top_k;
+
+  struct Tile {
+    int e, w, row0, nrows, N, count;
+  };
+  auto tile_at = [&](int idx) {
+    Tile t;
+    if (kMode == kDense) {
+      t.e = 0;
+      t.w = idx / dense_tiles;
+      t.row0 = (idx % dense_tiles) * tw;
+      t.count = args.M;
+      t.nrows = min(tw, args.M - t.row0);
+    } else {
+      const TileCoord c = decode_tile<kNmax>(prefix, cnt, E, idx);
+      t.e = c.e;
+      t.w = c.w;
+      t.count = cnt[c.e];
+      t.nrows = min(kNmax, t.count - c.t * kNmax);
+      t.row0 = args.offsets[c.e] + c.t * kNmax;
+    }
+    t.N = (t.nrows + 31) & ~31;
+    return t;
+  };
+
+  if (warp == 0) {
+    // ------------------------------------------------ weight producer (both CTAs)
+    if (lane == 0) {
+      prefetch_tensor_map(&tm_a0);
+      if (kMode == kUp) prefetch_tensor_map(&tm_a1);
+    }
+    int ka = 0;
+    bool alive = true;
+    for (int tile = pair; tile < total && alive; tile += npairs) {
+      const Tile c = tile_at(tile);
+      const uint64_t pol = c.count <= tw ? l2_policy_evict_first() : l2_policy_evict_normal();
+      const int row_a0 = c.e * args.rows_per_expert + c.w * kBlock + static_cast<int>(rank) * kBM;
+      const int row_a1 = kMode == kUp ? row_a0 : row_a0 + 2 * kBM;
+      for (int k = 0; k < nk; ++k, ++ka) {
+        const int s = ka % kStagesA;
+        bool ok = true;
+        if (lane == 0) {
+          ok = mbar_wait_bounded(&a_empty[s], ((ka / kStagesA) & 1) ^ 1, abort_flag);
+          if (ok && leader) mbar_arrive_expect_tx(&a_full[s], 2 * C::kAStage);
+        }
+        ok = __shfl_sync(0xffffffffu, ok, 0);
+        if (!ok) {
+          if (lane == 0) {
+            *abort_flag = 1;
+            set_error(args.err, kErrTimeout);
+          }
+          alive = false;
+          break;
+        }
+        uint8_t* st = a_ring + s * C::kAStage;
+        const uint32_t bar = cluster_addr(&a_full[s], 0);
+        if (lane == 0)
+          tma_load_2d_pair(&tm_a0, bar, st, k * kBK, row_a0, pol);
+        else if (lane == 1)
+          tma_load_2d_pair(kMode == kUp ? &tm_a1 : &tm_a0, bar, st + kBoxBytes, k * kBK, row_a1, pol);
+      }
+    }
+    __syncwarp();
+  } else if (warp == 2) {
+    // ------------------------------------------------ token-row producer (both CTAs)
+    if (lane == 0) prefetch_tensor_map(&tm_b);
+    const uint64_t pol_b = l2_policy_evict_normal();
+    int kb = 0;
+    bool alive = true;
+    for (int tile = pair; tile < total && alive; tile += npairs) {
+      const Tile c = tile_at(tile);
+      const int half = c.N / 2;
+      const int row0 = c.row0 + static_cast<int>(rank) * half;
+      const int nbox = (half + kBRows - 1) / kBRows;
+      // gathered: lane i copies rows 4 i .. 4 i + 3 of this CTA's half (rows past the tile's last take token 0;
+      // their columns are never stored)
+      int tok[4] = {0, 0, 0, 0};
+      if (kGather) {
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const int r = 4 * lane + u;
+          if (r < half && static_cast<int>(rank) * half + r < c.nrows) {
+            const int id = args.sorted_ids[row0 + r];
+            tok[u] = (id >= 0 && id < nslots) ? id / args.top_k : 0;
+          }
+        }
+      }
+      const uint32_t b_bytes = kGather ? 2u * half * kBK : 2u * nbox * kBRows * kBK;
+      for (int k = 0; k < nk; ++k, ++kb) {
+        const int s = kb % kStagesB;
+        bool ok = true;
+        if (lane == 0) {
+          ok = mbar_wait_bounded(&b_empty[s], ((kb / kStagesB) & 1) ^ 1, abort_flag);
+          if (ok && leader) mbar_arrive_expect_tx(&b_full[s], b_bytes);
+        }
+        ok = __shfl_sync(0xffffffffu, ok, 0);
+        if (!ok) {
+          if (lane == 0) {
+            *abort_flag = 1;
+            set_error(args.err, kErrTimeout);
+          }
+          alive = false;
+          break;
+        }
+        uint8_t* st = b_ring + s * C::kBStage;
+        if (kGather) {
+          if (4 * lane < half)
+            tma_gather4_pair(&tm_b, cluster_addr(&b_full[s], 0), st + lane * 4 * kBK, k * kBK, tok[0], tok[1], tok[2],
+                             tok[3], pol_b);
+        } else if (lane < nbox) {
+          tma_load_2d_pair(&tm_b, cluster_addr(&b_full[s], 0), st + lane * kBRows * kBK, k * kBK,
+                           row0 + lane * kBRows, pol_b);
+        }
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ------------------------------------------------ MMA issuer (leader only)
+    if (leader && lane == 0) {
+      int ka = 0, kb = 0, j = 0;
+      bool alive = true;
+      for (int tile = pair; tile < total && alive; tile += npairs, ++j) {
+        const uint32_t idesc = umma_idesc_s8(2 * kBM, tile_at(tile).N);
+        const int buf = j % C::kAccBufs;
+        if (!mbar_wait_bounded(&acc_empty[buf], ((j / C::kAccBufs) & 1) ^ 1, abort_flag)) {
+          *abort_flag = 1;
+          set_error(args.err, kErrTimeout);
+          break;
+        }
+        tc_fence_after_sync();
+        const uint32_t d0 = tmem + buf * C::kAccCols;
+        const uint32_t d1 = d0 + kNmax;
+        for (int k = 0; k < nk; ++k, ++ka, ++kb) {
+          const int sa = ka % kStagesA, sb = kb % kStagesB;
+          if (!mbar_wait_bounded(&a_full[sa], (ka / kStagesA) & 1, abort_flag) ||
+              !mbar_wait_bounded(&b_full[sb], (kb / kStagesB) & 1, abort_flag)) {
+            *abort_flag = 1;
+            set_error(args.err, kErrTimeout);
+            alive = false;
+            break;
+          }
+          tc_fence_after_sync();
+          const uint64_t da0 = umma_desc_sw128(a_ring + sa * C::kAStage);
+          const uint64_t da1 = umma_desc_sw128(a_ring + sa * C::kAStage + kBoxBytes);
+          const uint64_t db = umma_desc_sw128(b_ring + sb * C::kBStage);
+#pragma unroll
+          for (int kk = 0; kk < kBK / 32; ++kk) {
+            const uint32_t acc = (k | kk) != 0 ? 1u : 0u;
+            umma_s8_pair(d0, da0 + 2 * kk, db + 2 * kk, idesc, acc);
+            umma_s8_pair(d1, da1 + 2 * kk, db + 2 * kk, idesc, acc);
+          }
+          umma_commit_pair(&a_empty[sa]);
+          umma_commit_pair(&b_empty[sb]);
+        }
+        umma_commit_pair(&acc_full[buf]);  // also on an abort, so neither epilogue is left waiting
+      }
+    }
+    __syncwarp();
+  } else if (warp >= 4) {
+    // ------------------------------------------------ epilogue (both CTAs: their own 2 x 128 channels)
+    const int q = warp & 3;
+    const int part_c = (warp - 4) >> 2;  // which of the four 16-column chunks of every 64 this warp drains
+    constexpr int kChunks = kNmax / 64;
+    const int g8 = lane >> 3, b8 = lane & 7;
+    int j = 0;
+    for (int tile = pair; tile < total; tile += npairs, ++j) {
+      const Tile c = tile_at(tile);
+      const int buf = j % C::kAccBufs;
+      const int colbase = c.w * kBlock + static_cast<int>(rank) * kBM + q * 32;  // this warp's first channel
+      // what the scaling needs, loaded while the tile is still being computed: the lane's channel scales, and in
+      // lane i < 16 the scale and output row of the chunk's token i
+      const int ch0 = colbase + lane, ch1 = kMode == kUp ? ch0 : ch0 + 2 * kBM;
+      const size_t ch_at = static_cast<size_t>(c.e) * args.rows_per_expert;
+      const float s0 = ch0 < args.rows_per_expert ? args.ch_scale0[ch_at + ch0] : 0.0f;
+      const float s1 = ch1 < args.rows_per_expert ? (kMode == kUp ? args.ch_scale1 : args.ch_scale0)[ch_at + ch1] : 0.0f;
+      float tok_s[kChunks];
+      int tok_row[kChunks];
+#pragma unroll
+      for (int i = 0; i < kChunks; ++i) {
+        const int n = 16 * part_c + 64 * i + (lane & 15);
+        tok_s[i] = 0.0f;
+        tok_row[i] = -1;
+        if (n < c.nrows) {
+          const int row = c.row0 + n;
+          if (kMode == kDense) {
+            tok_s[i] = args.row_scale[row];
+            tok_row[i] = row;
+          } else {
+            const int id = args.sorted_ids[row];
+            if (id >= 0 && id < nslots) {
+              tok_s[i] = args.row_scale[kGather ? id / args.top_k : row];
+              tok_row[i] = kMode == kUp ? row : id;
+            } else {
+              set_error(args.err, kErrInvalidInput);
+            }
+          }
+        }
+      }
+      bool ok = true;
+      if (lane == 0) ok = mbar_wait_bounded(&acc_full[buf], (j / C::kAccBufs) & 1, abort_flag);
+      ok = __shfl_sync(0xffffffffu, ok, 0);
+      tc_fence_after_sync();
+      const bool go = __shfl_sync(0xffffffffu, ok && !*abort_flag, 0);
+      if (!go) {
+        if (lane == 0 && !ok) set_error(args.err, kErrTimeout);
+        break;
+      }
+      const uint32_t lane_base = tmem + (static_cast<uint32_t>(q * 32) << 16) + buf * C::kAccCols;
+      if (kMode == kDense && args.out_plain) {
+        // fp32 results, or rows that take no 16-byte stores: lane = channel, one store per token and half
+#pragma unroll
+        for (int i = 0; i < kChunks; ++i) {
+          const int cb = 16 * part_c + 64 * i;
+          if (cb >= c.N) break;
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            uint32_t v[16];
+            tmem_load_16(lane_base + half * kNmax + cb, v);
+            tmem_load_wait();
+            const int ch = half ? ch1 : ch0;
+            const float sc = half ? s1 : s0;
+#pragma unroll
+            for (int p = 0; p < 16; ++p) {
+              const int row = __shfl_sync(0xffffffffu, tok_row[i], p);
+              const float r = (__shfl_sync(0xffffffffu, tok_s[i], p) * sc) * static_cast<float>(static_cast<int>(v[p]));
+              if (row < 0 || ch >= args.rows_per_expert) continue;
+              const size_t at = static_cast<size_t>(row) * args.out_ld + ch;
+              if (args.out_f32)
+                static_cast<float*>(args.out)[at] = r;
+              else
+                static_cast<__nv_bfloat16*>(args.out)[at] = __float2bfloat16_rn(r);
+            }
+          }
+        }
+        tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(cluster_addr(&acc_empty[buf], 0));
+        continue;
+      }
+      // 1. drain: lane l holds channel ch0 (ch1) for the tokens of its chunks; scaled and packed as bf16 token
+      //    pairs, then the accumulator is released at once, so the next tile's MMAs run while this one is stored
+      constexpr int kWords = kMode == kUp ? 8 : 16;
+      uint32_t pk[kChunks][kWords];
+#pragma unroll
+      for (int i = 0; i < kChunks; ++i) {
+        const int cb = 16 * part_c + 64 * i;
+        if (cb >= c.N) break;
+        uint32_t v0[16], v1[16];
+        tmem_load_16(lane_base + cb, v0);
+        tmem_load_16(lane_base + kNmax + cb, v1);
+        tmem_load_wait();
+#pragma unroll
+        for (int p = 0; p < 8; ++p) {
+          float a[2], b[2];
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            const float sx = __shfl_sync(0xffffffffu, tok_s[i], 2 * p + u);
+            a[u] = (sx * s0) * static_cast<float>(static_cast<int>(v0[2 * p + u]));
+            b[u] = (sx * s1) * static_cast<float>(static_cast<int>(v1[2 * p + u]));
+          }
+          if (kMode == kUp) {
+            pk[i][p] = pack_bf16x2(silu_mul(a[0], b[0]), silu_mul(a[1], b[1]));
+          } else {
+            pk[i][p] = pack_bf16x2(a[0], a[1]);
+            pk[i][kWords - 8 + p] = pack_bf16x2(b[0], b[1]);
+          }
+        }
+      }
+      tc_fence_before_sync();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(cluster_addr(&acc_empty[buf], 0));
+      // 2. store: the 8 x 8 transpose in each group of 8 lanes gives lane 8 g + b tokens 2 b and 2 b + 1 of the
+      //    chunk at channels colbase + 8 g .. + 7: 16-byte row stores
+      const int col8 = colbase + 8 * g8;
+#pragma unroll
+      for (int i = 0; i < kChunks; ++i) {
+        const int cb = 16 * part_c + 64 * i;
+        if (cb >= c.N) break;
+        const int d0 = __shfl_sync(0xffffffffu, tok_row[i], 2 * b8);
+        const int d1 = __shfl_sync(0xffffffffu, tok_row[i], 2 * b8 + 1);
+#pragma unroll
+        for (int half = 0; half < (kMode == kUp ? 1 : 2); ++half) {
+          uint32_t w[8];
+#pragma unroll
+          for (int p = 0; p < 8; ++p) w[p] = pk[i][8 * half + p];
+          transpose8x8(w, b8);
+          const uint4 r0 = make_uint4(__byte_perm(w[0], w[1], 0x5410), __byte_perm(w[2], w[3], 0x5410),
+                                      __byte_perm(w[4], w[5], 0x5410), __byte_perm(w[6], w[7], 0x5410));
+          const uint4 r1 = make_uint4(__byte_perm(w[0], w[1], 0x7632), __byte_perm(w[2], w[3], 0x7632),
+                                      __byte_perm(w[4], w[5], 0x7632), __byte_perm(w[6], w[7], 0x7632));
+          const int cc = col8 + half * 2 * kBM;
+          if (cc >= args.rows_per_expert) continue;  // a multiple of 8 here
+          uint16_t* out = static_cast<uint16_t*>(args.out);
+          if (d0 >= 0) *reinterpret_cast<uint4*>(out + static_cast<size_t>(d0) * args.out_ld + cc) = r0;
+          if (d1 >= 0) *reinterpret_cast<uint4*>(out + static_cast<size_t>(d1) * args.out_ld + cc) = r1;
+        }
+      }
+    }
+  }
+  tc_fence_before_sync();
+  __syncthreads();
+  cluster_sync_all();  // neither CTA leaves while the other may still use its shared or tensor memory
+  if (warp == 1) tmem_dealloc_pair(tmem, 512);
+}
+
+template <int kMode, bool kGather, int kNmax, int kStagesA, int kStagesB>
+cudaError_t launch_pairs(const CUtensorMap& a0, const CUtensorMap& a1, const CUtensorMap& b, const Int8GemmArgs& args,
+                         int num_sms, cudaStream_t stream) {
+  using C = PCfg<kNmax, kStagesA, kStagesB>;
+  auto kern = int8_pair_kernel<kMode, kGather, kNmax, kStagesA, kStagesB>;
+  int dev = 0;
+  cudaError_t st = cudaGetDevice(&dev);
+  if (st != cudaSuccess) return st;
+  static bool done[64] = {};
+  if (dev >= 64 || !done[dev]) {
+    st = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    if (st != cudaSuccess) return st;
+    if (dev < 64) done[dev] = true;
+  }
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(num_sms & ~1));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = C::kSmem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, a0, a1, b, args);
+}
+
+}  // namespace
+
+cudaError_t launch_int8_pair_up(const CUtensorMap& w_gate, const CUtensorMap& w_up, const CUtensorMap& x_rows,
+                                const Int8GemmArgs& args, int nmax, bool gather, int num_sms, cudaStream_t stream) {
+  if (nmax >= 256) {
+    if (gather) return launch_pairs<kUp, true, 256, 5, 3>(w_gate, w_up, x_rows, args, num_sms, stream);
+    return launch_pairs<kUp, false, 256, 5, 3>(w_gate, w_up, x_rows, args, num_sms, stream);
+  }
+  if (gather) return launch_pairs<kUp, true, 128, 5, 6>(w_gate, w_up, x_rows, args, num_sms, stream);
+  return launch_pairs<kUp, false, 128, 5, 6>(w_gate, w_up, x_rows, args, num_sms, stream);
+}
+
+cudaError_t launch_int8_pair_down(const CUtensorMap& w_down, const CUtensorMap& h_rows, const Int8GemmArgs& args,
+                                  int nmax, int num_sms, cudaStream_t stream) {
+  if (nmax >= 256) return launch_pairs<kDown, false, 256, 5, 3>(w_down, w_down, h_rows, args, num_sms, stream);
+  return launch_pairs<kDown, false, 128, 5, 6>(w_down, w_down, h_rows, args, num_sms, stream);
+}
+
+cudaError_t launch_int8_pair_dense(const CUtensorMap& w, const CUtensorMap& x_rows, const Int8GemmArgs& args,
+                                   int num_sms, cudaStream_t stream) {
+  if (args.tile_n < 32 || args.tile_n > 256 || args.tile_n % 32 != 0) return cudaErrorInvalidValue;
+  return launch_pairs<kDense, false, 256, 5, 3>(w, w, x_rows, args, num_sms, stream);
+}
+
+}  // namespace moe

@@ -248,6 +248,8 @@ struct Int8GemmArgs {
   void* out;                  // up: h [cap, I]; down: y [M*K, H]; dense: [M, out_ld]
   int64_t out_ld;
   int out_f32;                // dense: fp32 results instead of bf16
+  int out_plain;              // dense: element stores (fp32, or rows that take no 16-byte stores)
+  int tile_n;                 // dense on pairs: tokens per tile, a multiple of 32 up to 256
   int32_t* err;
   int M, E, top_k;
   int rows_per_expert;        // up: I; down: H; dense: N
@@ -261,5 +263,14 @@ cudaError_t launch_int8_down(const CUtensorMap& w_down, const CUtensorMap& h_row
                              cudaStream_t stream);
 cudaError_t launch_int8_dense(const CUtensorMap& w, const CUtensorMap& x_rows, const Int8GemmArgs& args, int nmax,
                               cudaStream_t stream);
+
+// int8_pair.cu: the same on 2-SM pairs.  Tensor maps: weights as above; token rows in 32-row boxes, or x codes in
+// one-row boxes (gather).
+cudaError_t launch_int8_pair_up(const CUtensorMap& w_gate, const CUtensorMap& w_up, const CUtensorMap& x_rows,
+                                const Int8GemmArgs& args, int nmax, bool gather, int num_sms, cudaStream_t stream);
+cudaError_t launch_int8_pair_down(const CUtensorMap& w_down, const CUtensorMap& h_rows, const Int8GemmArgs& args,
+                                  int nmax, int num_sms, cudaStream_t stream);
+cudaError_t launch_int8_pair_dense(const CUtensorMap& w, const CUtensorMap& x_rows, const Int8GemmArgs& args,
+                                   int num_sms, cudaStream_t stream);
 
 }  // namespace moe
