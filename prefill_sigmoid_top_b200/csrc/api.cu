@@ -627,7 +627,7 @@ moe_status_t run_up_int8(const moe_bf16_t* x, const moe_weights_t* w, const moe_
   a.kdim = s.H;
   if (const int n = int8_pair_nmax(s))
     return cuda_status(moe::launch_int8_pair_up(mg, mu, mx, a, n, true, num_sms(), stream));
-  return cuda_status(moe::launch_int8_up(mg, mu, mx, a, choose_nmax(s), stream));
+  return cuda_status(moe::launch_int8_up(mg, mu, mx, a, choose_nmax(s), num_sms(), stream));
 }
 
 // int8 down: the real plan rows of h -> codes and scales -> GEMM scattered to slots.
@@ -661,7 +661,7 @@ moe_status_t run_down_int8(const moe_bf16_t* h, const moe_weights_t* w, const mo
   a.rows_per_expert = s.H;
   a.kdim = s.I;
   if (pairs != 0) return cuda_status(moe::launch_int8_pair_down(md, mh, a, pairs, num_sms(), stream));
-  return cuda_status(moe::launch_int8_down(md, mh, a, choose_nmax(s), stream));
+  return cuda_status(moe::launch_int8_down(md, mh, a, choose_nmax(s), num_sms(), stream));
 }
 
 // moe_linear_int8's arguments that its workspace size depends on.
@@ -1222,7 +1222,7 @@ moe_status_t moe_linear_int8(const moe_bf16_t* x, int64_t ldx, const int8_t* w, 
   a.out_plain = a.out_f32 || N % 8 != 0 || ldo % 8 != 0 || !aligned16(out);
   a.tile_n = tile_n;
   if (tile_n != 0) return cuda_status(moe::launch_int8_pair_dense(mw, mx, a, num_sms(), cs));
-  return cuda_status(moe::launch_int8_dense(mw, mx, a, M <= 32 ? 32 : 128, cs));
+  return cuda_status(moe::launch_int8_dense(mw, mx, a, M <= 32 ? 32 : 128, num_sms(), cs));
 }
 
 moe_status_t moe_selftest_wait_timeout(int32_t* err_flag, uint32_t limit_us, moe_stream_t stream) {

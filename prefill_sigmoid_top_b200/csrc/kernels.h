@@ -249,6 +249,7 @@ struct Int8GemmArgs {
   int64_t out_ld;
   int out_f32;                // dense: fp32 results instead of bf16
   int out_plain;              // dense: element stores (fp32, or rows that take no 16-byte stores)
+  int split;                  // int8_gemm.cu sets it: CTAs that share a tile's K
   int tile_n;                 // dense on pairs: tokens per tile, a multiple of 32 up to 256
   int32_t* err;
   int M, E, top_k;
@@ -258,11 +259,11 @@ struct Int8GemmArgs {
 // Tensor maps: weights in 128-row boxes of 128 bytes; up: x codes [M, H] in one-row boxes (gathered by token);
 // down / dense: h codes [cap, I] / x codes [M, K] in 16-row boxes.
 cudaError_t launch_int8_up(const CUtensorMap& w_gate, const CUtensorMap& w_up, const CUtensorMap& x_rows,
-                           const Int8GemmArgs& args, int nmax, cudaStream_t stream);
+                           const Int8GemmArgs& args, int nmax, int num_sms, cudaStream_t stream);
 cudaError_t launch_int8_down(const CUtensorMap& w_down, const CUtensorMap& h_rows, const Int8GemmArgs& args, int nmax,
-                             cudaStream_t stream);
+                             int num_sms, cudaStream_t stream);
 cudaError_t launch_int8_dense(const CUtensorMap& w, const CUtensorMap& x_rows, const Int8GemmArgs& args, int nmax,
-                              cudaStream_t stream);
+                              int num_sms, cudaStream_t stream);
 
 // int8_pair.cu: the same on 2-SM pairs.  Tensor maps: weights as above; token rows in 32-row boxes, or x codes in
 // one-row boxes (gather).

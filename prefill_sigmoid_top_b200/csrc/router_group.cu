@@ -7,8 +7,23 @@
 //   the topk_group groups with the largest s_g stay; of their experts the top_k with the largest keys, ties to
 //   the lower id;  w_k = p_k, or p_k / sum_j p_j, times routed_scale.
 //
-// The choice is a comparison of sums of rounded numbers, so it is defined in 64 bits: p, keys and group scores
-// in fp64.
+// The choice is a comparison of rounded numbers, so it is defined in fp64: p, keys and group scores.  fp64 arithmetic
+// is slow (a token of 256 experts: 20 us alone, and 168 us for 32767 tokens), so a token is first routed in fp32 with
+// a bound on what fp32 may be off by, and only where two candidates next to each other are nearer than that (or a
+// number is not finite, or far out) its warp computes it again in fp64.  The result is the fp64 one either way.
+//
+// fp32 path, one warp per token:
+//  1. logits in (coalesced, each read once), keys to shared memory.  Without a bias the key is the logit itself (the
+//     scores grow with it), so equal keys are equal logits and no bound is needed between different ones.
+//  2. group scores: 32 / n_group lanes (a power of two) scan each group's keys for the two largest.
+//  3. the kept groups' keys into registers, as integers that order like the numbers; top_k + 1 rounds of a warp
+//     maximum (redux) and the lowest id that has it.  The round past the last one shows the gap behind the choice.
+//  4. weights from the K logits.
+// Errors (ex2.approx and rcp are within 2 ulp; the scaled argument of the exponential adds |z| 2^-23.4 relative):
+//   sigmoid: |p32 - p| <= p (1 - p) (|z| 2^-23.4 + 2^-21.5) + p 2^-21 < 2^-20
+//   softmax: relative 2^-19 + |z - max| 2^-23, and p <= e^-|z - max| / denom: below 2^-18 / denom
+// plus 2^-24 of each sum that follows.  Two keys further apart than both errors are in the right order.
+// Bound: issue slots (about 400 instructions per token of 256 experts), not memory.
 #include "common.cuh"
 #include "kernels.h"
 
@@ -40,17 +55,13 @@ __device__ __forceinline__ double exp_score(double z, double zmax) {
   return exp(z - zmax);
 }
 
+// One token in fp64, whatever its logits hold: the definition, and the answer for the tokens that the fp32 path
+// leaves.  One warp; `key`: E doubles of shared memory.
 template <bool kBf16>
-__global__ void __launch_bounds__(32 * kWarps) route_group_kernel(const void* __restrict__ logits, int64_t ld,
-                                                                  const float* __restrict__ bias, int M, int E, int K,
-                                                                  RouteGroupOpts o, int32_t* __restrict__ topk_ids,
-                                                                  float* __restrict__ topk_w) {
-  extern __shared__ double keys_smem[];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int t = blockIdx.x * kWarps + warp;
-  if (t >= M) return;
-  double* key = keys_smem + warp * E;
-  const uint8_t* row = static_cast<const uint8_t*>(logits) + static_cast<size_t>(t) * ld * (kBf16 ? 2 : 4);
+__device__ __noinline__ void route_token_fp64(const void* row, const float* bias, int E, int K,
+                                              const RouteGroupOpts& o, double* key, int32_t* ids, float* w) {
+  const int lane = threadIdx.x & 31;
+  __syncwarp();
 
   double zmax = -INFINITY, denom = 1.0;
   if (o.scoring == MOE_SCORE_SOFTMAX) {
@@ -124,22 +135,245 @@ __global__ void __launch_bounds__(32 * kWarps) route_group_kernel(const void* __
   for (int off = 16; off >= 1; off >>= 1) total += shfl_xor_d(total, off);
   if (o.renormalize) p = total > 0.0 ? p / total : 0.0;
   if (lane < K) {
-    topk_ids[static_cast<size_t>(t) * K + lane] = sel;
-    topk_w[static_cast<size_t>(t) * K + lane] = static_cast<float>(p * static_cast<double>(o.routed_scale));
+    ids[lane] = sel;
+    w[lane] = static_cast<float>(p * static_cast<double>(o.routed_scale));
   }
+}
+
+// Integers that order like the numbers; 0 is below every finite one.
+__device__ __forceinline__ uint32_t order_bits(float v) {
+  const uint32_t b = __float_as_uint(v + 0.0f);  // -0 -> +0
+  return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
+}
+__device__ __forceinline__ float from_order_bits(uint32_t u) {
+  return __uint_as_float((u & 0x80000000u) ? (u & 0x7fffffffu) : ~u);
+}
+
+// kPer: candidates per lane, the kept groups' experts / 32 rounded up to a power of two.
+template <bool kBf16, int kPer>
+__global__ void __launch_bounds__(32 * kWarps) route_group_kernel(const void* __restrict__ logits, int64_t ld,
+                                                                  const float* __restrict__ bias, int M, int E, int K,
+                                                                  RouteGroupOpts o, int32_t* __restrict__ topk_ids,
+                                                                  float* __restrict__ topk_w) {
+  extern __shared__ double keys_smem[];
+  __shared__ uint8_t kept_groups[kWarps][32];  // the groups that stay, in order
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int t = blockIdx.x * kWarps + warp;
+  if (t >= M) return;
+  float* zs = reinterpret_cast<float*>(keys_smem + warp * E);  // logits [E]
+  float* key = zs + E;                                         // keys [E]
+  const uint8_t* row = static_cast<const uint8_t*>(logits) + static_cast<size_t>(t) * ld * (kBf16 ? 2 : 4);
+  int32_t* ids = topk_ids + static_cast<size_t>(t) * K;
+  float* w = topk_w + static_cast<size_t>(t) * K;
+  const bool softmax = o.scoring == MOE_SCORE_SOFTMAX;
+  const bool groups = o.topk_group < o.n_group;
+  const bool by_logit = bias == nullptr;
+  const bool group_sums = groups && o.group_score == MOE_GROUP_TOP2 && E > o.n_group;
+
+  // ---- 1. logits and keys
+  bool fine = true;
+  float zmax = -INFINITY;
+  for (int e0 = 0; e0 < E; e0 += 256) {  // eight loads in flight
+    float z[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int e = e0 + 32 * i + lane;
+      z[i] = e < E ? load_logit<kBf16>(row, e) : 0.0f;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int e = e0 + 32 * i + lane;
+      if (e < E) {
+        zs[e] = z[i];
+        fine = fine && fabsf(z[i]) < INFINITY;
+        zmax = fmaxf(zmax, z[i]);
+      }
+    }
+  }
+  if (softmax) zmax = from_order_bits(__reduce_max_sync(0xffffffffu, order_bits(zmax)));
+  float denom = 1.0f;
+  if (softmax && !(by_logit && !group_sums && o.renormalize)) {
+    denom = 0.0f;
+    for (int e = lane; e < E; e += 32) denom += expf(zs[e] - zmax);
+#pragma unroll
+    for (int off = 16; off >= 1; off >>= 1) denom += __shfl_xor_sync(0xffffffffu, denom, off);
+  }
+  const float inv_denom = 1.0f / denom;
+  auto score32 = [&](float z) {
+    return softmax ? __expf(z - zmax) * inv_denom : __fdividef(1.0f, 1.0f + __expf(-z));
+  };
+  float top_abs = 0.0f;
+  if (by_logit && !group_sums) {
+    key = zs;
+  } else {
+    for (int e = lane; e < E; e += 32) {
+      const float v = by_logit ? score32(zs[e]) : score32(zs[e]) + bias[e];
+      key[e] = v;
+      fine = fine && fabsf(v) < INFINITY;
+      top_abs = fmaxf(top_abs, fabsf(v));
+    }
+    top_abs = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top_abs)));
+  }
+  const float off_key = (softmax ? 0x1p-18f * inv_denom : 0x1p-20f) + top_abs * 0x1p-23f;  // of a key that holds a score
+  fine = __all_sync(0xffffffffu, fine);
+  __syncwarp();
+
+  // Two logits give scores that fp64 tells apart, in their order: they differ by more than 2^-30, and neither score
+  // is so near to 1 or to 0 that the difference is lost there.
+  auto logits_apart = [&](float hi, float lo) {
+    if (hi == lo) return true;  // the same score: the lower id, as found
+    if (!(hi - lo > 0x1p-30f)) return false;
+    return softmax ? lo - zmax > -600.0f : (hi < 12.0f && lo > -600.0f);
+  };
+
+  // ---- 2. groups
+  const int gs = E / o.n_group;
+  if (groups && fine) {
+    const int per_group = 1 << (31 - __clz(32 / o.n_group));  // lanes
+    const int g = lane / per_group, sub = lane % per_group;
+    float a = -INFINITY, b = -INFINITY;
+    if (g < o.n_group) {
+      const int turn = (g * per_group) % gs;  // each group starts elsewhere, so that the lanes read different banks
+      for (int i = sub; i < gs; i += per_group) {
+        const float v = key[g * gs + (i + turn < gs ? i + turn : i + turn - gs)];
+        b = fmaxf(b, fminf(a, v));
+        a = fmaxf(a, v);
+      }
+    }
+    for (int off = per_group >> 1; off >= 1; off >>= 1) {
+      const float oa = __shfl_xor_sync(0xffffffffu, a, off), ob = __shfl_xor_sync(0xffffffffu, b, off);
+      b = fmaxf(fminf(a, oa), fmaxf(b, ob));
+      a = fmaxf(a, oa);
+    }
+    // lane q: group q's score and its place among them
+    float s = group_sums ? a + b : a;
+    s = __shfl_sync(0xffffffffu, s, (lane * per_group) & 31);
+    int before = 0;
+    for (int q = 0; q < o.n_group; ++q) {
+      const float v = __shfl_sync(0xffffffffu, s, q);
+      before += v > s || (v == s && q < lane);
+    }
+    const bool mine = lane < o.n_group;
+    const bool stays = mine && before < o.topk_group;
+    const unsigned kept = __ballot_sync(0xffffffffu, stays);
+    if (stays) kept_groups[warp][__popc(kept & ((1u << lane) - 1u))] = static_cast<uint8_t>(lane);
+    __syncwarp();
+    // the last group that stays against the first that does not
+    const int last = __ffs(__ballot_sync(0xffffffffu, mine && before == o.topk_group - 1)) - 1;
+    const int next = __ffs(__ballot_sync(0xffffffffu, mine && before == o.topk_group)) - 1;
+    const float hi = __shfl_sync(0xffffffffu, s, last), lo = __shfl_sync(0xffffffffu, s, next);
+    if (by_logit && !group_sums)
+      fine = logits_apart(hi, lo);
+    else
+      fine = hi - lo > (group_sums ? 4.0f : 2.0f) * off_key + fabsf(hi) * 0x1p-22f;
+  }
+
+  // ---- 3. experts
+  int sel = 0;
+  float zsel = 0.0f;
+  if (fine) {
+    const float* order = by_logit ? zs : key;
+    const int ncand = o.topk_group * gs;
+    const float inv_gs = 1.0f / static_cast<float>(gs);
+    uint32_t u[kPer];
+    int id[kPer];
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int c = lane + 32 * i;
+      u[i] = 0;
+      id[i] = 0x7fffffff;
+      if (c < ncand) {
+        int e = c;
+        if (groups) {
+          // c / gs: (c + 1/2) / gs is at least 1/2048 from a whole number, the product off by 2^-13 at most
+          const int q = static_cast<int>((static_cast<float>(c) + 0.5f) * inv_gs);
+          e = kept_groups[warp][q] * gs + (c - q * gs);
+        }
+        id[i] = e;
+        u[i] = order_bits(order[e]);
+      }
+    }
+    uint32_t prev = 0;
+    int prev_id = 0;
+    const int rounds = min(K + 1, ncand);
+    for (int k = 0; k < rounds; ++k) {
+      uint32_t best = u[0];
+      int bid = id[0];
+#pragma unroll
+      for (int i = 1; i < kPer; ++i)
+        if (u[i] > best) {  // ids grow with i: the first of equal ones stays
+          best = u[i];
+          bid = id[i];
+        }
+      const uint32_t top = __reduce_max_sync(0xffffffffu, best);
+      const int win = static_cast<int>(__reduce_min_sync(0xffffffffu, best == top ? bid : 0x7fffffff));
+#pragma unroll
+      for (int i = 0; i < kPer; ++i)
+        if (id[i] == win) u[i] = 0;
+      if (lane == k) {
+        sel = win;
+        zsel = zs[win];
+      }
+      if (k > 0) {
+        const float hi = from_order_bits(prev), lo = from_order_bits(top);
+        if (by_logit)
+          fine = fine && logits_apart(hi, lo);
+        else
+          fine = fine && (hi - lo > 2.0f * off_key ||
+                          (prev == top && zs[prev_id] == zs[win] && bias[prev_id] == bias[win]));
+      }
+      prev = top;
+      prev_id = win;
+    }
+    // scores far below the fp32 range are the fp64 path's
+    const bool far = lane < K && (softmax ? zsel - zmax : zsel) < -80.0f;
+    fine = !__any_sync(0xffffffffu, far) && fine;
+  }
+  if (!fine) {
+    route_token_fp64<kBf16>(row, bias, E, K, o, reinterpret_cast<double*>(zs), ids, w);
+    return;
+  }
+
+  // ---- 4. weights
+  float p = 0.0f;
+  if (lane < K) p = softmax ? expf(zsel - zmax) : __fdiv_rn(1.0f, 1.0f + expf(-zsel));
+  float total = p;
+#pragma unroll
+  for (int off = 16; off >= 1; off >>= 1) total += __shfl_xor_sync(0xffffffffu, total, off);
+  if (lane < K) {
+    ids[lane] = sel;
+    w[lane] = __fdiv_rn(p, o.renormalize ? total : denom) * o.routed_scale;
+  }
+}
+
+template <bool kBf16>
+cudaError_t launch_typed(const void* logits, int64_t ld, const float* bias, int M, int E, int K,
+                         const RouteGroupOpts& o, int32_t* topk_ids, float* topk_w, cudaStream_t stream) {
+  const dim3 grid((M + kWarps - 1) / kWarps);
+  const size_t smem = sizeof(double) * kWarps * E;  // at most 32 KB
+  const int per = (o.topk_group * (E / o.n_group) + 31) / 32;
+  auto run = [&](auto kern) { kern<<<grid, 32 * kWarps, smem, stream>>>(logits, ld, bias, M, E, K, o, topk_ids, topk_w); };
+  if (per <= 1)
+    run(route_group_kernel<kBf16, 1>);
+  else if (per <= 2)
+    run(route_group_kernel<kBf16, 2>);
+  else if (per <= 4)
+    run(route_group_kernel<kBf16, 4>);
+  else if (per <= 8)
+    run(route_group_kernel<kBf16, 8>);
+  else if (per <= 16)
+    run(route_group_kernel<kBf16, 16>);
+  else
+    run(route_group_kernel<kBf16, 32>);
+  return cudaGetLastError();
 }
 
 }  // namespace
 
 cudaError_t launch_route_group(const void* logits, bool bf16, int64_t ld, const float* bias, int M, int E, int K,
                                const RouteGroupOpts& o, int32_t* topk_ids, float* topk_w, cudaStream_t stream) {
-  const dim3 grid((M + kWarps - 1) / kWarps);
-  const size_t smem = sizeof(double) * kWarps * E;  // at most 32 KB
-  if (bf16)
-    route_group_kernel<true><<<grid, 32 * kWarps, smem, stream>>>(logits, ld, bias, M, E, K, o, topk_ids, topk_w);
-  else
-    route_group_kernel<false><<<grid, 32 * kWarps, smem, stream>>>(logits, ld, bias, M, E, K, o, topk_ids, topk_w);
-  return cudaGetLastError();
+  return bf16 ? launch_typed<true>(logits, ld, bias, M, E, K, o, topk_ids, topk_w, stream)
+              : launch_typed<false>(logits, ld, bias, M, E, K, o, topk_ids, topk_w, stream);
 }
 
 }  // namespace moe
