@@ -8,8 +8,8 @@ cannot be loaded, every call raises.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
+import functools
 import os
 import threading
 from dataclasses import dataclass
@@ -249,28 +249,49 @@ def route_ex(x, w_router, bias, top_k, scoring=SCORE_SIGMOID, renormalize=True, 
     return topk_ids, topk_w
 
 
-def _same_device(*ts):
-    """All the given CUDA tensors lie on one device; makes it current for the rest of the call if it is not."""
-    _need_cuda(*ts)
-    dev = ts[0].device
-    for t in ts[1:]:
-        if t is not None and t.device != dev:
+def _device_of(*ts):
+    """The index of the one CUDA device that all the given tensors (None: absent) lie on."""
+    dev = ts[0].get_device()
+    for t in ts:
+        if t is not None and t.get_device() != dev:
             raise ValueError("tensors on different devices")
-    return _AS_IS if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
+    if dev < 0:
+        raise ValueError("moe_b200 operates on CUDA tensors only")
+    return dev
 
 
-_AS_IS = contextlib.nullcontext()
+def _launch(dev, what, *args):
+    """Calls the library's function on the current stream of device ``dev`` (made current for the call if it is
+    not): the stream is the last argument."""
+    fn = getattr(library(), what)
+    if dev == torch.cuda.current_device():
+        status = fn(*args, _raw_stream(dev))
+    else:
+        with torch.cuda.device(dev):
+            status = fn(*args, _raw_stream(dev))
+    if status != 0:
+        raise MoEError(status, what)
+
+
+def _raw_stream(dev):
+    return torch._C._cuda_getCurrentRawStream(dev)
+
+
+def _adr(t):
+    return None if t is None else t.data_ptr()
 
 
 def _want(t, dtype, shape, what):
-    if t is not None and (t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous()):
+    if t is not None and (t.dtype is not dtype or t.shape != shape or not t.is_contiguous()):
         raise ValueError(f"{what}: expected a contiguous {dtype} tensor of shape {tuple(shape)}")
     return t
 
 
+@functools.lru_cache(maxsize=256)
 def _group_opts(n_group, topk_group, group_score, scoring, renormalize, routed_scale):
-    return _GroupOpts(int(scoring), int(bool(renormalize)), int(n_group), int(topk_group), int(group_score),
-                      float(routed_scale))
+    """The options as the library takes them (it only reads them): built once for each setting."""
+    return ctypes.byref(_GroupOpts(int(scoring), int(bool(renormalize)), int(n_group), int(topk_group),
+                                   int(group_score), float(routed_scale)))
 
 
 def route_logits(logits, bias, top_k, n_group=1, topk_group=1, group_score=GROUP_TOP2, scoring=SCORE_SIGMOID,
@@ -281,13 +302,12 @@ def route_logits(logits, bias, top_k, n_group=1, topk_group=1, group_score=GROUP
     if logits.dim() != 2 or logits.dtype not in _DTYPES or (logits.shape[1] > 1 and logits.stride(1) != 1):
         raise ValueError("logits: expected an fp32 or bf16 [M, E] tensor with contiguous rows")
     M, E = logits.shape
-    with _same_device(logits, bias, topk_ids, topk_w):
-        _want(bias, torch.float32, (E,), "bias")
-        topk_ids, topk_w = _routing_out(M, top_k, logits.device, topk_ids, topk_w)
-        opts = _group_opts(n_group, topk_group, group_score, scoring, renormalize, routed_scale)
-        _check(library().moe_route_logits(_ptr(logits), _DTYPES[logits.dtype], _row_stride(logits), _ptr(bias), M, E,
-                                          int(top_k), ctypes.byref(opts), _ptr(topk_ids), _ptr(topk_w), _stream()),
-               "moe_route_logits")
+    dev = _device_of(logits, bias, topk_ids, topk_w)
+    _want(bias, torch.float32, (E,), "bias")
+    topk_ids, topk_w = _routing_out(M, top_k, logits, topk_ids, topk_w)
+    opts = _group_opts(n_group, topk_group, group_score, scoring, renormalize, routed_scale)
+    _launch(dev, "moe_route_logits", logits.data_ptr(), _DTYPES[logits.dtype], _row_stride(logits), _adr(bias), M, E,
+            top_k, opts, topk_ids.data_ptr(), topk_w.data_ptr())
     return topk_ids, topk_w
 
 
@@ -297,16 +317,15 @@ def route_group(x, w_router, bias, top_k, n_group=1, topk_group=1, group_score=G
     M, H = x.shape
     E = w_router.shape[0]
     shape = Shape(M, H, 128, E, top_k, 16)
-    with _same_device(x, w_router, bias, topk_ids, topk_w, ws):
-        _want(w_router, torch.bfloat16, (E, H), "w_router")
-        _want(bias, torch.float32, (E,), "bias")
-        topk_ids, topk_w = _routing_out(M, top_k, x.device, topk_ids, topk_w)
-        if ws is None:
-            ws = torch.empty(max(route_workspace_size(shape), 1), dtype=torch.uint8, device=x.device)
-        opts = _group_opts(n_group, topk_group, group_score, scoring, renormalize, routed_scale)
-        _check(library().moe_route_group(_ptr(_bf16(x)), _ptr(w_router), _ptr(bias), shape.c(), ctypes.byref(opts),
-                                         _ptr(topk_ids), _ptr(topk_w), _ptr(ws), ws.numel(), _stream()),
-               "moe_route_group")
+    dev = _device_of(x, w_router, bias, topk_ids, topk_w, ws)
+    _want(w_router, torch.bfloat16, (E, H), "w_router")
+    _want(bias, torch.float32, (E,), "bias")
+    topk_ids, topk_w = _routing_out(M, top_k, x, topk_ids, topk_w)
+    if ws is None:
+        ws = x.new_empty(max(route_workspace_size(shape), 1), dtype=torch.uint8)
+    opts = _group_opts(n_group, topk_group, group_score, scoring, renormalize, routed_scale)
+    _launch(dev, "moe_route_group", _bf16(x).data_ptr(), w_router.data_ptr(), _adr(bias), shape.c(), opts,
+            topk_ids.data_ptr(), topk_w.data_ptr(), ws.data_ptr(), ws.numel())
     return topk_ids, topk_w
 
 
@@ -315,11 +334,11 @@ def _row_stride(t):
     return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
 
 
-def _routing_out(M, top_k, device, topk_ids, topk_w):
+def _routing_out(M, top_k, like, topk_ids, topk_w):
     if topk_ids is None:
-        topk_ids = torch.empty(M, top_k, dtype=torch.int32, device=device)
+        topk_ids = like.new_empty((M, top_k), dtype=torch.int32)
     if topk_w is None:
-        topk_w = torch.empty(M, top_k, dtype=torch.float32, device=device)
+        topk_w = like.new_empty((M, top_k), dtype=torch.float32)
     return _want(topk_ids, torch.int32, (M, top_k), "topk_ids"), _want(topk_w, torch.float32, (M, top_k), "topk_w")
 
 
@@ -581,15 +600,14 @@ def quantize_int8(w):
     """w bf16 [..., cols] -> (codes int8 of the same shape, scales fp32 [...]): code = rint(127 v / amax of the
     row), scale = amax / 127.  The codes' rows lie a multiple of 16 bytes apart (a view of a wider buffer where
     cols is not one), as linear_int8 takes them."""
-    with _same_device(w):
-        cols = w.shape[-1]
-        _want(w, torch.bfloat16, w.shape, "w")
-        rows = w.numel() // cols if cols else 0
-        pitch = (cols + 15) // 16 * 16
-        buf = torch.empty(*w.shape[:-1], pitch, dtype=torch.int8, device=w.device)
-        scales = torch.empty(w.shape[:-1], dtype=torch.float32, device=w.device)
-        _check(library().moe_quantize_int8(_ptr(w), cols, rows, cols, _ptr(buf), pitch, _ptr(scales), _stream()),
-               "moe_quantize_int8")
+    dev = _device_of(w)
+    cols = w.shape[-1]
+    _want(w, torch.bfloat16, w.shape, "w")
+    rows = w.numel() // cols if cols else 0
+    pitch = (cols + 15) // 16 * 16
+    buf = w.new_empty((*w.shape[:-1], pitch), dtype=torch.int8)
+    scales = w.new_empty(w.shape[:-1], dtype=torch.float32)
+    _launch(dev, "moe_quantize_int8", w.data_ptr(), cols, rows, cols, buf.data_ptr(), pitch, scales.data_ptr())
     return buf[..., :cols], scales
 
 
@@ -599,6 +617,7 @@ def int8_weights(w_gate, w_up, w_down) -> Int8Weights:
     return Int8Weights(g, u, d, gs, us, ds)
 
 
+@functools.lru_cache(maxsize=256)
 def linear_int8_workspace_size(M: int, N: int, K: int) -> int:
     return int(library().moe_linear_int8_workspace_size(M, N, K))
 
@@ -606,56 +625,52 @@ def linear_int8_workspace_size(M: int, N: int, K: int) -> int:
 def linear_int8(x, codes, scales, out=None, out_dtype=torch.bfloat16, ws=None, err_flag=None):
     """out[M,N] = x . W^T with W given as 8-bit codes [N,K] (rows a multiple of 16 bytes apart) and channel
     scales [N]; x bf16 [M,K] (rows may be strided) is quantised per row on the fly.  out: bf16 or fp32."""
-    if x.dim() != 2 or x.dtype != torch.bfloat16 or (x.shape[1] > 1 and x.stride(1) != 1):
+    if x.dim() != 2 or x.dtype is not torch.bfloat16 or (x.shape[1] > 1 and x.stride(1) != 1):
         raise ValueError("x: expected a bf16 [M, K] tensor with contiguous rows")
     M, K = x.shape
     N = codes.shape[0]
-    if codes.dtype != torch.int8 or tuple(codes.shape) != (N, K) or (K > 1 and codes.stride(1) != 1):
+    if codes.dtype is not torch.int8 or codes.shape != (N, K) or (K > 1 and codes.stride(1) != 1):
         raise ValueError("codes: expected an int8 [N, K] tensor with contiguous rows")
-    with _same_device(x, codes, scales, out, ws, err_flag):
-        _want(scales, torch.float32, (N,), "scales")
-        if out is None:
-            out = torch.empty(M, N, dtype=out_dtype, device=x.device)
-        elif out.dtype not in _DTYPES or tuple(out.shape) != (M, N) or (N > 1 and out.stride(1) != 1):
-            raise ValueError("out: expected a bf16 or fp32 [M, N] tensor with contiguous rows")
-        if out.dtype not in _DTYPES:
+    dev = _device_of(x, codes, scales, out, ws, err_flag)
+    _want(scales, torch.float32, (N,), "scales")
+    if out is None:
+        if out_dtype not in _DTYPES:
             raise ValueError("out_dtype: expected torch.bfloat16 or torch.float32")
-        ldw = codes.stride(0) if N > 1 else (max(codes.stride(0), K) + 15) // 16 * 16
-        if ws is None:
-            ws = torch.empty(max(linear_int8_workspace_size(M, N, K), 1), dtype=torch.uint8, device=x.device)
-        _check(library().moe_linear_int8(_ptr(x), _row_stride(x), _ptr(codes), ldw, _ptr(scales), M, N, K, _ptr(out),
-                                         _row_stride(out), _DTYPES[out.dtype], _ptr(ws), ws.numel(), _ptr(err_flag),
-                                         _stream()), "moe_linear_int8")
+        out = x.new_empty((M, N), dtype=out_dtype)
+    elif out.dtype not in _DTYPES or out.shape != (M, N) or (N > 1 and out.stride(1) != 1):
+        raise ValueError("out: expected a bf16 or fp32 [M, N] tensor with contiguous rows")
+    ldw = codes.stride(0) if N > 1 else (max(codes.stride(0), K) + 15) // 16 * 16
+    if ws is None:
+        ws = x.new_empty(max(linear_int8_workspace_size(M, N, K), 1), dtype=torch.uint8)
+    _launch(dev, "moe_linear_int8", x.data_ptr(), _row_stride(x), codes.data_ptr(), ldw, scales.data_ptr(), M, N, K,
+            out.data_ptr(), _row_stride(out), _DTYPES[out.dtype], ws.data_ptr(), ws.numel(), _adr(err_flag))
     return out
 
 
 def grouped_up_swiglu_int8(x, iw: Int8Weights, plan, shape: Shape, h=None, err_flag=None, ws=None):
     """int8 form of grouped_up_swiglu (every token's x quantised on the fly into ws)."""
     ts = iw.check(shape, "gate", "up")
-    with _same_device(x, *ts, plan["sorted_ids"], h, err_flag, ws):
-        _want(x, torch.bfloat16, (shape.M, shape.H), "x")
-        if h is None:
-            h = torch.empty(align_capacity(shape), shape.I, dtype=torch.bfloat16, device=x.device)
-        if ws is None:
-            ws = torch.empty(max(up_workspace_size(shape, MOE_W_INT8), 1), dtype=torch.uint8, device=x.device)
-        w, p = iw.c(), _plan_struct(plan)
-        _check(library().moe_grouped_up_swiglu(_ptr(x), ctypes.byref(w), ctypes.byref(p), shape.c(), _ptr(_bf16(h)),
-                                               _ptr(ws), ws.numel(), _ptr(err_flag), _stream()),
-               "moe_grouped_up_swiglu")
+    dev = _device_of(x, *ts, plan["sorted_ids"], h, err_flag, ws)
+    _want(x, torch.bfloat16, (shape.M, shape.H), "x")
+    if h is None:
+        h = x.new_empty((align_capacity(shape), shape.I))
+    if ws is None:
+        ws = x.new_empty(max(up_workspace_size(shape, MOE_W_INT8), 1), dtype=torch.uint8)
+    _launch(dev, "moe_grouped_up_swiglu", x.data_ptr(), ctypes.byref(iw.c()), ctypes.byref(_plan_struct(plan)),
+            shape.c(), _bf16(h).data_ptr(), ws.data_ptr(), ws.numel(), _adr(err_flag))
     return h
 
 
 def grouped_down_int8(h, iw: Int8Weights, plan, shape: Shape, y=None, err_flag=None, ws=None):
     """int8 form of grouped_down (the real plan rows of h quantised on the fly into ws)."""
     ts = iw.check(shape, "down")
-    with _same_device(h, *ts, plan["sorted_ids"], y, err_flag, ws):
-        if y is None:
-            y = torch.empty(shape.M * shape.top_k, shape.H, dtype=torch.bfloat16, device=h.device)
-        if ws is None:
-            ws = torch.empty(max(down_workspace_size(shape, MOE_W_INT8), 1), dtype=torch.uint8, device=h.device)
-        w, p = iw.c(), _plan_struct(plan)
-        _check(library().moe_grouped_down(_ptr(_bf16(h)), ctypes.byref(w), ctypes.byref(p), shape.c(), _ptr(_bf16(y)),
-                                          _ptr(ws), ws.numel(), _ptr(err_flag), _stream()), "moe_grouped_down")
+    dev = _device_of(h, *ts, plan["sorted_ids"], y, err_flag, ws)
+    if y is None:
+        y = h.new_empty((shape.M * shape.top_k, shape.H))
+    if ws is None:
+        ws = h.new_empty(max(down_workspace_size(shape, MOE_W_INT8), 1), dtype=torch.uint8)
+    _launch(dev, "moe_grouped_down", _bf16(h).data_ptr(), ctypes.byref(iw.c()), ctypes.byref(_plan_struct(plan)),
+            shape.c(), _bf16(y).data_ptr(), ws.data_ptr(), ws.numel(), _adr(err_flag))
     return y
 
 
@@ -668,15 +683,14 @@ def layer_int8(x, w_router, bias, iw: Int8Weights, gamma, eps, top_k, block_size
     E, I = iw.gate.shape[0], iw.gate.shape[1]
     shape = Shape(M, H, I, E, top_k, block_size)
     ts = iw.check(shape, "gate", "up", "down")
-    with _same_device(x, w_router, bias, *ts, gamma, ws, out, residual_out, topk_ids, topk_w):
-        if ws is None:
-            ws = torch.empty(max(layer_workspace_size(shape, MOE_W_INT8), 1), dtype=torch.uint8, device=x.device)
-        if out is None:
-            out = torch.empty_like(x)
-        w = iw.c()
-        _check(library().moe_layer(_ptr(_bf16(x)), _ptr(_bf16(w_router)), _ptr(bias), ctypes.byref(w),
-                                   _ptr(_bf16(gamma)), float(eps), shape.c(), _ptr(out), _ptr(residual_out),
-                                   _ptr(topk_ids), _ptr(topk_w), _ptr(ws), ws.numel(), _stream()), "moe_layer")
+    dev = _device_of(x, w_router, bias, *ts, gamma, ws, out, residual_out, topk_ids, topk_w)
+    if ws is None:
+        ws = x.new_empty(max(layer_workspace_size(shape, MOE_W_INT8), 1), dtype=torch.uint8)
+    if out is None:
+        out = torch.empty_like(x)
+    _launch(dev, "moe_layer", _bf16(x).data_ptr(), _bf16(w_router).data_ptr(), _adr(bias), ctypes.byref(iw.c()),
+            _bf16(gamma).data_ptr(), float(eps), shape.c(), out.data_ptr(), _adr(residual_out), _adr(topk_ids),
+            _adr(topk_w), ws.data_ptr(), ws.numel())
     return out
 
 

@@ -38,13 +38,27 @@ __device__ __forceinline__ double shfl_xor_d(double v, int off) { return __shfl_
 __device__ __forceinline__ double rank_key(double v) { return isnan(v) ? -INFINITY : v; }
 
 template <bool kBf16>
+__device__ __forceinline__ float raw_logit(const void* row, int e) {
+  if (kBf16) return __uint_as_float(static_cast<uint32_t>(static_cast<const uint16_t*>(row)[e]) << 16);
+  return static_cast<const float*>(row)[e];
+}
+
+template <bool kBf16>
 __device__ __forceinline__ float load_logit(const void* row, int e) {
-  float z;
-  if (kBf16)
-    z = __uint_as_float(static_cast<uint32_t>(static_cast<const uint16_t*>(row)[e]) << 16);
-  else
-    z = static_cast<const float*>(row)[e];
+  const float z = raw_logit<kBf16>(row, e);
   return isnan(z) ? -INFINITY : z;
+}
+
+// The hardware's base-2 exponential and reciprocal, results below 2^-126 flushed to 0 (within the bound of 2^-20).
+__device__ __forceinline__ float exp2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float rcp_approx(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
 
 // e^(z - zmax) with the limits: a row whose largest logit is +inf shares among its +inf entries, a row of
@@ -171,25 +185,21 @@ __global__ void __launch_bounds__(32 * kWarps) route_group_kernel(const void* __
   const bool group_sums = groups && o.group_score == MOE_GROUP_TOP2 && E > o.n_group;
 
   // ---- 1. logits and keys
-  bool fine = true;
+  uint32_t zbits = 0;  // largest |z| as bits: from 0x7f800000 on a logit is not finite
   float zmax = -INFINITY;
-  for (int e0 = 0; e0 < E; e0 += 256) {  // eight loads in flight
+  for (int e0 = lane; e0 < E; e0 += 256) {  // eight loads in flight
     float z[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int e = e0 + 32 * i + lane;
-      z[i] = e < E ? load_logit<kBf16>(row, e) : 0.0f;
-    }
+    for (int i = 0; i < 8; ++i) z[i] = e0 + 32 * i < E ? raw_logit<kBf16>(row, e0 + 32 * i) : 0.0f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const int e = e0 + 32 * i + lane;
-      if (e < E) {
-        zs[e] = z[i];
-        fine = fine && fabsf(z[i]) < INFINITY;
-        zmax = fmaxf(zmax, z[i]);
-      }
+      if (e0 + 32 * i >= E) break;
+      zs[e0 + 32 * i] = z[i];
+      zbits = max(zbits, __float_as_uint(z[i]) & 0x7fffffffu);
+      zmax = fmaxf(zmax, z[i]);
     }
   }
+  uint32_t kbits = 0;
   if (softmax) zmax = from_order_bits(__reduce_max_sync(0xffffffffu, order_bits(zmax)));
   float denom = 1.0f;
   if (softmax && !(by_logit && !group_sums && o.renormalize)) {
@@ -200,22 +210,23 @@ __global__ void __launch_bounds__(32 * kWarps) route_group_kernel(const void* __
   }
   const float inv_denom = 1.0f / denom;
   auto score32 = [&](float z) {
-    return softmax ? __expf(z - zmax) * inv_denom : __fdividef(1.0f, 1.0f + __expf(-z));
+    constexpr float kLog2e = 1.4426950408889634f;
+    return softmax ? exp2_approx((z - zmax) * kLog2e) * inv_denom : rcp_approx(1.0f + exp2_approx(-z * kLog2e));
   };
-  float top_abs = 0.0f;
   if (by_logit && !group_sums) {
     key = zs;
   } else {
+#pragma unroll 4
     for (int e = lane; e < E; e += 32) {
       const float v = by_logit ? score32(zs[e]) : score32(zs[e]) + bias[e];
       key[e] = v;
-      fine = fine && fabsf(v) < INFINITY;
-      top_abs = fmaxf(top_abs, fabsf(v));
+      kbits = max(kbits, __float_as_uint(v) & 0x7fffffffu);
     }
-    top_abs = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top_abs)));
+    kbits = __reduce_max_sync(0xffffffffu, kbits);
   }
-  const float off_key = (softmax ? 0x1p-18f * inv_denom : 0x1p-20f) + top_abs * 0x1p-23f;  // of a key that holds a score
-  fine = __all_sync(0xffffffffu, fine);
+  // what a key that holds a score may be off by
+  const float off_key = (softmax ? 0x1p-18f * inv_denom : 0x1p-20f) + __uint_as_float(kbits) * 0x1p-23f;
+  bool fine = __reduce_max_sync(0xffffffffu, zbits) < 0x7f800000u && kbits < 0x7f800000u;
   __syncwarp();
 
   // Two logits give scores that fp64 tells apart, in their order: they differ by more than 2^-30, and neither score
@@ -234,6 +245,7 @@ __global__ void __launch_bounds__(32 * kWarps) route_group_kernel(const void* __
     float a = -INFINITY, b = -INFINITY;
     if (g < o.n_group) {
       const int turn = (g * per_group) % gs;  // each group starts elsewhere, so that the lanes read different banks
+#pragma unroll 4
       for (int i = sub; i < gs; i += per_group) {
         const float v = key[g * gs + (i + turn < gs ? i + turn : i + turn - gs)];
         b = fmaxf(b, fminf(a, v));
@@ -293,41 +305,73 @@ __global__ void __launch_bounds__(32 * kWarps) route_group_kernel(const void* __
         u[i] = order_bits(order[e]);
       }
     }
-    uint32_t prev = 0;
-    int prev_id = 0;
+    if (kPer <= 4) {
+      // each lane's candidates in descending order (neighbours change places only if the later one is larger, so
+      // equal ones keep the lower id first): a round takes a lane's first and moves the others up
+#pragma unroll
+      for (int i = 1; i < kPer; ++i)
+#pragma unroll
+        for (int l = i; l >= 1; --l) {
+          const bool swap = u[l] > u[l - 1];
+          const uint32_t hi_u = swap ? u[l] : u[l - 1], lo_u = swap ? u[l - 1] : u[l];
+          const int hi_id = swap ? id[l] : id[l - 1], lo_id = swap ? id[l - 1] : id[l];
+          u[l - 1] = hi_u;
+          u[l] = lo_u;
+          id[l - 1] = hi_id;
+          id[l] = lo_id;
+        }
+    }
+    uint32_t mine = 0, top = 0;  // the key of round `lane`; of the last round
     const int rounds = min(K + 1, ncand);
     for (int k = 0; k < rounds; ++k) {
       uint32_t best = u[0];
       int bid = id[0];
+      if (kPer > 4) {
 #pragma unroll
-      for (int i = 1; i < kPer; ++i)
-        if (u[i] > best) {  // ids grow with i: the first of equal ones stays
-          best = u[i];
-          bid = id[i];
-        }
-      const uint32_t top = __reduce_max_sync(0xffffffffu, best);
+        for (int i = 1; i < kPer; ++i)
+          if (u[i] > best) {  // ids grow with i: the first of equal ones stays
+            best = u[i];
+            bid = id[i];
+          }
+      }
+      top = __reduce_max_sync(0xffffffffu, best);
       const int win = static_cast<int>(__reduce_min_sync(0xffffffffu, best == top ? bid : 0x7fffffff));
+      if (kPer > 4) {
 #pragma unroll
-      for (int i = 0; i < kPer; ++i)
-        if (id[i] == win) u[i] = 0;
+        for (int i = 0; i < kPer; ++i)
+          if (id[i] == win) u[i] = 0;
+      } else if (bid == win) {
+#pragma unroll
+        for (int i = 1; i < kPer; ++i) {
+          u[i - 1] = u[i];
+          id[i - 1] = id[i];
+        }
+        u[kPer - 1] = 0;
+        id[kPer - 1] = 0x7fffffff;
+      }
       if (lane == k) {
+        mine = top;
         sel = win;
-        zsel = zs[win];
       }
-      if (k > 0) {
-        const float hi = from_order_bits(prev), lo = from_order_bits(top);
-        if (by_logit)
-          fine = fine && logits_apart(hi, lo);
-        else
-          fine = fine && (hi - lo > 2.0f * off_key ||
-                          (prev == top && zs[prev_id] == zs[win] && bias[prev_id] == bias[win]));
-      }
-      prev = top;
-      prev_id = win;
     }
-    // scores far below the fp32 range are the fp64 path's
-    const bool far = lane < K && (softmax ? zsel - zmax : zsel) < -80.0f;
-    fine = !__any_sync(0xffffffffu, far) && fine;
+    // every choice against the next one: lane k compares rounds k and k + 1 (round 32 is in no lane)
+    const uint32_t after = __shfl_down_sync(0xffffffffu, mine, 1);
+    const int after_id = __shfl_down_sync(0xffffffffu, sel, 1);
+    bool good = true;
+    if (lane + 1 < rounds) {
+      const float hi = from_order_bits(mine), lo = from_order_bits(lane < 31 ? after : top);
+      if (by_logit)
+        good = logits_apart(hi, lo);
+      else
+        good = hi - lo > 2.0f * off_key ||
+               (lane < 31 && hi == lo && zs[sel] == zs[after_id] && bias[sel] == bias[after_id]);
+    }
+    if (lane < K) {
+      zsel = zs[sel];
+      // scores far below the fp32 range are the fp64 path's
+      good = good && !((softmax ? zsel - zmax : zsel) < -80.0f);
+    }
+    fine = __all_sync(0xffffffffu, good);
   }
   if (!fine) {
     route_token_fp64<kBf16>(row, bias, E, K, o, reinterpret_cast<double*>(zs), ids, w);
