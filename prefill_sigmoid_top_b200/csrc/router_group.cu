@@ -12,18 +12,23 @@
 // a bound on what fp32 may be off by, and only where two candidates next to each other are nearer than that (or a
 // number is not finite, or far out) its warp computes it again in fp64.  The result is the fp64 one either way.
 //
-// fp32 path, one warp per token:
-//  1. logits in (coalesced, each read once), keys to shared memory.  Without a bias the key is the logit itself (the
-//     scores grow with it), so equal keys are equal logits and no bound is needed between different ones.
-//  2. group scores: 32 / n_group lanes (a power of two) scan each group's keys for the two largest.
-//  3. the kept groups' keys into registers, as integers that order like the numbers; top_k + 1 rounds of a warp
-//     maximum (redux) and the lowest id that has it.  The round past the last one shows the gap behind the choice.
+// fp32 path, one warp per token, no shared memory:
+//  1. 32 / n_group lanes (a power of two) hold a group, each up to kPer neighbouring experts in registers (16-byte
+//     loads where rows allow).  Without a bias the key is the logit itself (the scores grow with it).
+//  2. group scores: the two largest keys of each lane, joined over the group's lanes by shuffles.
+//  3. the kept groups' keys become integers (22 or 23 bits of the distance from the smallest key, in steps of
+//     range / 2^b), with the inverted expert id below: all different, larger key first, lower id first.  Up to 8 per
+//     lane are sorted once (Batcher's network, a minimum and a maximum per exchange); then top_k + 1 rounds of ONE
+//     warp maximum (redux): the owner moves its list up.  The round past the last shows the gap behind the choice.
 //  4. weights from the K logits.
-// Errors (ex2.approx and rcp are within 2 ulp; the scaled argument of the exponential adds |z| 2^-23.4 relative):
-//   sigmoid: |p32 - p| <= p (1 - p) (|z| 2^-23.4 + 2^-21.5) + p 2^-21 < 2^-20
+// Two keys are in the right order where their integers are 3 or more apart (an integer is off by less than 3/4 of a
+// step) and that distance exceeds what the keys may be off by:
+//   sigmoid: |p32 - p| <= p (1 - p) (|z| 2^-23.4 + 2^-21.5) + p 2^-21 < 2^-20 (ex2.approx and rcp.approx are within
+//            2 ulp; the scaled argument of the exponential adds |z| 2^-23.4 relative)
 //   softmax: relative 2^-19 + |z - max| 2^-23, and p <= e^-|z - max| / denom: below 2^-18 / denom
-// plus 2^-24 of each sum that follows.  Two keys further apart than both errors are in the right order.
-// Bound: issue slots (about 400 instructions per token of 256 experts), not memory.
+// plus 2^-24 of each sum that follows.  Of bf16 logits, two that are nearer than their spacing are equal: a tie.
+// Bound: issue slots, not memory.  Measured, 32767 tokens x 256 experts, 8 groups, K = 8: two warp reductions on (key,
+// id) pairs out of shared memory 50 us.
 #include "common.cuh"
 #include "kernels.h"
 
@@ -163,218 +168,223 @@ __device__ __forceinline__ float from_order_bits(uint32_t u) {
   return __uint_as_float((u & 0x80000000u) ? (u & 0x7fffffffu) : ~u);
 }
 
-// kPer: candidates per lane, the kept groups' experts / 32 rounded up to a power of two.
+// Descending order by Batcher's odd-even merge network (n a power of two).
+template <int kN>
+__device__ __forceinline__ void sort_descending(uint32_t (&v)[kN]) {
+#pragma unroll
+  for (int p = 1; p < kN; p <<= 1)
+#pragma unroll
+    for (int k = p; k >= 1; k >>= 1)
+#pragma unroll
+      for (int j = k % p; j + k < kN; j += 2 * k)
+#pragma unroll
+        for (int i = 0; i < k; ++i)
+          if (i + j + k < kN && (i + j) / (2 * p) == (i + j + k) / (2 * p)) {
+            const uint32_t a = v[i + j], b = v[i + j + k];
+            v[i + j] = max(a, b);
+            v[i + j + k] = min(a, b);
+          }
+}
+
+// kPer: experts per lane, rounded up to a power of two.
 template <bool kBf16, int kPer>
 __global__ void __launch_bounds__(32 * kWarps) route_group_kernel(const void* __restrict__ logits, int64_t ld,
                                                                   const float* __restrict__ bias, int M, int E, int K,
                                                                   RouteGroupOpts o, int32_t* __restrict__ topk_ids,
                                                                   float* __restrict__ topk_w) {
-  extern __shared__ double keys_smem[];
-  __shared__ uint8_t kept_groups[kWarps][32];  // the groups that stay, in order
+  extern __shared__ double keys_smem[];  // the fp64 path's
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int t = blockIdx.x * kWarps + warp;
   if (t >= M) return;
-  float* zs = reinterpret_cast<float*>(keys_smem + warp * E);  // logits [E]
-  float* key = zs + E;                                         // keys [E]
   const uint8_t* row = static_cast<const uint8_t*>(logits) + static_cast<size_t>(t) * ld * (kBf16 ? 2 : 4);
   int32_t* ids = topk_ids + static_cast<size_t>(t) * K;
   float* w = topk_w + static_cast<size_t>(t) * K;
   const bool softmax = o.scoring == MOE_SCORE_SOFTMAX;
   const bool groups = o.topk_group < o.n_group;
   const bool by_logit = bias == nullptr;
-  const bool group_sums = groups && o.group_score == MOE_GROUP_TOP2 && E > o.n_group;
+  const int gs = E / o.n_group;
+  const bool group_sums = groups && o.group_score == MOE_GROUP_TOP2 && gs > 1;
 
-  // ---- 1. logits and keys
-  uint32_t zbits = 0;  // largest |z| as bits: from 0x7f800000 on a logit is not finite
-  float zmax = -INFINITY;
-  for (int e0 = lane; e0 < E; e0 += 256) {  // eight loads in flight
-    float z[8];
+  // ---- 1. this lane's experts and their keys
+  const int lanes_log = 31 - __clz(32 / o.n_group);  // lanes per group
+  const int group = lane >> lanes_log;
+  const int chunk = (gs + (1 << lanes_log) - 1) >> lanes_log;  // <= kPer
+  const int from = (lane & ((1 << lanes_log) - 1)) * chunk;
+  const int n = group < o.n_group ? max(0, min(chunk, gs - from)) : 0;
+  const int e0 = n > 0 ? group * gs + from : 0;
+  float v[kPer];
+  constexpr int kVec = kBf16 ? 8 : 4;  // logits per 16 bytes
+  const bool vectors = kPer >= kVec && chunk == kPer && gs == chunk << lanes_log && group < o.n_group &&
+                       (reinterpret_cast<uintptr_t>(row + static_cast<size_t>(e0) * (kBf16 ? 2 : 4)) & 15u) == 0;
+  if (vectors) {
+    const uint4* src = reinterpret_cast<const uint4*>(row + static_cast<size_t>(e0) * (kBf16 ? 2 : 4));
 #pragma unroll
-    for (int i = 0; i < 8; ++i) z[i] = e0 + 32 * i < E ? raw_logit<kBf16>(row, e0 + 32 * i) : 0.0f;
+    for (int i = 0; i < kPer / kVec; ++i) {
+      const uint4 q = src[i];
+      const uint32_t x[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      if (e0 + 32 * i >= E) break;
-      zs[e0 + 32 * i] = z[i];
-      zbits = max(zbits, __float_as_uint(z[i]) & 0x7fffffffu);
-      zmax = fmaxf(zmax, z[i]);
+      for (int u = 0; u < 4; ++u) {
+        if (kBf16) {
+          v[(8 * i + 2 * u) % kPer] = bf16_lo(x[u]);
+          v[(8 * i + 2 * u + 1) % kPer] = bf16_hi(x[u]);
+        } else {
+          v[(4 * i + u) % kPer] = __uint_as_float(x[u]);
+        }
+      }
     }
-  }
-  uint32_t kbits = 0;
-  if (softmax) zmax = from_order_bits(__reduce_max_sync(0xffffffffu, order_bits(zmax)));
-  float denom = 1.0f;
-  if (softmax && !(by_logit && !group_sums && o.renormalize)) {
-    denom = 0.0f;
-    for (int e = lane; e < E; e += 32) denom += expf(zs[e] - zmax);
+  } else {
 #pragma unroll
-    for (int off = 16; off >= 1; off >>= 1) denom += __shfl_xor_sync(0xffffffffu, denom, off);
+    for (int i = 0; i < kPer; ++i) v[i] = i < n ? raw_logit<kBf16>(row, e0 + i) : 0.0f;
+  }
+  uint32_t zbits = 0;  // largest |z| as bits: from 0x7f800000 on a logit is not finite
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) zbits = max(zbits, __float_as_uint(v[i]) & 0x7fffffffu);
+  bool fine = __reduce_max_sync(0xffffffffu, zbits) < 0x7f800000u;
+  float zmax = 0.0f, denom = 1.0f;
+  if (softmax) {
+    zmax = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i)
+      if (i < n) zmax = fmaxf(zmax, v[i]);
+    zmax = from_order_bits(__reduce_max_sync(0xffffffffu, order_bits(zmax)));
+    if (!by_logit || group_sums || !o.renormalize) {
+      denom = 0.0f;
+#pragma unroll
+      for (int i = 0; i < kPer; ++i)
+        if (i < n) denom += expf(v[i] - zmax);
+#pragma unroll
+      for (int off = 16; off >= 1; off >>= 1) denom += __shfl_xor_sync(0xffffffffu, denom, off);
+    }
   }
   const float inv_denom = 1.0f / denom;
   auto score32 = [&](float z) {
     constexpr float kLog2e = 1.4426950408889634f;
     return softmax ? exp2_approx((z - zmax) * kLog2e) * inv_denom : rcp_approx(1.0f + exp2_approx(-z * kLog2e));
   };
-  if (by_logit && !group_sums) {
-    key = zs;
-  } else {
-#pragma unroll 4
-    for (int e = lane; e < E; e += 32) {
-      const float v = by_logit ? score32(zs[e]) : score32(zs[e]) + bias[e];
-      key[e] = v;
-      kbits = max(kbits, __float_as_uint(v) & 0x7fffffffu);
-    }
-    kbits = __reduce_max_sync(0xffffffffu, kbits);
+  if (!by_logit) {
+#pragma unroll
+    for (int i = 0; i < kPer; ++i)
+      if (i < n) v[i] = score32(v[i]) + bias[e0 + i];
   }
-  // what a key that holds a score may be off by
-  const float off_key = (softmax ? 0x1p-18f * inv_denom : 0x1p-20f) + __uint_as_float(kbits) * 0x1p-23f;
-  bool fine = __reduce_max_sync(0xffffffffu, zbits) < 0x7f800000u && kbits < 0x7f800000u;
-  __syncwarp();
+  float hi = -INFINITY, lo = INFINITY;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i)
+    if (i < n) {
+      hi = fmaxf(hi, v[i]);
+      lo = fminf(lo, v[i]);
+    }
+  const float kmax = from_order_bits(__reduce_max_sync(0xffffffffu, order_bits(hi)));
+  const float kmin = from_order_bits(__reduce_min_sync(0xffffffffu, order_bits(lo)));
+  const float top_abs = by_logit ? 1.0f : fmaxf(fabsf(kmax), fabsf(kmin));  // of keys that hold scores
+  fine = fine && top_abs < INFINITY;
+  const float off_key = (softmax ? 0x1p-18f * inv_denom : 0x1p-20f) + top_abs * 0x1p-23f;  // what they may be off by
 
   // Two logits give scores that fp64 tells apart, in their order: they differ by more than 2^-30, and neither score
   // is so near to 1 or to 0 that the difference is lost there.
-  auto logits_apart = [&](float hi, float lo) {
-    if (hi == lo) return true;  // the same score: the lower id, as found
-    if (!(hi - lo > 0x1p-30f)) return false;
-    return softmax ? lo - zmax > -600.0f : (hi < 12.0f && lo > -600.0f);
+  auto clear_of_limits = [&](float zhi, float zlo) {
+    return softmax ? zlo - zmax > -600.0f : (zhi < 12.0f && zlo > -600.0f);
   };
 
   // ---- 2. groups
-  const int gs = E / o.n_group;
-  if (groups && fine) {
-    const int per_group = 1 << (31 - __clz(32 / o.n_group));  // lanes
-    const int g = lane / per_group, sub = lane % per_group;
+  bool kept = group < o.n_group;
+  if (groups) {
     float a = -INFINITY, b = -INFINITY;
-    if (g < o.n_group) {
-      const int turn = (g * per_group) % gs;  // each group starts elsewhere, so that the lanes read different banks
-#pragma unroll 4
-      for (int i = sub; i < gs; i += per_group) {
-        const float v = key[g * gs + (i + turn < gs ? i + turn : i + turn - gs)];
-        b = fmaxf(b, fminf(a, v));
-        a = fmaxf(a, v);
+#pragma unroll
+    for (int i = 0; i < kPer; ++i)
+      if (i < n) {
+        b = fmaxf(b, fminf(a, v[i]));
+        a = fmaxf(a, v[i]);
       }
-    }
-    for (int off = per_group >> 1; off >= 1; off >>= 1) {
+    for (int off = 1 << lanes_log >> 1; off >= 1; off >>= 1) {
       const float oa = __shfl_xor_sync(0xffffffffu, a, off), ob = __shfl_xor_sync(0xffffffffu, b, off);
       b = fmaxf(fminf(a, oa), fmaxf(b, ob));
       a = fmaxf(a, oa);
     }
-    // lane q: group q's score and its place among them
-    float s = group_sums ? a + b : a;
-    s = __shfl_sync(0xffffffffu, s, (lane * per_group) & 31);
-    int before = 0;
+    const float s = !group_sums ? a : (by_logit ? score32(a) + score32(b) : a + b);  // in every lane of the group
+    int before = 0;  // groups ahead of this lane's
+#pragma unroll 4
     for (int q = 0; q < o.n_group; ++q) {
-      const float v = __shfl_sync(0xffffffffu, s, q);
-      before += v > s || (v == s && q < lane);
+      const float x = __shfl_sync(0xffffffffu, s, q << lanes_log);
+      before += x > s || (x == s && q < group);
     }
-    const bool mine = lane < o.n_group;
-    const bool stays = mine && before < o.topk_group;
-    const unsigned kept = __ballot_sync(0xffffffffu, stays);
-    if (stays) kept_groups[warp][__popc(kept & ((1u << lane) - 1u))] = static_cast<uint8_t>(lane);
-    __syncwarp();
     // the last group that stays against the first that does not
-    const int last = __ffs(__ballot_sync(0xffffffffu, mine && before == o.topk_group - 1)) - 1;
-    const int next = __ffs(__ballot_sync(0xffffffffu, mine && before == o.topk_group)) - 1;
-    const float hi = __shfl_sync(0xffffffffu, s, last), lo = __shfl_sync(0xffffffffu, s, next);
+    const unsigned last = __ballot_sync(0xffffffffu, kept && before == o.topk_group - 1);
+    const unsigned next = __ballot_sync(0xffffffffu, kept && before == o.topk_group);
+    kept = kept && before < o.topk_group;
+    const float shi = __shfl_sync(0xffffffffu, s, (__ffs(last) - 1) & 31);
+    const float slo = __shfl_sync(0xffffffffu, s, (__ffs(next) - 1) & 31);
     if (by_logit && !group_sums)
-      fine = logits_apart(hi, lo);
+      fine = fine && (shi == slo || (shi - slo > 0x1p-30f && clear_of_limits(shi, slo)));
     else
-      fine = hi - lo > (group_sums ? 4.0f : 2.0f) * off_key + fabsf(hi) * 0x1p-22f;
+      fine = fine && shi - slo > (group_sums ? 4.0f : 2.0f) * off_key + fabsf(shi) * 0x1p-22f;
   }
 
   // ---- 3. experts
-  int sel = 0;
-  float zsel = 0.0f;
-  if (fine) {
-    const float* order = by_logit ? zs : key;
-    const int ncand = o.topk_group * gs;
-    const float inv_gs = 1.0f / static_cast<float>(gs);
-    uint32_t u[kPer];
-    int id[kPer];
+  const int id_bits = max(1, 32 - __clz(E - 1));  // E <= 1024: at most 10
+  const uint32_t id_mask = (1u << id_bits) - 1u;
+  const int key_bits = min(23, 32 - id_bits);
+  const float steps = static_cast<float>((1 << key_bits) - 2);
+  const float base = fmaxf(kmin, kmax - 32.0f);  // keys further below share the lowest integer
+  const float inv_step = kmax > base ? steps / (kmax - base) : 0.0f;
+  fine = fine && inv_step < INFINITY;
+  uint32_t u[kPer];
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      const int c = lane + 32 * i;
-      u[i] = 0;
-      id[i] = 0x7fffffff;
-      if (c < ncand) {
-        int e = c;
-        if (groups) {
-          // c / gs: (c + 1/2) / gs is at least 1/2048 from a whole number, the product off by 2^-13 at most
-          const int q = static_cast<int>((static_cast<float>(c) + 0.5f) * inv_gs);
-          e = kept_groups[warp][q] * gs + (c - q * gs);
-        }
-        id[i] = e;
-        u[i] = order_bits(order[e]);
+  for (int i = 0; i < kPer; ++i) {
+    // 1 .. 2^key_bits - 1 in the mantissa
+    const uint32_t q = __float_as_uint(fmaf(fmaxf(v[i] - base, 0.0f), inv_step, 8388609.0f)) & 0x7fffffu;
+    u[i] = kept && i < n ? (q << id_bits) | (id_mask - static_cast<uint32_t>(e0 + i)) : 0u;
+  }
+  const int rounds = min(K + 1, o.topk_group * gs);
+  uint32_t mine = 0, top = 0;  // of round `lane`; of the last round
+  if (kPer <= 8) {
+    sort_descending(u);
+    for (int k = 0; k < rounds; ++k) {
+      top = __reduce_max_sync(0xffffffffu, u[0]);
+      if (u[0] == top) {
+#pragma unroll
+        for (int i = 1; i < kPer; ++i) u[i - 1] = u[i];
+        u[kPer - 1] = 0;
       }
+      if (lane == k) mine = top;
     }
-    if (kPer <= 4) {
-      // each lane's candidates in descending order (neighbours change places only if the later one is larger, so
-      // equal ones keep the lower id first): a round takes a lane's first and moves the others up
-#pragma unroll
-      for (int i = 1; i < kPer; ++i)
-#pragma unroll
-        for (int l = i; l >= 1; --l) {
-          const bool swap = u[l] > u[l - 1];
-          const uint32_t hi_u = swap ? u[l] : u[l - 1], lo_u = swap ? u[l - 1] : u[l];
-          const int hi_id = swap ? id[l] : id[l - 1], lo_id = swap ? id[l - 1] : id[l];
-          u[l - 1] = hi_u;
-          u[l] = lo_u;
-          id[l - 1] = hi_id;
-          id[l] = lo_id;
-        }
-    }
-    uint32_t mine = 0, top = 0;  // the key of round `lane`; of the last round
-    const int rounds = min(K + 1, ncand);
+  } else {
     for (int k = 0; k < rounds; ++k) {
       uint32_t best = u[0];
-      int bid = id[0];
-      if (kPer > 4) {
 #pragma unroll
-        for (int i = 1; i < kPer; ++i)
-          if (u[i] > best) {  // ids grow with i: the first of equal ones stays
-            best = u[i];
-            bid = id[i];
-          }
-      }
+      for (int i = 1; i < kPer; ++i) best = max(best, u[i]);
       top = __reduce_max_sync(0xffffffffu, best);
-      const int win = static_cast<int>(__reduce_min_sync(0xffffffffu, best == top ? bid : 0x7fffffff));
-      if (kPer > 4) {
 #pragma unroll
-        for (int i = 0; i < kPer; ++i)
-          if (id[i] == win) u[i] = 0;
-      } else if (bid == win) {
-#pragma unroll
-        for (int i = 1; i < kPer; ++i) {
-          u[i - 1] = u[i];
-          id[i - 1] = id[i];
-        }
-        u[kPer - 1] = 0;
-        id[kPer - 1] = 0x7fffffff;
-      }
-      if (lane == k) {
-        mine = top;
-        sel = win;
-      }
+      for (int i = 0; i < kPer; ++i)
+        if (u[i] == top) u[i] = 0;
+      if (lane == k) mine = top;
     }
-    // every choice against the next one: lane k compares rounds k and k + 1 (round 32 is in no lane)
-    const uint32_t after = __shfl_down_sync(0xffffffffu, mine, 1);
-    const int after_id = __shfl_down_sync(0xffffffffu, sel, 1);
-    bool good = true;
-    if (lane + 1 < rounds) {
-      const float hi = from_order_bits(mine), lo = from_order_bits(lane < 31 ? after : top);
-      if (by_logit)
-        good = logits_apart(hi, lo);
-      else
-        good = hi - lo > 2.0f * off_key ||
-               (lane < 31 && hi == lo && zs[sel] == zs[after_id] && bias[sel] == bias[after_id]);
-    }
-    if (lane < K) {
-      zsel = zs[sel];
-      // scores far below the fp32 range are the fp64 path's
-      good = good && !((softmax ? zsel - zmax : zsel) < -80.0f);
-    }
-    fine = __all_sync(0xffffffffu, good);
   }
+  // every choice against the next one: lane k compares rounds k and k + 1 (round 32 is in no lane)
+  auto id_of = [&](uint32_t x) { return min(static_cast<int>(id_mask - (x & id_mask)), E - 1); };
+  const int sel = id_of(mine);
+  const float zsel = lane < rounds ? raw_logit<kBf16>(row, sel) : 0.0f;
+  const uint32_t below = __shfl_down_sync(0xffffffffu, mine, 1);
+  float zlo = __shfl_down_sync(0xffffffffu, zsel, 1);
+  bool good = true;
+  if (lane + 1 < rounds) {
+    const uint32_t other = lane < 31 ? below : top;
+    if (lane == 31) zlo = raw_logit<kBf16>(row, id_of(other));
+    const int apart = static_cast<int>(mine >> id_bits) - static_cast<int>(other >> id_bits);
+    const float step = 1.0f / inv_step;
+    const float gap = static_cast<float>(apart - 2) * step;
+    if (!by_logit)
+      good = gap > 2.0f * off_key;
+    else if (kBf16 && fabsf(zsel) > 0x1p-20f && 4.0f * step < fabsf(zsel) * 0x1p-8f)
+      // different logits are further apart than 4 steps and 2^-28
+      good = apart == 0 || clear_of_limits(zsel, zlo);
+    else
+      good = gap > 0x1p-30f && clear_of_limits(zsel, zlo);
+  }
+  // scores far below the fp32 range are the fp64 path's
+  if (lane < K) good = good && !((softmax ? zsel - zmax : zsel) < -80.0f);
+  fine = __all_sync(0xffffffffu, good) && fine;
   if (!fine) {
-    route_token_fp64<kBf16>(row, bias, E, K, o, reinterpret_cast<double*>(zs), ids, w);
+    route_token_fp64<kBf16>(row, bias, E, K, o, keys_smem + warp * E, ids, w);
     return;
   }
 
@@ -395,7 +405,9 @@ cudaError_t launch_typed(const void* logits, int64_t ld, const float* bias, int 
                          const RouteGroupOpts& o, int32_t* topk_ids, float* topk_w, cudaStream_t stream) {
   const dim3 grid((M + kWarps - 1) / kWarps);
   const size_t smem = sizeof(double) * kWarps * E;  // at most 32 KB
-  const int per = (o.topk_group * (E / o.n_group) + 31) / 32;
+  int lanes = 1;  // per group
+  while (2 * lanes * o.n_group <= 32) lanes *= 2;
+  const int per = (E / o.n_group + lanes - 1) / lanes;  // experts per lane: at most 60 (17 groups, one lane each)
   auto run = [&](auto kern) { kern<<<grid, 32 * kWarps, smem, stream>>>(logits, ld, bias, M, E, K, o, topk_ids, topk_w); };
   if (per <= 1)
     run(route_group_kernel<kBf16, 1>);
@@ -407,8 +419,10 @@ cudaError_t launch_typed(const void* logits, int64_t ld, const float* bias, int 
     run(route_group_kernel<kBf16, 8>);
   else if (per <= 16)
     run(route_group_kernel<kBf16, 16>);
-  else
+  else if (per <= 32)
     run(route_group_kernel<kBf16, 32>);
+  else
+    run(route_group_kernel<kBf16, 64>);
   return cudaGetLastError();
 }
 
