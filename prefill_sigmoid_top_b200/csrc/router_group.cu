@@ -74,82 +74,106 @@ __device__ __forceinline__ double exp_score(double z, double zmax) {
   return exp(z - zmax);
 }
 
-// One token in fp64, whatever its logits hold: the definition, and the answer for the tokens that the fp32 path
-// leaves.  One warp; `key`: E doubles of shared memory.
-template <bool kBf16>
-__device__ __noinline__ void route_token_fp64(const void* row, const float* bias, int E, int K,
-                                              const RouteGroupOpts& o, double* key, int32_t* ids, float* w) {
-  const int lane = threadIdx.x & 31;
-  __syncwarp();
+// Which experts a lane holds: 32 / n_group lanes (rounded down to a power of two) per group, neighbours in each.
+struct Share {
+  int lanes_log, group, n, e0;  // lanes per group (log2); this lane's group, experts, first expert
+  __device__ __forceinline__ Share(int lane, int n_group, int gs) {
+    lanes_log = 31 - __clz(32 / n_group);
+    group = lane >> lanes_log;
+    const int chunk = (gs + (1 << lanes_log) - 1) >> lanes_log;  // <= kPer
+    const int from = (lane & ((1 << lanes_log) - 1)) * chunk;
+    n = group < n_group ? max(0, min(chunk, gs - from)) : 0;
+    e0 = n > 0 ? group * gs + from : 0;
+  }
+};
 
+// One token in fp64, whatever its logits hold: the definition, and the answer for the tokens that the fp32 path
+// leaves.  One warp, keys in registers; few tokens come here, so what counts is the time of one (it can be the last
+// of the grid): the exponentials of a lane are independent chains, a choice is three warp reductions.
+template <bool kBf16, int kPer>
+__device__ __noinline__ void route_token_fp64(const void* row, const float* bias, int E, int K,
+                                              const RouteGroupOpts o, int32_t* ids, float* w) {
+  const int lane = threadIdx.x & 31;
+  const int gs = E / o.n_group;
+  const Share me(lane, o.n_group, gs);
+  const bool softmax = o.scoring == MOE_SCORE_SOFTMAX;
+  double v[kPer];
   double zmax = -INFINITY, denom = 1.0;
-  if (o.scoring == MOE_SCORE_SOFTMAX) {
-    for (int e = lane; e < E; e += 32) zmax = fmax(zmax, static_cast<double>(load_logit<kBf16>(row, e)));
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) v[i] = i < me.n ? load_logit<kBf16>(row, me.e0 + i) : -INFINITY;
+  if (softmax) {
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) zmax = fmax(zmax, v[i]);
     for (int off = 16; off >= 1; off >>= 1) zmax = fmax(zmax, shfl_xor_d(zmax, off));
     denom = 0.0;
-    for (int e = lane; e < E; e += 32) denom += exp_score(load_logit<kBf16>(row, e), zmax);
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) denom += i < me.n ? exp_score(v[i], zmax) : 0.0;
     for (int off = 16; off >= 1; off >>= 1) denom += shfl_xor_d(denom, off);
   }
-  auto score = [&](int e) {
-    const double z = load_logit<kBf16>(row, e);
-    if (o.scoring == MOE_SCORE_SOFTMAX) return denom > 0.0 ? exp_score(z, zmax) / denom : 0.0;
+  auto score = [&](double z) {
+    if (softmax) return denom > 0.0 ? exp_score(z, zmax) / denom : 0.0;
     return 1.0 / (1.0 + exp(-z));
   };
-  for (int e = lane; e < E; e += 32)
-    key[e] = rank_key(bias != nullptr ? score(e) + static_cast<double>(bias[e]) : score(e));
-  __syncwarp();
-
-  // groups: lane g keeps the score of group g and whether it stays
-  const int gs = E / o.n_group;
-  unsigned kept = 0xffffffffu;
-  if (o.topk_group < o.n_group) {
-    double mine = -INFINITY;
-    for (int g = 0; g < o.n_group; ++g) {
-      double a = -INFINITY, b = -INFINITY;  // two largest keys
-      for (int i = lane; i < gs; i += 32) {
-        const double v = key[g * gs + i];
-        b = fmax(b, fmin(a, v));
-        a = fmax(a, v);
-      }
-      for (int off = 16; off >= 1; off >>= 1) {
-        const double oa = shfl_xor_d(a, off), ob = shfl_xor_d(b, off);
-        b = fmax(fmin(a, oa), fmax(b, ob));
-        a = fmax(a, oa);
-      }
-      if (lane == g) mine = (o.group_score == MOE_GROUP_TOP2 && gs > 1) ? rank_key(a + b) : a;
-    }
-    int before = 0;
-    for (int g = 0; g < o.n_group; ++g) {
-      const double v = __shfl_sync(0xffffffffu, mine, g);
-      before += v > mine || (v == mine && g < lane);
-    }
-    kept = __ballot_sync(0xffffffffu, lane < o.n_group && before < o.topk_group);
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const double p = score(v[i]);
+    v[i] = rank_key(bias != nullptr && i < me.n ? p + static_cast<double>(bias[me.e0 + i]) : p);
   }
-  uint32_t live = 0;  // bit i: expert lane + 32 i may be chosen
-  for (int e = lane, i = 0; e < E; e += 32, ++i)
-    if ((kept >> (e / gs)) & 1u) live |= 1u << i;
 
+  // group scores, in every lane of the group
+  bool kept = me.group < o.n_group;
+  if (o.topk_group < o.n_group) {
+    double a = -INFINITY, b = -INFINITY;  // two largest keys
+#pragma unroll
+    for (int i = 0; i < kPer; ++i)
+      if (i < me.n) {
+        b = fmax(b, fmin(a, v[i]));
+        a = fmax(a, v[i]);
+      }
+    for (int off = 1 << me.lanes_log >> 1; off >= 1; off >>= 1) {
+      const double oa = shfl_xor_d(a, off), ob = shfl_xor_d(b, off);
+      b = fmax(fmin(a, oa), fmax(b, ob));
+      a = fmax(a, oa);
+    }
+    const double s = (o.group_score == MOE_GROUP_TOP2 && gs > 1) ? rank_key(a + b) : a;
+    int before = 0;
+    for (int q = 0; q < o.n_group; ++q) {
+      const double x = __shfl_sync(0xffffffffu, s, q << me.lanes_log);
+      before += x > s || (x == s && q < me.group);
+    }
+    kept = kept && before < o.topk_group;
+  }
+  // as integers that order like the numbers; 0: not (or no more) a candidate
+  uint64_t u[kPer];
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const uint64_t x = static_cast<uint64_t>(__double_as_longlong(v[i] + 0.0));
+    u[i] = kept && i < me.n ? ((x >> 63) ? ~x : (x | 0x8000000000000000ull)) : 0ull;
+  }
   int sel = 0;
   for (int k = 0; k < K; ++k) {
-    double bv = -INFINITY;
-    int bi = 0x7fffffff;
-    for (int e = lane, i = 0; e < E; e += 32, ++i)
-      if (((live >> i) & 1u) && (bi == 0x7fffffff || key[e] > bv)) {
-        bv = key[e];
-        bi = e;
+    uint64_t best = u[0];
+    int bi = 0;
+#pragma unroll
+    for (int i = 1; i < kPer; ++i)
+      if (u[i] > best) {  // the first of equal ones stays
+        best = u[i];
+        bi = i;
       }
-    for (int off = 16; off >= 1; off >>= 1) {
-      const double ov = shfl_xor_d(bv, off);
-      const int oi = __shfl_xor_sync(0xffffffffu, bi, off);
-      if (ov > bv || (ov == bv && oi < bi)) {
-        bv = ov;
-        bi = oi;
-      }
+    const uint32_t hi = static_cast<uint32_t>(best >> 32);
+    const uint32_t top = __reduce_max_sync(0xffffffffu, hi);
+    const uint32_t low = hi == top ? static_cast<uint32_t>(best) : 0u;
+    const uint32_t low_top = __reduce_max_sync(0xffffffffu, low);
+    const bool has = hi == top && static_cast<uint32_t>(best) == low_top && best != 0;
+    const int win = static_cast<int>(__reduce_min_sync(0xffffffffu, has ? me.e0 + bi : E - 1));
+    if (has && me.e0 + bi == win) {
+#pragma unroll
+      for (int i = 0; i < kPer; ++i)
+        if (i == bi) u[i] = 0;
     }
-    if ((bi & 31) == lane) live &= ~(1u << (bi >> 5));
-    if (lane == k) sel = bi;
+    if (lane == k) sel = win;
   }
-  double p = lane < K ? score(sel) : 0.0;
+  double p = lane < K ? score(load_logit<kBf16>(row, sel)) : 0.0;
   double total = p;
   for (int off = 16; off >= 1; off >>= 1) total += shfl_xor_d(total, off);
   if (o.renormalize) p = total > 0.0 ? p / total : 0.0;
@@ -186,13 +210,13 @@ __device__ __forceinline__ void sort_descending(uint32_t (&v)[kN]) {
           }
 }
 
-// kPer: experts per lane, rounded up to a power of two.
-template <bool kBf16, int kPer>
+// kPer: experts per lane, rounded up to a power of two.  kFull: every lane has exactly kPer, and every lane's logits
+// start at a multiple of 16 bytes (or 8 experts or fewer at one of their own size).
+template <bool kBf16, int kPer, bool kFull>
 __global__ void __launch_bounds__(32 * kWarps) route_group_kernel(const void* __restrict__ logits, int64_t ld,
                                                                   const float* __restrict__ bias, int M, int E, int K,
                                                                   RouteGroupOpts o, int32_t* __restrict__ topk_ids,
                                                                   float* __restrict__ topk_w) {
-  extern __shared__ double keys_smem[];  // the fp64 path's
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int t = blockIdx.x * kWarps + warp;
   if (t >= M) return;
@@ -206,31 +230,31 @@ __global__ void __launch_bounds__(32 * kWarps) route_group_kernel(const void* __
   const bool group_sums = groups && o.group_score == MOE_GROUP_TOP2 && gs > 1;
 
   // ---- 1. this lane's experts and their keys
-  const int lanes_log = 31 - __clz(32 / o.n_group);  // lanes per group
-  const int group = lane >> lanes_log;
-  const int chunk = (gs + (1 << lanes_log) - 1) >> lanes_log;  // <= kPer
-  const int from = (lane & ((1 << lanes_log) - 1)) * chunk;
-  const int n = group < o.n_group ? max(0, min(chunk, gs - from)) : 0;
-  const int e0 = n > 0 ? group * gs + from : 0;
+  const Share me(lane, o.n_group, gs);
+  const int lanes_log = me.lanes_log, group = me.group;
+  const int n = kFull ? kPer : me.n;
+  const int e0 = kFull ? kPer * lane : me.e0;
   float v[kPer];
-  constexpr int kVec = kBf16 ? 8 : 4;  // logits per 16 bytes
-  const bool vectors = kPer >= kVec && chunk == kPer && gs == chunk << lanes_log && group < o.n_group &&
-                       (reinterpret_cast<uintptr_t>(row + static_cast<size_t>(e0) * (kBf16 ? 2 : 4)) & 15u) == 0;
-  if (vectors) {
-    const uint4* src = reinterpret_cast<const uint4*>(row + static_cast<size_t>(e0) * (kBf16 ? 2 : 4));
+  if (kFull) {
+    constexpr int kBytes = kPer * (kBf16 ? 2 : 4);
+    uint32_t x[(kBytes + 3) / 4];
+    const uint8_t* src = row + static_cast<size_t>(lane) * kBytes;
+    if (kBytes >= 16) {
 #pragma unroll
-    for (int i = 0; i < kPer / kVec; ++i) {
-      const uint4 q = src[i];
-      const uint32_t x[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        if (kBf16) {
-          v[(8 * i + 2 * u) % kPer] = bf16_lo(x[u]);
-          v[(8 * i + 2 * u + 1) % kPer] = bf16_hi(x[u]);
-        } else {
-          v[(4 * i + u) % kPer] = __uint_as_float(x[u]);
-        }
+      for (int i = 0; i < kBytes / 16; ++i) {
+        const uint4 q = reinterpret_cast<const uint4*>(src)[i];
+        x[(4 * i) % (kBytes / 4)] = q.x;
+        x[(4 * i + 1) % (kBytes / 4)] = q.y;
+        x[(4 * i + 2) % (kBytes / 4)] = q.z;
+        x[(4 * i + 3) % (kBytes / 4)] = q.w;
       }
+#pragma unroll
+      for (int i = 0; i < kPer; ++i)
+        v[i] = !kBf16 ? __uint_as_float(x[i % (kBytes / 4)])
+                      : (i & 1) ? bf16_hi(x[(i / 2) % (kBytes / 4)]) : bf16_lo(x[(i / 2) % (kBytes / 4)]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) v[i] = raw_logit<kBf16>(row, e0 + i);
     }
   } else {
 #pragma unroll
@@ -245,13 +269,13 @@ __global__ void __launch_bounds__(32 * kWarps) route_group_kernel(const void* __
     zmax = -INFINITY;
 #pragma unroll
     for (int i = 0; i < kPer; ++i)
-      if (i < n) zmax = fmaxf(zmax, v[i]);
+      if (kFull || i < n) zmax = fmaxf(zmax, v[i]);
     zmax = from_order_bits(__reduce_max_sync(0xffffffffu, order_bits(zmax)));
     if (!by_logit || group_sums || !o.renormalize) {
       denom = 0.0f;
 #pragma unroll
       for (int i = 0; i < kPer; ++i)
-        if (i < n) denom += expf(v[i] - zmax);
+        if (kFull || i < n) denom += expf(v[i] - zmax);
 #pragma unroll
       for (int off = 16; off >= 1; off >>= 1) denom += __shfl_xor_sync(0xffffffffu, denom, off);
     }
@@ -264,12 +288,12 @@ __global__ void __launch_bounds__(32 * kWarps) route_group_kernel(const void* __
   if (!by_logit) {
 #pragma unroll
     for (int i = 0; i < kPer; ++i)
-      if (i < n) v[i] = score32(v[i]) + bias[e0 + i];
+      if (kFull || i < n) v[i] = score32(v[i]) + bias[e0 + i];
   }
   float hi = -INFINITY, lo = INFINITY;
 #pragma unroll
   for (int i = 0; i < kPer; ++i)
-    if (i < n) {
+    if (kFull || i < n) {
       hi = fmaxf(hi, v[i]);
       lo = fminf(lo, v[i]);
     }
@@ -291,7 +315,7 @@ __global__ void __launch_bounds__(32 * kWarps) route_group_kernel(const void* __
     float a = -INFINITY, b = -INFINITY;
 #pragma unroll
     for (int i = 0; i < kPer; ++i)
-      if (i < n) {
+      if (kFull || i < n) {
         b = fmaxf(b, fminf(a, v[i]));
         a = fmaxf(a, v[i]);
       }
@@ -332,7 +356,7 @@ __global__ void __launch_bounds__(32 * kWarps) route_group_kernel(const void* __
   for (int i = 0; i < kPer; ++i) {
     // 1 .. 2^key_bits - 1 in the mantissa
     const uint32_t q = __float_as_uint(fmaf(fmaxf(v[i] - base, 0.0f), inv_step, 8388609.0f)) & 0x7fffffu;
-    u[i] = kept && i < n ? (q << id_bits) | (id_mask - static_cast<uint32_t>(e0 + i)) : 0u;
+    u[i] = kept && (kFull || i < n) ? (q << id_bits) | (id_mask - static_cast<uint32_t>(e0 + i)) : 0u;
   }
   const int rounds = min(K + 1, o.topk_group * gs);
   uint32_t mine = 0, top = 0;  // of round `lane`; of the last round
@@ -384,7 +408,7 @@ __global__ void __launch_bounds__(32 * kWarps) route_group_kernel(const void* __
   if (lane < K) good = good && !((softmax ? zsel - zmax : zsel) < -80.0f);
   fine = __all_sync(0xffffffffu, good) && fine;
   if (!fine) {
-    route_token_fp64<kBf16>(row, bias, E, K, o, keys_smem + warp * E, ids, w);
+    route_token_fp64<kBf16, kPer>(row, bias, E, K, o, ids, w);
     return;
   }
 
@@ -400,30 +424,37 @@ __global__ void __launch_bounds__(32 * kWarps) route_group_kernel(const void* __
   }
 }
 
+template <bool kBf16, int kPer>
+cudaError_t launch_per(const void* logits, int64_t ld, const float* bias, int M, int E, int K, const RouteGroupOpts& o,
+                       int32_t* topk_ids, float* topk_w, cudaStream_t stream) {
+  const dim3 grid((M + kWarps - 1) / kWarps);
+  const int size = kBf16 ? 2 : 4;
+  const int vec = kPer * size < 16 ? size : 16;  // bytes of a load
+  const bool full = E == 32 * kPer && (o.n_group & (o.n_group - 1)) == 0 && (ld * size) % vec == 0 &&
+                    (reinterpret_cast<uintptr_t>(logits) & (vec - 1)) == 0;
+  if (full)
+    route_group_kernel<kBf16, kPer, true>
+        <<<grid, 32 * kWarps, 0, stream>>>(logits, ld, bias, M, E, K, o, topk_ids, topk_w);
+  else
+    route_group_kernel<kBf16, kPer, false>
+        <<<grid, 32 * kWarps, 0, stream>>>(logits, ld, bias, M, E, K, o, topk_ids, topk_w);
+  return cudaGetLastError();
+}
+
 template <bool kBf16>
 cudaError_t launch_typed(const void* logits, int64_t ld, const float* bias, int M, int E, int K,
                          const RouteGroupOpts& o, int32_t* topk_ids, float* topk_w, cudaStream_t stream) {
-  const dim3 grid((M + kWarps - 1) / kWarps);
-  const size_t smem = sizeof(double) * kWarps * E;  // at most 32 KB
   int lanes = 1;  // per group
   while (2 * lanes * o.n_group <= 32) lanes *= 2;
   const int per = (E / o.n_group + lanes - 1) / lanes;  // experts per lane: at most 60 (17 groups, one lane each)
-  auto run = [&](auto kern) { kern<<<grid, 32 * kWarps, smem, stream>>>(logits, ld, bias, M, E, K, o, topk_ids, topk_w); };
-  if (per <= 1)
-    run(route_group_kernel<kBf16, 1>);
-  else if (per <= 2)
-    run(route_group_kernel<kBf16, 2>);
-  else if (per <= 4)
-    run(route_group_kernel<kBf16, 4>);
-  else if (per <= 8)
-    run(route_group_kernel<kBf16, 8>);
-  else if (per <= 16)
-    run(route_group_kernel<kBf16, 16>);
-  else if (per <= 32)
-    run(route_group_kernel<kBf16, 32>);
-  else
-    run(route_group_kernel<kBf16, 64>);
-  return cudaGetLastError();
+  auto run = [&](auto f) { return f(logits, ld, bias, M, E, K, o, topk_ids, topk_w, stream); };
+  if (per <= 1) return run(launch_per<kBf16, 1>);
+  if (per <= 2) return run(launch_per<kBf16, 2>);
+  if (per <= 4) return run(launch_per<kBf16, 4>);
+  if (per <= 8) return run(launch_per<kBf16, 8>);
+  if (per <= 16) return run(launch_per<kBf16, 16>);
+  if (per <= 32) return run(launch_per<kBf16, 32>);
+  return run(launch_per<kBf16, 64>);
 }
 
 }  // namespace
