@@ -301,7 +301,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           } else {
             const int id = args.sorted_ids[row];
             if (id >= 0 && id < nslots) {
-              tok_s[i] = args.row_scale[kGather ? id / args.top_k : row];
+              tok_s[i] = args.row_scale[kMode == kUp ? id / args.top_k : row];
               tok_row[i] = kMode == kUp ? row : id;
             } else {
               set_error(args.err, kErrInvalidInput);

@@ -12,23 +12,24 @@
 // a bound on what fp32 may be off by, and only where two candidates next to each other are nearer than that (or a
 // number is not finite, or far out) its warp computes it again in fp64.  The result is the fp64 one either way.
 //
-// fp32 path, one warp per token, no shared memory:
+// fp32 path, one warp per token, no shared memory.  What bounds it is the ALU pipe (compare, select, minimum and
+// integer logic issue at half rate), so keys are shaped with multiply-adds and compared as few times as can be:
 //  1. 32 / n_group lanes (a power of two) hold a group, each up to kPer neighbouring experts in registers (16-byte
 //     loads where rows allow).  Without a bias the key is the logit itself (the scores grow with it).
-//  2. group scores: the two largest keys of each lane, joined over the group's lanes by shuffles.
-//  3. the kept groups' keys become integers (22 or 23 bits of the distance from the smallest key, in steps of
-//     range / 2^b), with the inverted expert id below: all different, larger key first, lower id first.  Up to 8 per
-//     lane are sorted once (Batcher's network, a minimum and a maximum per exchange); then top_k + 1 rounds of ONE
-//     warp maximum (redux): the owner moves its list up.  The round past the last shows the gap behind the choice.
-//  4. weights from the K logits.
-// Two keys are in the right order where their integers are 3 or more apart (an integer is off by less than 3/4 of a
-// step) and that distance exceeds what the keys may be off by:
-//   sigmoid: |p32 - p| <= p (1 - p) (|z| 2^-23.4 + 2^-21.5) + p 2^-21 < 2^-20 (ex2.approx and rcp.approx are within
-//            2 ulp; the scaled argument of the exponential adds |z| 2^-23.4 relative)
+//  2. a key becomes an integer, its place between kmax - range and kmax in 2^23 (2^22) steps, with the inverted expert
+//     id below: two multiply-adds and one integer multiply-add.  All are different; larger key first, lower id first.
+//     Up to 8 per lane are sorted (Batcher's network: one minimum and one maximum per exchange).
+//  3. group scores from the two first integers of each lane, joined over the group's lanes by shuffles.
+//  4. top_k + 1 rounds of ONE warp maximum (redux) over the lanes' first integers; the owner moves its list up.  The
+//     round past the last shows the gap behind the choice.
+//  5. weights from the K logits.
+// Two keys are in the right order where their integers are 3 or more apart (one is off by less than a step) and that
+// distance exceeds what the keys may be off by:
+//   sigmoid: |p32 - p| <= p (1 - p) (|z| 2^-23.4 + 2^-22) + p (2^-24 + 2^-23) < 1.5 * 2^-22 (ex2.approx is within 2^-22,
+//            rcp.approx within 2^-23; the scaled argument of the exponential adds |z| 2^-23.4 relative)
 //   softmax: relative 2^-19 + |z - max| 2^-23, and p <= e^-|z - max| / denom: below 2^-18 / denom
-// plus 2^-24 of each sum that follows.  Of bf16 logits, two that are nearer than their spacing are equal: a tie.
-// Bound: issue slots, not memory.  Measured, 32767 tokens x 256 experts, 8 groups, K = 8: two warp reductions on (key,
-// id) pairs out of shared memory 50 us.
+// plus 2^-23 of each sum that follows.  Of bf16 logits, two that are nearer than their spacing are equal: a tie.
+// Keys below the range share the lowest integer: a choice that reaches them goes to fp64.
 #include "common.cuh"
 #include "kernels.h"
 
@@ -54,7 +55,7 @@ __device__ __forceinline__ float load_logit(const void* row, int e) {
   return isnan(z) ? -INFINITY : z;
 }
 
-// The hardware's base-2 exponential and reciprocal, results below 2^-126 flushed to 0 (within the bound of 2^-20).
+// The hardware's base-2 exponential and reciprocal, results below 2^-126 flushed to 0 (within the bounds above).
 __device__ __forceinline__ float exp2_approx(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -77,8 +78,9 @@ __device__ __forceinline__ double exp_score(double z, double zmax) {
 // Which experts a lane holds: 32 / n_group lanes (rounded down to a power of two) per group, neighbours in each.
 struct Share {
   int lanes_log, group, n, e0;  // lanes per group (log2); this lane's group, experts, first expert
-  __device__ __forceinline__ Share(int lane, int n_group, int gs) {
-    lanes_log = 31 - __clz(32 / n_group);
+  __device__ __forceinline__ Share(int lane, const RouteGroupOpts& o) {
+    const int n_group = o.n_group, gs = o.group_size;
+    lanes_log = o.lanes_log;
     group = lane >> lanes_log;
     const int chunk = (gs + (1 << lanes_log) - 1) >> lanes_log;  // <= kPer
     const int from = (lane & ((1 << lanes_log) - 1)) * chunk;
@@ -94,8 +96,8 @@ template <bool kBf16, int kPer>
 __device__ __noinline__ void route_token_fp64(const void* row, const float* bias, int E, int K,
                                               const RouteGroupOpts o, int32_t* ids, float* w) {
   const int lane = threadIdx.x & 31;
-  const int gs = E / o.n_group;
-  const Share me(lane, o.n_group, gs);
+  const int gs = o.group_size;
+  const Share me(lane, o);
   const bool softmax = o.scoring == MOE_SCORE_SOFTMAX;
   double v[kPer];
   double zmax = -INFINITY, denom = 1.0;
@@ -226,11 +228,11 @@ __global__ void __launch_bounds__(32 * kWarps) route_group_kernel(const void* __
   const bool softmax = o.scoring == MOE_SCORE_SOFTMAX;
   const bool groups = o.topk_group < o.n_group;
   const bool by_logit = bias == nullptr;
-  const int gs = E / o.n_group;
+  const int gs = o.group_size;
   const bool group_sums = groups && o.group_score == MOE_GROUP_TOP2 && gs > 1;
 
   // ---- 1. this lane's experts and their keys
-  const Share me(lane, o.n_group, gs);
+  const Share me(lane, o);
   const int lanes_log = me.lanes_log, group = me.group;
   const int n = kFull ? kPer : me.n;
   const int e0 = kFull ? kPer * lane : me.e0;
@@ -260,10 +262,9 @@ __global__ void __launch_bounds__(32 * kWarps) route_group_kernel(const void* __
 #pragma unroll
     for (int i = 0; i < kPer; ++i) v[i] = i < n ? raw_logit<kBf16>(row, e0 + i) : 0.0f;
   }
-  uint32_t zbits = 0;  // largest |z| as bits: from 0x7f800000 on a logit is not finite
+  float whole = 0.0f;  // NaN as soon as a logit (later: a key) is not finite
 #pragma unroll
-  for (int i = 0; i < kPer; ++i) zbits = max(zbits, __float_as_uint(v[i]) & 0x7fffffffu);
-  bool fine = __reduce_max_sync(0xffffffffu, zbits) < 0x7f800000u;
+  for (int i = 0; i < kPer; ++i) whole = fmaf(v[i], 0.0f, whole);
   float zmax = 0.0f, denom = 1.0f;
   if (softmax) {
     zmax = -INFINITY;
@@ -280,7 +281,7 @@ __global__ void __launch_bounds__(32 * kWarps) route_group_kernel(const void* __
       for (int off = 16; off >= 1; off >>= 1) denom += __shfl_xor_sync(0xffffffffu, denom, off);
     }
   }
-  const float inv_denom = 1.0f / denom;
+  const float inv_denom = rcp_approx(denom);
   auto score32 = [&](float z) {
     constexpr float kLog2e = 1.4426950408889634f;
     return softmax ? exp2_approx((z - zmax) * kLog2e) * inv_denom : rcp_approx(1.0f + exp2_approx(-z * kLog2e));
@@ -290,78 +291,106 @@ __global__ void __launch_bounds__(32 * kWarps) route_group_kernel(const void* __
     for (int i = 0; i < kPer; ++i)
       if (kFull || i < n) v[i] = score32(v[i]) + bias[e0 + i];
   }
-  float hi = -INFINITY, lo = INFINITY;
+  float hi = -INFINITY;
 #pragma unroll
   for (int i = 0; i < kPer; ++i)
-    if (kFull || i < n) {
-      hi = fmaxf(hi, v[i]);
-      lo = fminf(lo, v[i]);
-    }
+    if (kFull || i < n) hi = fmaxf(hi, v[i]);
   const float kmax = from_order_bits(__reduce_max_sync(0xffffffffu, order_bits(hi)));
-  const float kmin = from_order_bits(__reduce_min_sync(0xffffffffu, order_bits(lo)));
-  const float top_abs = by_logit ? 1.0f : fmaxf(fabsf(kmax), fabsf(kmin));  // of keys that hold scores
-  fine = fine && top_abs < INFINITY;
-  const float off_key = (softmax ? 0x1p-18f * inv_denom : 0x1p-20f) + top_abs * 0x1p-23f;  // what they may be off by
+  if (!by_logit) {
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) whole = fmaf(v[i], 0.0f, whole);
+  }
+
+  // ---- 2. integers
+  const int id_bits = max(8, 32 - __clz(E - 1));  // E <= 1024: at most 10
+  const uint32_t id_mask = (1u << id_bits) - 1u;
+  const float steps = id_bits <= 9 ? 8388606.0f : 4194302.0f;  // 2^min(23, 32 - id_bits) - 2
+  const float range = by_logit ? fmaf(0.5f, fabsf(kmax), 4.0f) : fabsf(kmax) + 2.0f;
+  const float inv_range = rcp_approx(range);
+  const float low = fmaf(-kmax, inv_range, 1.0f);  // key * inv_range + low: 1 at kmax, 0 at kmax - range
+  const float step = range * (id_bits <= 9 ? 1.0f / 8388606.0f : 1.0f / 4194302.0f);
+  const float sure = step * 0.9999f;               // of two keys n + 2 integers apart: n of these at least
+  uint32_t u[kPer];
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const float at = __saturatef(fmaf(v[i], inv_range, low));
+    // 2^23 + 1 .. 2^23 + steps + 1: shifting by id_bits >= 8 leaves the integer alone (bit 23 of 0x4b000000 is 0)
+    const uint32_t q = __float_as_uint(fmaf(at, steps, 8388609.0f));
+    u[i] = q * (id_mask + 1u) + (id_mask - static_cast<uint32_t>(e0 + i));
+    if (!kFull) u[i] = i < n ? u[i] : 0u;
+  }
+  if (kPer <= 8) sort_descending(u);
+  // what the keys may be off by, and the range that the integers show
+  const float top_abs = by_logit ? 1.0f : fabsf(kmax) + range;
+  const float off_key = (softmax ? 0x1p-18f * inv_denom : 0x1.8p-22f) + top_abs * 0x1p-23f;
+  // a key from its integer: within two steps and the rounding of range and step (4 steps)
+  auto value_of = [&](uint32_t q) { return fmaf(static_cast<float>(q), step, kmax - range); };
 
   // Two logits give scores that fp64 tells apart, in their order: they differ by more than 2^-30, and neither score
   // is so near to 1 or to 0 that the difference is lost there.
   auto clear_of_limits = [&](float zhi, float zlo) {
     return softmax ? zlo - zmax > -600.0f : (zhi < 12.0f && zlo > -600.0f);
   };
+  // Two logits with the integers q and q - apart: a tie, or apart as above (in the lowest integer anything may be).
+  auto logits_clear = [&](uint32_t q, int apart, float zhi, float zlo) {
+    if (kBf16 && q > 2 && fabsf(zhi) > 0x1p-20f && 5.0f * step < fabsf(zhi) * 0x1p-8f)
+      return apart == 0 || clear_of_limits(zhi, zlo);  // different ones are further apart than 4 steps and 2^-28
+    return static_cast<float>(apart - 2) * sure > 0x1p-30f && clear_of_limits(zhi, zlo);
+  };
+  bool good = true;
 
-  // ---- 2. groups
-  bool kept = group < o.n_group;
+  // ---- 3. groups
   if (groups) {
-    float a = -INFINITY, b = -INFINITY;
+    uint32_t a = u[0], b = kPer > 1 ? u[1 % kPer] : 0u;
+    if (kPer > 8) {
+      b = 0;
 #pragma unroll
-    for (int i = 0; i < kPer; ++i)
-      if (kFull || i < n) {
-        b = fmaxf(b, fminf(a, v[i]));
-        a = fmaxf(a, v[i]);
+      for (int i = 1; i < kPer; ++i) {
+        b = max(b, min(a, u[i]));
+        a = max(a, u[i]);
       }
-    for (int off = 1 << lanes_log >> 1; off >= 1; off >>= 1) {
-      const float oa = __shfl_xor_sync(0xffffffffu, a, off), ob = __shfl_xor_sync(0xffffffffu, b, off);
-      b = fmaxf(fminf(a, oa), fmaxf(b, ob));
-      a = fmaxf(a, oa);
     }
-    const float s = !group_sums ? a : (by_logit ? score32(a) + score32(b) : a + b);  // in every lane of the group
+    for (int off = 1 << lanes_log >> 1; off >= 1; off >>= 1) {
+      const uint32_t oa = __shfl_xor_sync(0xffffffffu, a, off), ob = __shfl_xor_sync(0xffffffffu, b, off);
+      b = max(min(a, oa), max(b, ob));
+      a = max(a, oa);
+    }
+    a >>= id_bits;
+    b >>= id_bits;
+    // as an integer in every lane of the group: steps, or the bits of a (positive) sum of scores
+    uint32_t s = a;
+    if (group_sums) s = by_logit ? __float_as_uint(score32(value_of(a)) + score32(value_of(b))) : a + b;
     int before = 0;  // groups ahead of this lane's
 #pragma unroll 4
     for (int q = 0; q < o.n_group; ++q) {
-      const float x = __shfl_sync(0xffffffffu, s, q << lanes_log);
+      const uint32_t x = __shfl_sync(0xffffffffu, s, q << lanes_log);
       before += x > s || (x == s && q < group);
     }
     // the last group that stays against the first that does not
-    const unsigned last = __ballot_sync(0xffffffffu, kept && before == o.topk_group - 1);
-    const unsigned next = __ballot_sync(0xffffffffu, kept && before == o.topk_group);
-    kept = kept && before < o.topk_group;
-    const float shi = __shfl_sync(0xffffffffu, s, (__ffs(last) - 1) & 31);
-    const float slo = __shfl_sync(0xffffffffu, s, (__ffs(next) - 1) & 31);
-    if (by_logit && !group_sums)
-      fine = fine && (shi == slo || (shi - slo > 0x1p-30f && clear_of_limits(shi, slo)));
-    else
-      fine = fine && shi - slo > (group_sums ? 4.0f : 2.0f) * off_key + fabsf(shi) * 0x1p-22f;
+    const bool real = group < o.n_group;
+    const unsigned last = __ballot_sync(0xffffffffu, real && before == o.topk_group - 1);
+    const unsigned next = __ballot_sync(0xffffffffu, real && before == o.topk_group);
+    const uint32_t shi = __shfl_sync(0xffffffffu, s, (__ffs(last) - 1) & 31);
+    const uint32_t slo = __shfl_sync(0xffffffffu, s, (__ffs(next) - 1) & 31);
+    const int apart = static_cast<int>(shi - slo);
+    if (!by_logit) {
+      good = static_cast<float>(apart - 4) * sure > 4.0f * off_key;
+    } else if (group_sums) {
+      const float fhi = __uint_as_float(shi);
+      good = fhi - __uint_as_float(slo) > 4.0f * (off_key + 6.0f * step) + fhi * 0x1p-22f;
+    } else {
+      good = logits_clear(shi, apart, value_of(shi), value_of(slo));
+    }
+    if (!(real && before < o.topk_group)) {
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) u[i] = 0;
+    }
   }
 
-  // ---- 3. experts
-  const int id_bits = max(1, 32 - __clz(E - 1));  // E <= 1024: at most 10
-  const uint32_t id_mask = (1u << id_bits) - 1u;
-  const int key_bits = min(23, 32 - id_bits);
-  const float steps = static_cast<float>((1 << key_bits) - 2);
-  const float base = fmaxf(kmin, kmax - 32.0f);  // keys further below share the lowest integer
-  const float inv_step = kmax > base ? steps / (kmax - base) : 0.0f;
-  fine = fine && inv_step < INFINITY;
-  uint32_t u[kPer];
-#pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    // 1 .. 2^key_bits - 1 in the mantissa
-    const uint32_t q = __float_as_uint(fmaf(fmaxf(v[i] - base, 0.0f), inv_step, 8388609.0f)) & 0x7fffffu;
-    u[i] = kept && (kFull || i < n) ? (q << id_bits) | (id_mask - static_cast<uint32_t>(e0 + i)) : 0u;
-  }
+  // ---- 4. experts
   const int rounds = min(K + 1, o.topk_group * gs);
   uint32_t mine = 0, top = 0;  // of round `lane`; of the last round
   if (kPer <= 8) {
-    sort_descending(u);
     for (int k = 0; k < rounds; ++k) {
       top = __reduce_max_sync(0xffffffffu, u[0]);
       if (u[0] == top) {
@@ -389,38 +418,39 @@ __global__ void __launch_bounds__(32 * kWarps) route_group_kernel(const void* __
   const float zsel = lane < rounds ? raw_logit<kBf16>(row, sel) : 0.0f;
   const uint32_t below = __shfl_down_sync(0xffffffffu, mine, 1);
   float zlo = __shfl_down_sync(0xffffffffu, zsel, 1);
-  bool good = true;
   if (lane + 1 < rounds) {
     const uint32_t other = lane < 31 ? below : top;
     if (lane == 31) zlo = raw_logit<kBf16>(row, id_of(other));
     const int apart = static_cast<int>(mine >> id_bits) - static_cast<int>(other >> id_bits);
-    const float step = 1.0f / inv_step;
-    const float gap = static_cast<float>(apart - 2) * step;
-    if (!by_logit)
-      good = gap > 2.0f * off_key;
-    else if (kBf16 && fabsf(zsel) > 0x1p-20f && 4.0f * step < fabsf(zsel) * 0x1p-8f)
-      // different logits are further apart than 4 steps and 2^-28
-      good = apart == 0 || clear_of_limits(zsel, zlo);
-    else
-      good = gap > 0x1p-30f && clear_of_limits(zsel, zlo);
+    good = good && (by_logit ? logits_clear(mine >> id_bits, apart, zsel, zlo)
+                             : static_cast<float>(apart - 2) * sure > 2.0f * off_key);
   }
   // scores far below the fp32 range are the fp64 path's
   if (lane < K) good = good && !((softmax ? zsel - zmax : zsel) < -80.0f);
-  fine = __all_sync(0xffffffffu, good) && fine;
-  if (!fine) {
+  if (!__all_sync(0xffffffffu, good && whole == 0.0f)) {
     route_token_fp64<kBf16, kPer>(row, bias, E, K, o, ids, w);
     return;
   }
 
-  // ---- 4. weights
+  // ---- 5. weights
   float p = 0.0f;
-  if (lane < K) p = softmax ? expf(zsel - zmax) : __fdiv_rn(1.0f, 1.0f + expf(-zsel));
+  if (lane < K) {
+    if (softmax) {
+      // the rounding of z - max counts in full in the exponential of a far logit: it goes in as a factor
+      const float d = zsel - zmax, back = d + zmax;
+      const float lost = (zsel - back) + ((back - d) - zmax);  // z - max = d + lost
+      const float e = expf(d);
+      p = fmaf(e, lost, e);
+    } else {
+      p = rcp_approx(1.0f + expf(-zsel));
+    }
+  }
   float total = p;
 #pragma unroll
   for (int off = 16; off >= 1; off >>= 1) total += __shfl_xor_sync(0xffffffffu, total, off);
   if (lane < K) {
     ids[lane] = sel;
-    w[lane] = __fdiv_rn(p, o.renormalize ? total : denom) * o.routed_scale;
+    w[lane] = p * rcp_approx(o.renormalize ? total : denom) * o.routed_scale;
   }
 }
 
@@ -443,10 +473,11 @@ cudaError_t launch_per(const void* logits, int64_t ld, const float* bias, int M,
 
 template <bool kBf16>
 cudaError_t launch_typed(const void* logits, int64_t ld, const float* bias, int M, int E, int K,
-                         const RouteGroupOpts& o, int32_t* topk_ids, float* topk_w, cudaStream_t stream) {
-  int lanes = 1;  // per group
-  while (2 * lanes * o.n_group <= 32) lanes *= 2;
-  const int per = (E / o.n_group + lanes - 1) / lanes;  // experts per lane: at most 60 (17 groups, one lane each)
+                         RouteGroupOpts o, int32_t* topk_ids, float* topk_w, cudaStream_t stream) {
+  o.group_size = E / o.n_group;
+  o.lanes_log = 0;
+  while ((2 << o.lanes_log) * o.n_group <= 32) ++o.lanes_log;
+  const int per = (o.group_size + (1 << o.lanes_log) - 1) >> o.lanes_log;  // experts per lane: at most 60 (17 groups, one lane each)
   auto run = [&](auto f) { return f(logits, ld, bias, M, E, K, o, topk_ids, topk_w, stream); };
   if (per <= 1) return run(launch_per<kBf16, 1>);
   if (per <= 2) return run(launch_per<kBf16, 2>);

@@ -145,6 +145,27 @@ def test_far_logits():
     check(z, None, 4, 4, 2, scoring=moe.SCORE_SOFTMAX)
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["fp32", "bf16"])
+@pytest.mark.parametrize("E,G,TG,K", [(64, 8, 3, 12), (256, 1, 1, 8), (1024, 4, 2, 32), (60, 5, 2, 7)])
+@pytest.mark.parametrize("scoring", [moe.SCORE_SIGMOID, moe.SCORE_SOFTMAX])
+def test_wide_narrow_and_shifted_logits(E, G, TG, K, dtype, scoring):
+    """Logits far apart, nearly equal, far from zero, mostly at the type's lowest value, and quantised to few values;
+    with and without a bias, which may be large against the scores."""
+    g = torch.Generator().manual_seed(E + K)
+    z = torch.randn(8, E, generator=g)
+    z[1] *= 200.0
+    z[2] = z[2] * 1e-3 + 0.25
+    z[3] = z[3] * 2.0 - 300.0
+    z[4, 5:] = torch.finfo(dtype).min
+    z[5] = (z[5] * 2).round() / 2
+    z[6] = z[6] * 8.0 + 1000.0
+    z[7, ::3] -= 40.0
+    b = torch.randn(E, generator=g)
+    for bias in (None, b * 0.01, b * 30.0):
+        check(z.to(dtype), bias, K, G, TG, moe.GROUP_TOP2, scoring, False)
+        check(z.to(dtype), bias, K, G, TG, moe.GROUP_MAX, scoring)
+
+
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 @pytest.mark.parametrize("off,pad", [(0, 3), (1, 7), (3, 1), (4, 4)])
 def test_strided_and_unaligned_rows(dtype, off, pad):
