@@ -29,7 +29,11 @@ namespace {
 constexpr int kBM = 128;          // weight rows per CTA
 constexpr int kBK = 128;          // codes per stage
 constexpr int kATile = kBM * kBK;
-constexpr int kThreads = 192;     // warp 0 = TMA producer, 1 = MMA issuer, 2..5 = epilogue
+// Warps 0..3 = TMA producers (k-steps in turn: one producer thread issues a 16 KB copy every 0.48 us at best, which
+// is 5.0 TB/s over all SMs), 4..7 = epilogue, 8 = MMA issuer.
+constexpr int kProducerWarps = 4;
+constexpr int kMmaWarp = 8;
+constexpr int kThreads = 32 * (kMmaWarp + 1);
 
 enum Mode { kUp = 0, kDown = 1, kDense = 2 };
 
@@ -42,6 +46,11 @@ constexpr int pow2_at_least(int v) {
 template <int kMode, int kNmax, int kStages, int kBufs>
 struct TCfg {
   static constexpr int kPanels = kMode == kUp ? 2 : 1;
+  // Producer warps in use, a power of two.  A producer that has seen step i - kProducers freed knows that step
+  // i - kProducers - kStages is consumed; its wait for step i tells phases apart only if that covers step
+  // i - 2 kStages, so there are no more of them than stages.
+  static constexpr int kProducers = kStages >= 4 ? 4 : (kStages >= 2 ? 2 : 1);
+  static_assert(kProducers <= kProducerWarps && kProducers <= kStages, "a producer is at most one phase behind");
   static constexpr int kBTile = kNmax * kBK;
   static constexpr int kStageBytes = kPanels * kATile + kBTile;
   static constexpr int kTmemCols = pow2_at_least(kBufs * kPanels * kNmax);
@@ -108,7 +117,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   const int total = kMode == kDense ? W * dense_tiles : prefix[args.E];
   if (first >= total) return;  // the whole cluster leaves
-  if (warp == 1) {
+  if (warp == kMmaWarp) {
     tmem_alloc(tmem_slot, C::kTmemCols);
     tmem_relinquish();
   }
@@ -171,16 +180,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       static_cast<__nv_bfloat16*>(args.out)[at] = __float2bfloat16_rn(v);
   };
 
-  if (warp == 0) {
-    // ------------------------------------------------ TMA producer
-    if (lane == 0) {
+  constexpr int kProducers = C::kProducers;
+  if (warp < kProducers) {
+    // ------------------------------------------------ TMA producers: warp w loads every kProducers-th k-step
+    if (warp == 0 && lane == 0) {
       prefetch_tensor_map(&tm_a0);
       if (kMode == kUp) prefetch_tensor_map(&tm_a1);
       prefetch_tensor_map(&tm_b);
     }
-    int it = 0;
+    const int nk = k_hi - k_lo;
+    int it0 = 0, issued = 0;  // k-steps before this tile; behind the last one that this warp issued
     bool alive = true;
-    for (int tile = first; tile < total && alive; tile += step) {
+    for (int tile = first; tile < total && alive; tile += step, it0 += nk) {
       const Tile c = tile_at(tile);
       const int a_row = c.e * args.rows_per_expert + c.w * kBM;
       // a panel that one token tile reads is streamed; others come from L2 the next time
@@ -194,8 +205,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             tok[u] = (id >= 0 && id < nslots) ? id / args.top_k : 0;
           }
       }
-      for (int k = k_lo; k < k_hi; ++k, ++it) {
-        const int s = it % kStages;
+      for (int i = (warp - it0) & (kProducers - 1); i < nk; i += kProducers) {
+        const int it = it0 + i, s = it % kStages, k = k_lo + i;
         bool ok = true;
         if (lane == 0) ok = mbar_wait_bounded(&empty[s], ((it / kStages) & 1) ^ 1, abort_flag);
         ok = __shfl_sync(0xffffffffu, ok, 0);
@@ -221,18 +232,22 @@ __global__ void __launch_bounds__(kThreads, 1)
         } else if (16 * lane < c.N) {
           tma_load_2d(&tm_b, &full[s], bt + lane * 16 * kBK, k * kBK, c.row0 + 16 * lane);
         }
+        issued = it + 1;
       }
     }
     // no exit while copies of this CTA may still land
     if (lane == 0) {
-      for (int k = max(0, it - kStages); k < it; ++k)
+      const int lo = max(0, (alive ? it0 : issued) - kStages);  // each slot's last use
+      for (int k = lo + ((warp - lo) & (kProducers - 1)); k < issued; k += kProducers)
         if (!mbar_wait_bounded(&full[k % kStages], (k / kStages) & 1, nullptr)) {
           set_error(args.err, kErrTimeout);
           break;
         }
     }
     __syncwarp();
-  } else if (warp == 1) {
+  } else if (warp < kProducerWarps) {
+    // idle
+  } else if (warp == kMmaWarp) {
     // ------------------------------------------------ MMA issuer
     if (lane == 0) {
       int it = 0, j = 0;
@@ -330,7 +345,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // every CTA of the cluster takes a share of the tile's rows and adds the others' partial sums to its own
     cluster_sync_all();
     const Tile c = tile_at(first);
-    if (warp >= 2 && !*abort_flag) {
+    if (warp >= kProducerWarps && warp < kMmaWarp && !*abort_flag) {
       const int q = warp & 3;
       const int ch = c.w * kBM + q * 32 + lane;
       const bool col_ok = ch < args.rows_per_expert;
@@ -355,7 +370,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   tc_fence_before_sync();
   __syncthreads();
-  if (warp == 1) tmem_dealloc(tmem, C::kTmemCols);
+  if (warp == kMmaWarp) tmem_dealloc(tmem, C::kTmemCols);
 }
 
 template <int kMode, int kNmax, int kStages, int kBufs>

@@ -11,7 +11,11 @@
 // and token rows [r N/2, (r + 1) N/2) of the tile's N (its tokens rounded up to 32, the width step of this MMA).
 // Channels past the expert's last row are computed and not stored.
 //
-// Warps (640 threads): 0 = weight producer, 1 = MMA issuer (leader), 2 = token producer, 3 idle, 4..19 = epilogue.
+// Warps (640 threads): 0..2 = producers, 3 = MMA issuer (leader), 4..19 = epilogue.  A stage holds the weight boxes
+// and the token rows of one k-step; the producer warps take stages in turn.  One producer thread per operand,
+// as the bf16 pair kernels have, needs about 0.7 us for a stage however wide its tokens and wherever the weights are
+// (the wake-up of its wait and the issue of its copies in series): that alone held 8192 x 7168 x 7168 at 0.69 us per
+// k-step.
 // Every wait is bounded; a timeout sets the error word and unwinds, and both CTAs still meet at the last cluster
 // barrier.
 #include "common.cuh"
@@ -26,43 +30,45 @@ constexpr int kBM = 128;              // weight rows per box
 constexpr int kBK = 128;              // codes per stage
 constexpr int kBoxBytes = kBM * kBK;  // 16 KB
 constexpr int kBRows = 32;            // rows per token box
+constexpr int kProducers = 3;
+constexpr int kMmaWarp = 3;
+constexpr int kFirstEpi = 4;
 constexpr int kEpiWarps = 16;
-constexpr int kThreads = 128 + 32 * kEpiWarps;
+constexpr int kThreads = 32 * (kFirstEpi + kEpiWarps);
 
 enum Mode { kUp = 0, kDown = 1, kDense = 2 };
 
-template <int kNmax, int kStagesA, int kStagesB>
+template <int kNmax, int kStages>
 struct PCfg {
   static constexpr int kHalf = kNmax / 2;
-  static constexpr int kAStage = 2 * kBoxBytes;
-  static constexpr int kBStage = kHalf * kBK;
+  static constexpr int kABytes = 2 * kBoxBytes;
+  static constexpr int kStage = kABytes + kHalf * kBK;
   static constexpr int kAccCols = 2 * kNmax;
   static constexpr int kAccBufs = 512 / kAccCols;
   static constexpr int kMisc = 10240;  // barriers, flags, counts and tile prefix over the experts (E <= 1024)
-  static constexpr int kSmem = 1024 + kStagesA * kAStage + kStagesB * kBStage + kMisc;
+  static constexpr int kSmem = 1024 + kStages * kStage + kMisc;
   static_assert(kNmax == 128 || kNmax == 256, "token-tile widths");
+  // A producer that has seen step i - kProducers freed knows that step i - kProducers - kStages is consumed; its wait
+  // for step i tells phases apart only if that covers step i - 2 kStages.
+  static_assert(kStages >= kProducers, "a producer is at most one phase behind");
   static_assert(kSmem <= 227 * 1024, "shared memory");
   static_assert(kSmem > 116 * 1024, "one CTA per SM: it owns all 512 tensor-memory columns");
 };
 
 // kGather (up): the token rows are gathered from the codes of x by token id (tile::gather4); otherwise they are
 // consecutive plan rows (or rows of x, dense).
-template <int kMode, bool kGather, int kNmax, int kStagesA, int kStagesB>
+template <int kMode, bool kGather, int kNmax, int kStages>
 __global__ void __launch_bounds__(kThreads, 1)
     int8_pair_kernel(const __grid_constant__ CUtensorMap tm_a0, const __grid_constant__ CUtensorMap tm_a1,
                      const __grid_constant__ CUtensorMap tm_b, const Int8GemmArgs args) {
-  using C = PCfg<kNmax, kStagesA, kStagesB>;
+  using C = PCfg<kNmax, kStages>;
   extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint8_t* a_ring = smem;
-  uint8_t* b_ring = a_ring + kStagesA * C::kAStage;
-  uint8_t* misc = b_ring + kStagesB * C::kBStage;
-  uint64_t* a_full = reinterpret_cast<uint64_t*>(misc);
-  uint64_t* a_empty = a_full + kStagesA;
-  uint64_t* b_full = a_empty + kStagesA;
-  uint64_t* b_empty = b_full + kStagesB;
-  uint64_t* acc_full = b_empty + kStagesB;  // [2]
-  uint64_t* acc_empty = acc_full + 2;       // [2] (the leader's counts both CTAs' epilogue warps)
+  uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* misc = ring + kStages * C::kStage;
+  uint64_t* full = reinterpret_cast<uint64_t*>(misc);
+  uint64_t* empty = full + kStages;
+  uint64_t* acc_full = empty + kStages;  // [2]
+  uint64_t* acc_empty = acc_full + 2;    // [2] (the leader's counts both CTAs' epilogue warps)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_empty + 2);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   int* cnt = const_cast<int*>(abort_flag + 1);  // [E]
@@ -85,13 +91,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   if (kMode != kDense && warp == 0) build_tile_prefix<kNmax>(cnt, prefix, E, W, lane);
   if (tid == 0) {
-    for (int s = 0; s < kStagesA; ++s) {
-      mbar_init(&a_full[s], 1);
-      mbar_init(&a_empty[s], 1);
-    }
-    for (int s = 0; s < kStagesB; ++s) {
-      mbar_init(&b_full[s], 1);
-      mbar_init(&b_empty[s], 1);
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&acc_full[b], 1);
@@ -102,7 +104,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   const int total = kMode == kDense ? W * dense_tiles : prefix[E];
   if (pair >= total) return;  // both CTAs of a pair see the same count
-  if (warp == 1) {
+  if (warp == kMmaWarp) {
     tmem_alloc_pair(tmem_slot, 512);
     tmem_relinquish_pair();
   }
@@ -136,52 +138,21 @@ __global__ void __launch_bounds__(kThreads, 1)
     return t;
   };
 
-  if (warp == 0) {
-    // ------------------------------------------------ weight producer (both CTAs)
-    if (lane == 0) {
+  if (warp < kProducers) {
+    // ------------------------------------------------ producers (both CTAs): warp w loads every third k-step
+    if (warp == 0 && lane == 0) {
       prefetch_tensor_map(&tm_a0);
       if (kMode == kUp) prefetch_tensor_map(&tm_a1);
+      prefetch_tensor_map(&tm_b);
     }
-    int ka = 0;
+    const uint64_t pol_b = l2_policy_evict_normal();
+    int it0 = 0;  // k-steps before this tile
     bool alive = true;
-    for (int tile = pair; tile < total && alive; tile += npairs) {
+    for (int tile = pair; tile < total && alive; tile += npairs, it0 += nk) {
       const Tile c = tile_at(tile);
       const uint64_t pol = c.count <= tw ? l2_policy_evict_first() : l2_policy_evict_normal();
       const int row_a0 = c.e * args.rows_per_expert + c.w * kBlock + static_cast<int>(rank) * kBM;
       const int row_a1 = kMode == kUp ? row_a0 : row_a0 + 2 * kBM;
-      for (int k = 0; k < nk; ++k, ++ka) {
-        const int s = ka % kStagesA;
-        bool ok = true;
-        if (lane == 0) {
-          ok = mbar_wait_bounded(&a_empty[s], ((ka / kStagesA) & 1) ^ 1, abort_flag);
-          if (ok && leader) mbar_arrive_expect_tx(&a_full[s], 2 * C::kAStage);
-        }
-        ok = __shfl_sync(0xffffffffu, ok, 0);
-        if (!ok) {
-          if (lane == 0) {
-            *abort_flag = 1;
-            set_error(args.err, kErrTimeout);
-          }
-          alive = false;
-          break;
-        }
-        uint8_t* st = a_ring + s * C::kAStage;
-        const uint32_t bar = cluster_addr(&a_full[s], 0);
-        if (lane == 0)
-          tma_load_2d_pair(&tm_a0, bar, st, k * kBK, row_a0, pol);
-        else if (lane == 1)
-          tma_load_2d_pair(kMode == kUp ? &tm_a1 : &tm_a0, bar, st + kBoxBytes, k * kBK, row_a1, pol);
-      }
-    }
-    __syncwarp();
-  } else if (warp == 2) {
-    // ------------------------------------------------ token-row producer (both CTAs)
-    if (lane == 0) prefetch_tensor_map(&tm_b);
-    const uint64_t pol_b = l2_policy_evict_normal();
-    int kb = 0;
-    bool alive = true;
-    for (int tile = pair; tile < total && alive; tile += npairs) {
-      const Tile c = tile_at(tile);
       const int half = c.N / 2;
       const int row0 = c.row0 + static_cast<int>(rank) * half;
       const int nbox = (half + kBRows - 1) / kBRows;
@@ -198,13 +169,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
-      const uint32_t b_bytes = kGather ? 2u * half * kBK : 2u * nbox * kBRows * kBK;
-      for (int k = 0; k < nk; ++k, ++kb) {
-        const int s = kb % kStagesB;
+      const uint32_t bytes = 2u * (C::kABytes + (kGather ? half : nbox * kBRows) * kBK);  // of both CTAs
+      for (int k = (warp + kProducers - it0 % kProducers) % kProducers; k < nk; k += kProducers) {
+        const int it = it0 + k, s = it % kStages;
         bool ok = true;
         if (lane == 0) {
-          ok = mbar_wait_bounded(&b_empty[s], ((kb / kStagesB) & 1) ^ 1, abort_flag);
-          if (ok && leader) mbar_arrive_expect_tx(&b_full[s], b_bytes);
+          ok = mbar_wait_bounded(&empty[s], ((it / kStages) & 1) ^ 1, abort_flag);
+          if (ok && leader) mbar_arrive_expect_tx(&full[s], bytes);
         }
         ok = __shfl_sync(0xffffffffu, ok, 0);
         if (!ok) {
@@ -215,22 +186,25 @@ __global__ void __launch_bounds__(kThreads, 1)
           alive = false;
           break;
         }
-        uint8_t* st = b_ring + s * C::kBStage;
+        uint8_t* st = ring + s * C::kStage;
+        const uint32_t bar = cluster_addr(&full[s], 0);
+        if (lane < 2)
+          tma_load_2d_pair(kMode == kUp && lane == 1 ? &tm_a1 : &tm_a0, bar, st + lane * kBoxBytes, k * kBK,
+                           lane == 0 ? row_a0 : row_a1, pol);
         if (kGather) {
           if (4 * lane < half)
-            tma_gather4_pair(&tm_b, cluster_addr(&b_full[s], 0), st + lane * 4 * kBK, k * kBK, tok[0], tok[1], tok[2],
-                             tok[3], pol_b);
+            tma_gather4_pair(&tm_b, bar, st + C::kABytes + lane * 4 * kBK, k * kBK, tok[0], tok[1], tok[2], tok[3],
+                             pol_b);
         } else if (lane < nbox) {
-          tma_load_2d_pair(&tm_b, cluster_addr(&b_full[s], 0), st + lane * kBRows * kBK, k * kBK,
-                           row0 + lane * kBRows, pol_b);
+          tma_load_2d_pair(&tm_b, bar, st + C::kABytes + lane * kBRows * kBK, k * kBK, row0 + lane * kBRows, pol_b);
         }
       }
     }
     __syncwarp();
-  } else if (warp == 1) {
+  } else if (warp == kMmaWarp) {
     // ------------------------------------------------ MMA issuer (leader only)
     if (leader && lane == 0) {
-      int ka = 0, kb = 0, j = 0;
+      int it = 0, j = 0;
       bool alive = true;
       for (int tile = pair; tile < total && alive; tile += npairs, ++j) {
         const uint32_t idesc = umma_idesc_s8(2 * kBM, tile_at(tile).N);
@@ -243,36 +217,34 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after_sync();
         const uint32_t d0 = tmem + buf * C::kAccCols;
         const uint32_t d1 = d0 + kNmax;
-        for (int k = 0; k < nk; ++k, ++ka, ++kb) {
-          const int sa = ka % kStagesA, sb = kb % kStagesB;
-          if (!mbar_wait_bounded(&a_full[sa], (ka / kStagesA) & 1, abort_flag) ||
-              !mbar_wait_bounded(&b_full[sb], (kb / kStagesB) & 1, abort_flag)) {
+        for (int k = 0; k < nk; ++k, ++it) {
+          const int s = it % kStages;
+          if (!mbar_wait_bounded(&full[s], (it / kStages) & 1, abort_flag)) {
             *abort_flag = 1;
             set_error(args.err, kErrTimeout);
             alive = false;
             break;
           }
           tc_fence_after_sync();
-          const uint64_t da0 = umma_desc_sw128(a_ring + sa * C::kAStage);
-          const uint64_t da1 = umma_desc_sw128(a_ring + sa * C::kAStage + kBoxBytes);
-          const uint64_t db = umma_desc_sw128(b_ring + sb * C::kBStage);
+          const uint64_t da0 = umma_desc_sw128(ring + s * C::kStage);
+          const uint64_t da1 = umma_desc_sw128(ring + s * C::kStage + kBoxBytes);
+          const uint64_t db = umma_desc_sw128(ring + s * C::kStage + C::kABytes);
 #pragma unroll
           for (int kk = 0; kk < kBK / 32; ++kk) {
             const uint32_t acc = (k | kk) != 0 ? 1u : 0u;
             umma_s8_pair(d0, da0 + 2 * kk, db + 2 * kk, idesc, acc);
             umma_s8_pair(d1, da1 + 2 * kk, db + 2 * kk, idesc, acc);
           }
-          umma_commit_pair(&a_empty[sa]);
-          umma_commit_pair(&b_empty[sb]);
+          umma_commit_pair(&empty[s]);
         }
         umma_commit_pair(&acc_full[buf]);  // also on an abort, so neither epilogue is left waiting
       }
     }
     __syncwarp();
-  } else if (warp >= 4) {
+  } else {
     // ------------------------------------------------ epilogue (both CTAs: their own 2 x 128 channels)
     const int q = warp & 3;
-    const int part_c = (warp - 4) >> 2;  // which of the four 16-column chunks of every 64 this warp drains
+    const int part_c = (warp - kFirstEpi) >> 2;  // which of the four 16-column chunks of every 64 this warp drains
     constexpr int kChunks = kNmax / 64;
     const int g8 = lane >> 3, b8 = lane & 7;
     int j = 0;
@@ -413,14 +385,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before_sync();
   __syncthreads();
   cluster_sync_all();  // neither CTA leaves while the other may still use its shared or tensor memory
-  if (warp == 1) tmem_dealloc_pair(tmem, 512);
+  if (warp == kMmaWarp) tmem_dealloc_pair(tmem, 512);
 }
 
-template <int kMode, bool kGather, int kNmax, int kStagesA, int kStagesB>
+template <int kMode, bool kGather, int kNmax, int kStages>
 cudaError_t launch_pairs(const CUtensorMap& a0, const CUtensorMap& a1, const CUtensorMap& b, const Int8GemmArgs& args,
                          int num_sms, cudaStream_t stream) {
-  using C = PCfg<kNmax, kStagesA, kStagesB>;
-  auto kern = int8_pair_kernel<kMode, kGather, kNmax, kStagesA, kStagesB>;
+  using C = PCfg<kNmax, kStages>;
+  auto kern = int8_pair_kernel<kMode, kGather, kNmax, kStages>;
   int dev = 0;
   cudaError_t st = cudaGetDevice(&dev);
   if (st != cudaSuccess) return st;
@@ -450,23 +422,23 @@ cudaError_t launch_pairs(const CUtensorMap& a0, const CUtensorMap& a1, const CUt
 cudaError_t launch_int8_pair_up(const CUtensorMap& w_gate, const CUtensorMap& w_up, const CUtensorMap& x_rows,
                                 const Int8GemmArgs& args, int nmax, bool gather, int num_sms, cudaStream_t stream) {
   if (nmax >= 256) {
-    if (gather) return launch_pairs<kUp, true, 256, 5, 3>(w_gate, w_up, x_rows, args, num_sms, stream);
-    return launch_pairs<kUp, false, 256, 5, 3>(w_gate, w_up, x_rows, args, num_sms, stream);
+    if (gather) return launch_pairs<kUp, true, 256, 4>(w_gate, w_up, x_rows, args, num_sms, stream);
+    return launch_pairs<kUp, false, 256, 4>(w_gate, w_up, x_rows, args, num_sms, stream);
   }
-  if (gather) return launch_pairs<kUp, true, 128, 5, 6>(w_gate, w_up, x_rows, args, num_sms, stream);
-  return launch_pairs<kUp, false, 128, 5, 6>(w_gate, w_up, x_rows, args, num_sms, stream);
+  if (gather) return launch_pairs<kUp, true, 128, 5>(w_gate, w_up, x_rows, args, num_sms, stream);
+  return launch_pairs<kUp, false, 128, 5>(w_gate, w_up, x_rows, args, num_sms, stream);
 }
 
 cudaError_t launch_int8_pair_down(const CUtensorMap& w_down, const CUtensorMap& h_rows, const Int8GemmArgs& args,
                                   int nmax, int num_sms, cudaStream_t stream) {
-  if (nmax >= 256) return launch_pairs<kDown, false, 256, 5, 3>(w_down, w_down, h_rows, args, num_sms, stream);
-  return launch_pairs<kDown, false, 128, 5, 6>(w_down, w_down, h_rows, args, num_sms, stream);
+  if (nmax >= 256) return launch_pairs<kDown, false, 256, 4>(w_down, w_down, h_rows, args, num_sms, stream);
+  return launch_pairs<kDown, false, 128, 5>(w_down, w_down, h_rows, args, num_sms, stream);
 }
 
 cudaError_t launch_int8_pair_dense(const CUtensorMap& w, const CUtensorMap& x_rows, const Int8GemmArgs& args,
                                    int num_sms, cudaStream_t stream) {
   if (args.tile_n < 32 || args.tile_n > 256 || args.tile_n % 32 != 0) return cudaErrorInvalidValue;
-  return launch_pairs<kDense, false, 256, 5, 3>(w, w, x_rows, args, num_sms, stream);
+  return launch_pairs<kDense, false, 256, 4>(w, w, x_rows, args, num_sms, stream);
 }
 
 }  // namespace moe
