@@ -688,26 +688,38 @@ bool linear_int8_shape_ok(int64_t M, int64_t N, int64_t K) {
 }
 int64_t linear_int8_pitch(int64_t K) { return (K + 15) / 16 * 16; }
 
-// Tokens per tile of the dense product on pairs (512 channels each), or 0 for the one-tile-per-CTA kernel, which
-// takes the sizes that cannot give every pair a tile.  Of the widths from 128 to 256 the one whose longest pair has
-// the fewest token columns to compute: whole tiles of 256 leave the last round of pairs short.
-int linear_int8_tile(int64_t M, int64_t N) {
+// Tokens per tile of the dense product on pairs (512 channels each), or 0 for the kernel with 128 channels x up to 128
+// tokens per CTA.  By estimated time, from measurements of both on 22 sizes (33 to 8192 tokens, 512 to 7168 channels
+// and columns; the estimates are within about 20 percent, the choice right or within 10 percent of the better one).
+// In us, nk = K / 128 steps:
+//   pairs:   4 + rounds of tiles over the pairs x (nk (0.48 + 0.0016 t) + 2) for t tokens per tile: whole tiles of
+//            256 leave a last round short, so t is chosen too;
+//   one CTA, split over a cluster of S:  nk/S (0.3 + 0.0045 t) + 6 + 0.05 t;  unsplit: rounds x (0.35 nk + 4.3).
+// Up to 32 tokens the weight stream of the CTAs wins throughout.
+int linear_int8_tile(int64_t M, int64_t N, int64_t K) {
   if (const char* env = std::getenv("MOE_INT8_TILE")) {
     const int v = std::atoi(env);
     if (v == 0 || (v >= 32 && v <= 256 && v % 32 == 0)) return v;
   }
-  const int64_t pairs = num_sms() / 2, W = (N + 511) / 512;
+  if (M <= 32) return 0;
+  const int sms = num_sms();
+  const int64_t pairs = sms / 2, W = (N + 511) / 512, nk = (K + 127) / 128;
   int best = 0;
-  int64_t best_cost = 0;
-  for (int t = 256; t >= 128; t -= 32) {
-    const int64_t rounds = (W * ((M + t - 1) / t) + pairs - 1) / pairs;
-    const int64_t cost = rounds * (t + 16);  // a tile's drain costs about 16 columns
+  double best_cost = 0.0;
+  for (int t = 64; t <= 256; t += 32) {
+    const double rounds = static_cast<double>((W * ((M + t - 1) / t) + pairs - 1) / pairs);
+    const double cost = 4.0 + rounds * (nk * (0.48 + 0.0016 * t) + 2.0);
     if (best == 0 || cost < best_cost) {
       best = t;
       best_cost = cost;
     }
   }
-  return W * ((M + best - 1) / best) >= pairs ? best : 0;
+  const int64_t tiles = (N + 127) / 128 * ((M + 127) / 128);
+  const int split = moe::int8_tile_split(tiles, static_cast<int>(nk), sms);
+  const double t = static_cast<double>(M >= 128 ? 128 : M);
+  const double single = split > 1 ? nk / split * (0.3 + 0.0045 * t) + 6.0 + 0.05 * t
+                                  : static_cast<double>((tiles + sms - 1) / sms) * (0.35 * nk + 4.3);
+  return best_cost < single ? best : 0;
 }
 
 // moe_route_logits' options, shape and logits: MOE_OK or the status of the call.
@@ -1220,7 +1232,7 @@ moe_status_t moe_linear_int8(const moe_bf16_t* x, int64_t ldx, const int8_t* w, 
   q.scales = reinterpret_cast<float*>(base + L.scales);
   if (moe::launch_quantize_int8(q, cs) != cudaSuccess) return MOE_ERR_CUDA;
   CUtensorMap mw, mx;
-  const int tile_n = linear_int8_tile(M, N);
+  const int tile_n = linear_int8_tile(M, N, K);
   if (!make_map_i8(&mw, w, N, K, ldw, 128) || !make_map_i8(&mx, q.codes, M, K, pitch, tile_n != 0 ? 32 : 16))
     return MOE_ERR_CUDA;
   moe::Int8GemmArgs a{};

@@ -92,6 +92,7 @@ __device__ __forceinline__ void write_codes(const uint4 (&v)[kVecs], const RowSc
 template <int kRowThreads>
 __global__ void __launch_bounds__(kQThreads) quantize_rows_kernel(Int8RowsArgs a) {
   __shared__ uint32_t part[kQThreads / 32];
+  grid_launch_dependents();  // the product that follows sets itself up and loads weights meanwhile
   const int tid = threadIdx.x % kRowThreads;
   const int64_t r = static_cast<int64_t>(blockIdx.x) * (kQThreads / kRowThreads) + threadIdx.x / kRowThreads;
   bool live = r < a.rows;
@@ -133,6 +134,7 @@ __global__ void __launch_bounds__(kQThreads) quantize_rows_kernel(Int8RowsArgs a
 // Any alignment and length: one CTA per row, two passes over it.
 __global__ void __launch_bounds__(kQThreads) quantize_any_kernel(Int8RowsArgs a) {
   __shared__ uint32_t part[kQThreads / 32];
+  grid_launch_dependents();
   const int tid = threadIdx.x;
   const int64_t r = blockIdx.x;
   if (a.sorted_ids != nullptr) {

@@ -16,6 +16,8 @@
 //    accumulator) runs under the next one's loads;
 //  * fewer (a dense layer for one token has N / 128 tiles): a cluster of S <= 8 CTAs takes a tile, each a share of K,
 //    and adds up the int32 partial sums through distributed shared memory: exact, in any order, no workspace.
+// Both overlap the quantiser before them (programmatic dependent launch): barriers, tensor memory, the tile list and
+// the first weight panels do not depend on it; token rows and scales are read after it has ended.
 #include <algorithm>
 
 #include "common.cuh"
@@ -191,6 +193,22 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int nk = k_hi - k_lo;
     int it0 = 0, issued = 0;  // k-steps before this tile; behind the last one that this warp issued
     bool alive = true;
+    // the weight panels of the first ring of k-steps, before the wait for the quantiser
+    const int ahead = min(nk, kStages);
+    {
+      const Tile c = tile_at(first);
+      const int a_row = c.e * args.rows_per_expert + c.w * kBM;
+      const uint64_t pol = c.count <= kNmax ? l2_policy_evict_first() : l2_policy_evict_normal();
+      if (lane == 0)
+        for (int i = warp; i < ahead; i += kProducers) {
+          uint8_t* st = stages + i * C::kStageBytes;
+          mbar_arrive_expect_tx(&full[i], C::kPanels * kATile + c.N * kBK);
+          tma_load_2d_hint(&tm_a0, &full[i], st, (k_lo + i) * kBK, a_row, pol);
+          if (kMode == kUp) tma_load_2d_hint(&tm_a1, &full[i], st + kATile, (k_lo + i) * kBK, a_row, pol);
+        }
+      __syncwarp();
+    }
+    grid_dependency_wait();
     for (int tile = first; tile < total && alive; tile += step, it0 += nk) {
       const Tile c = tile_at(tile);
       const int a_row = c.e * args.rows_per_expert + c.w * kBM;
@@ -207,8 +225,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       for (int i = (warp - it0) & (kProducers - 1); i < nk; i += kProducers) {
         const int it = it0 + i, s = it % kStages, k = k_lo + i;
+        uint8_t* st = stages + s * C::kStageBytes;
+        uint8_t* bt = st + C::kPanels * kATile;
+        const bool panels = it >= ahead;  // else they are on their way
         bool ok = true;
-        if (lane == 0) ok = mbar_wait_bounded(&empty[s], ((it / kStages) & 1) ^ 1, abort_flag);
+        if (panels && lane == 0) ok = mbar_wait_bounded(&empty[s], ((it / kStages) & 1) ^ 1, abort_flag);
         ok = __shfl_sync(0xffffffffu, ok, 0);
         if (!ok) {
           if (lane == 0) {
@@ -218,9 +239,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           alive = false;
           break;
         }
-        uint8_t* st = stages + s * C::kStageBytes;
-        uint8_t* bt = st + C::kPanels * kATile;
-        if (lane == 0) {
+        if (panels && lane == 0) {
           mbar_arrive_expect_tx(&full[s], C::kPanels * kATile + c.N * kBK);
           tma_load_2d_hint(&tm_a0, &full[s], st, k * kBK, a_row, pol);
           if (kMode == kUp) tma_load_2d_hint(&tm_a1, &full[s], st + kATile, k * kBK, a_row, pol);
@@ -288,6 +307,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
   } else {
     // ------------------------------------------------ epilogue: a warp reads the tensor-memory lanes of its quarter
+    grid_dependency_wait();
     const int q = warp & 3;
     int j = 0;
     for (int tile = first; tile < total; tile += step, ++j) {
@@ -392,13 +412,15 @@ cudaError_t launch_tiles(const CUtensorMap& a0, const CUtensorMap& a1, const CUt
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = C::kSmem;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = static_cast<unsigned>(args.split);
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = static_cast<unsigned>(args.split);
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = args.split > 1 ? 1 : 0;
+  cfg.numAttrs = args.split > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kern, a0, a1, b, args);
 }
 
@@ -417,9 +439,7 @@ cudaError_t launch_form(const CUtensorMap& a0, const CUtensorMap& a1, const CUte
   tiles *= W;
   if (tiles >= (1ll << 31)) return cudaErrorInvalidValue;
   const int nk = (args.kdim + kBK - 1) / kBK;
-  // CTAs that fit on the GPU at once, two per SM, shared out over the tiles; a share of K is at least two stages
-  args.split = 1;
-  while (args.split < 8 && 4 * args.split <= nk && 2 * args.split * tiles <= 2 * num_sms) args.split *= 2;
+  args.split = int8_tile_split(tiles, nk, num_sms);
   if (args.split > 1)
     return launch_tiles<kMode, kNmax, kShallow, 1>(a0, a1, b, args, static_cast<unsigned>(tiles * args.split), stream);
   return launch_tiles<kMode, kNmax, kDeep, kBufs>(a0, a1, b, args,
@@ -427,6 +447,12 @@ cudaError_t launch_form(const CUtensorMap& a0, const CUtensorMap& a1, const CUte
 }
 
 }  // namespace
+
+int int8_tile_split(long long tiles, int nk, int num_sms) {
+  int split = 1;
+  while (split < 8 && 4 * split <= nk && split * tiles <= num_sms) split *= 2;
+  return split;
+}
 
 cudaError_t launch_int8_up(const CUtensorMap& w_gate, const CUtensorMap& w_up, const CUtensorMap& x_rows,
                            const Int8GemmArgs& args, int nmax, int num_sms, cudaStream_t stream) {

@@ -16,7 +16,8 @@
 // as the bf16 pair kernels have, needs about 0.7 us for a stage however wide its tokens and wherever the weights are
 // (the wake-up of its wait and the issue of its copies in series): that alone held 8192 x 7168 x 7168 at 0.69 us per
 // k-step.
-// Every wait is bounded; a timeout sets the error word and unwinds, and both CTAs still meet at the last cluster
+// The launch overlaps the kernel before it (programmatic dependent launch): set-up and the first weight boxes come
+// before the wait for it.  Every mbarrier wait is bounded; a timeout sets the error word and unwinds, and both CTAs still meet at the last cluster
 // barrier.
 #include "common.cuh"
 #include "kernels.h"
@@ -148,6 +149,24 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint64_t pol_b = l2_policy_evict_normal();
     int it0 = 0;  // k-steps before this tile
     bool alive = true;
+    // the weight boxes of the first ring of k-steps, before the wait for the kernel that writes the token rows
+    const int ahead = min(nk, kStages);
+    {
+      const Tile c = tile_at(pair);
+      const uint64_t pol = c.count <= tw ? l2_policy_evict_first() : l2_policy_evict_normal();
+      const int row_a0 = c.e * args.rows_per_expert + c.w * kBlock + static_cast<int>(rank) * kBM;
+      const int row_a1 = kMode == kUp ? row_a0 : row_a0 + 2 * kBM;
+      const int half = c.N / 2, nbox = (half + kBRows - 1) / kBRows;
+      for (int k = warp; k < ahead; k += kProducers) {
+        if (leader && lane == 0)
+          mbar_arrive_expect_tx(&full[k], 2u * (C::kABytes + (kGather ? half : nbox * kBRows) * kBK));
+        __syncwarp();
+        if (lane < 2)
+          tma_load_2d_pair(kMode == kUp && lane == 1 ? &tm_a1 : &tm_a0, cluster_addr(&full[k], 0),
+                           ring + k * C::kStage + lane * kBoxBytes, k * kBK, lane == 0 ? row_a0 : row_a1, pol);
+      }
+    }
+    grid_dependency_wait();
     for (int tile = pair; tile < total && alive; tile += npairs, it0 += nk) {
       const Tile c = tile_at(tile);
       const uint64_t pol = c.count <= tw ? l2_policy_evict_first() : l2_policy_evict_normal();
@@ -172,8 +191,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t bytes = 2u * (C::kABytes + (kGather ? half : nbox * kBRows) * kBK);  // of both CTAs
       for (int k = (warp + kProducers - it0 % kProducers) % kProducers; k < nk; k += kProducers) {
         const int it = it0 + k, s = it % kStages;
+        const bool boxes = it >= ahead;  // else they are on their way
         bool ok = true;
-        if (lane == 0) {
+        if (boxes && lane == 0) {
           ok = mbar_wait_bounded(&empty[s], ((it / kStages) & 1) ^ 1, abort_flag);
           if (ok && leader) mbar_arrive_expect_tx(&full[s], bytes);
         }
@@ -188,7 +208,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         uint8_t* st = ring + s * C::kStage;
         const uint32_t bar = cluster_addr(&full[s], 0);
-        if (lane < 2)
+        if (boxes && lane < 2)
           tma_load_2d_pair(kMode == kUp && lane == 1 ? &tm_a1 : &tm_a0, bar, st + lane * kBoxBytes, k * kBK,
                            lane == 0 ? row_a0 : row_a1, pol);
         if (kGather) {
@@ -243,6 +263,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
   } else {
     // ------------------------------------------------ epilogue (both CTAs: their own 2 x 128 channels)
+    grid_dependency_wait();
     const int q = warp & 3;
     const int part_c = (warp - kFirstEpi) >> 2;  // which of the four 16-column chunks of every 64 this warp drains
     constexpr int kChunks = kNmax / 64;
@@ -407,13 +428,15 @@ cudaError_t launch_pairs(const CUtensorMap& a0, const CUtensorMap& a1, const CUt
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = C::kSmem;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = 2;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, kern, a0, a1, b, args);
 }
 

@@ -266,6 +266,10 @@ cudaError_t launch_int8_down(const CUtensorMap& w_down, const CUtensorMap& h_row
 cudaError_t launch_int8_dense(const CUtensorMap& w, const CUtensorMap& x_rows, const Int8GemmArgs& args, int nmax,
                               int num_sms, cudaStream_t stream);
 
+// CTAs that share the K of each of `tiles` tiles (a power of two up to 8): as many as two per SM hold, each with at
+// least two of the nk steps.
+int int8_tile_split(long long tiles, int nk, int num_sms);
+
 // int8_pair.cu: the same on 2-SM pairs.  Tensor maps: weights as above; token rows in 32-row boxes, or x codes in
 // one-row boxes (gather).
 cudaError_t launch_int8_pair_up(const CUtensorMap& w_gate, const CUtensorMap& w_up, const CUtensorMap& x_rows,
