@@ -263,18 +263,17 @@ def _device_of(*ts):
 def _launch(dev, what, *args):
     """Calls the library's function on the current stream of device ``dev`` (made current for the call if it is
     not): the stream is the last argument."""
-    fn = getattr(library(), what)
+    fn = getattr(_lib or library(), what)
     if dev == torch.cuda.current_device():
         status = fn(*args, _raw_stream(dev))
     else:
         with torch.cuda.device(dev):
             status = fn(*args, _raw_stream(dev))
-    if status != 0:
+    if status:
         raise MoEError(status, what)
 
 
-def _raw_stream(dev):
-    return torch._C._cuda_getCurrentRawStream(dev)
+_raw_stream = torch._C._cuda_getCurrentRawStream  # the cudaStream_t of a device's current stream, without a Stream object
 
 
 def _adr(t):
@@ -306,7 +305,7 @@ def route_logits(logits, bias, top_k, n_group=1, topk_group=1, group_score=GROUP
     _want(bias, torch.float32, (E,), "bias")
     topk_ids, topk_w = _routing_out(M, top_k, logits, topk_ids, topk_w)
     opts = _group_opts(n_group, topk_group, group_score, scoring, renormalize, routed_scale)
-    _launch(dev, "moe_route_logits", logits.data_ptr(), _DTYPES[logits.dtype], _row_stride(logits), _adr(bias), M, E,
+    _launch(dev, "moe_route_logits", logits.data_ptr(), _DTYPES[logits.dtype], _row_stride(logits, M, E), _adr(bias), M, E,
             top_k, opts, topk_ids.data_ptr(), topk_w.data_ptr())
     return topk_ids, topk_w
 
@@ -329,17 +328,21 @@ def route_group(x, w_router, bias, top_k, n_group=1, topk_group=1, group_score=G
     return topk_ids, topk_w
 
 
-def _row_stride(t):
-    """Elements between rows (any value fits a single row)."""
-    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+def _row_stride(t, rows, cols):
+    """Elements between the rows of t [rows, cols] (any value fits a single row)."""
+    return t.stride(0) if rows > 1 else cols
 
 
 def _routing_out(M, top_k, like, topk_ids, topk_w):
     if topk_ids is None:
-        topk_ids = like.new_empty((M, top_k), dtype=torch.int32)
+        topk_ids = torch.empty((M, top_k), dtype=torch.int32, device=like.device)
+    else:
+        _want(topk_ids, torch.int32, (M, top_k), "topk_ids")
     if topk_w is None:
-        topk_w = like.new_empty((M, top_k), dtype=torch.float32)
-    return _want(topk_ids, torch.int32, (M, top_k), "topk_ids"), _want(topk_w, torch.float32, (M, top_k), "topk_w")
+        topk_w = torch.empty((M, top_k), dtype=torch.float32, device=like.device)
+    else:
+        _want(topk_w, torch.float32, (M, top_k), "topk_w")
+    return topk_ids, topk_w
 
 
 def align_block_size(topk_ids, E, block_size, err_flag=None, out=None):
@@ -636,14 +639,16 @@ def linear_int8(x, codes, scales, out=None, out_dtype=torch.bfloat16, ws=None, e
     if out is None:
         if out_dtype not in _DTYPES:
             raise ValueError("out_dtype: expected torch.bfloat16 or torch.float32")
-        out = x.new_empty((M, N), dtype=out_dtype)
+        out = torch.empty((M, N), dtype=out_dtype, device=x.device)
     elif out.dtype not in _DTYPES or out.shape != (M, N) or (N > 1 and out.stride(1) != 1):
         raise ValueError("out: expected a bf16 or fp32 [M, N] tensor with contiguous rows")
     ldw = codes.stride(0) if N > 1 else (max(codes.stride(0), K) + 15) // 16 * 16
-    if ws is None:
-        ws = x.new_empty(max(linear_int8_workspace_size(M, N, K), 1), dtype=torch.uint8)
-    _launch(dev, "moe_linear_int8", x.data_ptr(), _row_stride(x), codes.data_ptr(), ldw, scales.data_ptr(), M, N, K,
-            out.data_ptr(), _row_stride(out), _DTYPES[out.dtype], ws.data_ptr(), ws.numel(), _adr(err_flag))
+    need = linear_int8_workspace_size(M, N, K)
+    if ws is None and need:
+        ws = x.new_empty(need, dtype=torch.uint8)
+    _launch(dev, "moe_linear_int8", x.data_ptr(), _row_stride(x, M, K), codes.data_ptr(), ldw, scales.data_ptr(), M, N, K,
+            out.data_ptr(), _row_stride(out, M, N), _DTYPES[out.dtype], _adr(ws), 0 if ws is None else ws.numel(),
+            _adr(err_flag))
     return out
 
 

@@ -1207,7 +1207,8 @@ moe_status_t moe_quantize_int8(const moe_bf16_t* src, int64_t ld, int64_t rows, 
 }
 
 size_t moe_linear_int8_workspace_size(int64_t M, int64_t N, int64_t K) {
-  return linear_int8_shape_ok(M, N, K) ? int8_layout(M, linear_int8_pitch(K)).total : 0;
+  if (!linear_int8_shape_ok(M, N, K) || moe::int8_few_takes(M, K)) return 0;
+  return int8_layout(M, linear_int8_pitch(K)).total;
 }
 
 moe_status_t moe_linear_int8(const moe_bf16_t* x, int64_t ldx, const int8_t* w, int64_t ldw, const float* w_scale,
@@ -1217,26 +1218,10 @@ moe_status_t moe_linear_int8(const moe_bf16_t* x, int64_t ldx, const int8_t* w, 
   if (!x || !w || !w_scale || !out) return MOE_ERR_INVALID_ARG;
   if (out_dtype != MOE_DT_F32 && out_dtype != MOE_DT_BF16) return MOE_ERR_INVALID_ARG;
   if (ldx < K || ldw < K || ldo < N || ldw % 16 != 0 || !aligned16(w)) return MOE_ERR_INVALID_ARG;
-  if (!ws || ws_bytes < moe_linear_int8_workspace_size(M, N, K) || !aligned16(ws)) return MOE_ERR_WORKSPACE;
+  const bool few = moe::int8_few_takes(M, K);
+  if (!few && (!ws || ws_bytes < moe_linear_int8_workspace_size(M, N, K) || !aligned16(ws))) return MOE_ERR_WORKSPACE;
   auto cs = static_cast<cudaStream_t>(stream);
-  const int64_t pitch = linear_int8_pitch(K);
-  const Int8Layout L = int8_layout(M, pitch);
-  auto* base = static_cast<uint8_t*>(ws);
-  moe::Int8RowsArgs q{};
-  q.src = x;
-  q.ld = ldx;
-  q.rows = M;
-  q.cols = static_cast<int>(K);
-  q.codes = reinterpret_cast<int8_t*>(base + L.codes);
-  q.pitch = pitch;
-  q.scales = reinterpret_cast<float*>(base + L.scales);
-  if (moe::launch_quantize_int8(q, cs) != cudaSuccess) return MOE_ERR_CUDA;
-  CUtensorMap mw, mx;
-  const int tile_n = linear_int8_tile(M, N, K);
-  if (!make_map_i8(&mw, w, N, K, ldw, 128) || !make_map_i8(&mx, q.codes, M, K, pitch, tile_n != 0 ? 32 : 16))
-    return MOE_ERR_CUDA;
   moe::Int8GemmArgs a{};
-  a.row_scale = q.scales;
   a.ch_scale0 = w_scale;
   a.ch_scale1 = w_scale;
   a.out = out;
@@ -1248,6 +1233,24 @@ moe_status_t moe_linear_int8(const moe_bf16_t* x, int64_t ldx, const int8_t* w, 
   a.top_k = 1;
   a.rows_per_expert = static_cast<int>(N);
   a.kdim = static_cast<int>(K);
+  if (few) return cuda_status(moe::launch_int8_few(x, ldx, w, ldw, a, num_sms(), cs));
+  const int64_t pitch = linear_int8_pitch(K);
+  const Int8Layout L = int8_layout(M, pitch);
+  auto* base = static_cast<uint8_t*>(ws);
+  moe::Int8RowsArgs q{};
+  q.src = x;
+  q.ld = ldx;
+  q.rows = M;
+  q.cols = static_cast<int>(K);
+  q.codes = reinterpret_cast<int8_t*>(base + L.codes);
+  q.pitch = pitch;
+  q.scales = reinterpret_cast<float*>(base + L.scales);
+  a.row_scale = q.scales;
+  if (moe::launch_quantize_int8(q, cs) != cudaSuccess) return MOE_ERR_CUDA;
+  const int tile_n = linear_int8_tile(M, N, K);
+  CUtensorMap mw, mx;
+  if (!make_map_i8(&mw, w, N, K, ldw, 128) || !make_map_i8(&mx, q.codes, M, K, pitch, tile_n != 0 ? 32 : 16))
+    return MOE_ERR_CUDA;
   // 16-byte row stores need whole, aligned vectors of 8 bf16 values
   a.out_plain = a.out_f32 || N % 8 != 0 || ldo % 8 != 0 || !aligned16(out);
   a.tile_n = tile_n;

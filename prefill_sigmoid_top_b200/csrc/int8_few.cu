@@ -1,0 +1,209 @@
+// The dense int8 product for one or two tokens in ONE launch, without the tensor cores: a decode step's projection reads
+// little but its weights (2048 x 7168: 2.2 us at HBM speed), so what counts is the chain from launch to result.  A
+// quantiser of its own, TMA rings, tensor memory and a split over a cluster make that chain 8.7 us (two launches) or
+// 9.2 us (one, with the rows quantised inside and the sums joined through distributed shared memory); this kernel
+// takes the weights straight into registers and multiplies with dp4a: 5.7 us.  (40000 x 7168: 44.6 us, 6.4 TB/s.)
+// Every CTA's own pass over the rows costs more with each row (2048 x 7168: 2 tokens 10.4 us, 4 16 us, 8 26 us; as two
+// launches 10.0 us for any of these), so two tokens, where one launch less on the host decides, are the end of it.
+//
+// Every CTA quantises the token rows for itself into shared memory (14 KB read per row of 7168, from L2), while its
+// first weight loads are on their way.  Then its 8 warps take output channels: 8 / kWays channels at a time, kWays
+// warps on one channel, each lane 16 codes at a time against every token's codes (dp4a: four exact products added to
+// an int32 sum).  Codes, scales and sums are those of the other forms, so the results are the same bits.
+#include <algorithm>
+
+#include "int8_rows.cuh"
+#include "kernels.h"
+
+namespace moe {
+namespace {
+
+constexpr int kWarps = 8;
+constexpr int kThreads = 32 * kWarps;
+constexpr int kMaxRows = 2;
+constexpr int kAhead = 8;               // 16-byte weight loads in flight per lane
+constexpr int kMaxRowBytes = 64 * 1024;  // codes of all rows in shared memory
+constexpr int kCtasPerSm = 4;
+
+__device__ __forceinline__ uint4 load_weights(const int8_t* p) {
+  uint4 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
+}
+
+__device__ __forceinline__ int dot16(const uint4& a, const uint4& b, int c) {
+  c = __dp4a(static_cast<int>(a.x), static_cast<int>(b.x), c);
+  c = __dp4a(static_cast<int>(a.y), static_cast<int>(b.y), c);
+  c = __dp4a(static_cast<int>(a.z), static_cast<int>(b.z), c);
+  return __dp4a(static_cast<int>(a.w), static_cast<int>(b.w), c);
+}
+
+// kRows: tokens.
+template <int kRows>
+__global__ void __launch_bounds__(kThreads) int8_few_kernel(const uint16_t* __restrict__ x, int64_t ldx, bool vectors,
+                                                            const int8_t* __restrict__ w, int64_t ldw, int ways,
+                                                            const Int8GemmArgs args) {
+  extern __shared__ __align__(16) uint8_t codes[];  // [kRows][chunks * 16]
+  __shared__ uint32_t top[kWarps][kRows];
+  __shared__ RowScale row_scale[kRows];
+  __shared__ float scale[kRows];
+  __shared__ int part[kWarps][kRows];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int M = args.M, N = args.rows_per_expert, K = args.kdim;
+  const int chunks = (K + 15) / 16;  // of 16 codes
+  const int pitch = chunks * 16;
+  const int at_once = kWarps / ways;  // channels of the CTA
+  const int way = warp % ways, mine = warp / ways;
+  const int first = lane + 32 * way, step = 32 * ways;  // this lane's chunks
+
+  // the first weights: they wait for nothing (a channel past the last reads the last one's and stores nothing)
+  uint4 a[kAhead];
+  auto fetch = [&](int group, int c0) {
+    const int8_t* row = w + static_cast<int64_t>(min(group * at_once + mine, N - 1)) * ldw;
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i)
+      a[i] = c0 + step * i < chunks ? load_weights(row + 16 * static_cast<int64_t>(c0 + step * i)) : make_uint4(0, 0, 0, 0);
+  };
+  const int groups = (N + at_once - 1) / at_once;
+  int group = blockIdx.x;
+  fetch(group, first);
+
+  // ---- token rows -> codes
+#pragma unroll
+  for (int m = 0; m < kRows; ++m) {
+    uint32_t t = 0;
+    if (m < M) {
+      if (vectors) {
+        const uint4* src = reinterpret_cast<const uint4*>(x + m * ldx);
+#pragma unroll 4
+        for (int c = tid; c < K / 8; c += kThreads) {
+          const uint4 v = src[c];
+          t = max_bits(max_bits(max_bits(max_bits(t, v.x), v.y), v.z), v.w);
+        }
+      } else {
+        for (int c = tid; c < K; c += kThreads) t = max(t, static_cast<uint32_t>(x[m * ldx + c] & 0x7fffu));
+      }
+    }
+    t = __reduce_max_sync(0xffffffffu, t);
+    if (lane == 0) top[warp][m] = t;
+  }
+  __syncthreads();
+  if (tid < kRows) {
+    uint32_t t = 0;
+#pragma unroll
+    for (int q = 0; q < kWarps; ++q) t = max(t, top[q][tid]);
+    row_scale[tid] = row_scale_of(t);
+    scale[tid] = scale_value(t);
+  }
+  __syncthreads();
+#pragma unroll
+  for (int m = 0; m < kRows; ++m) {
+    uint8_t* dst = codes + m * pitch;
+    const RowScale s = row_scale[m];
+    if (m < M && vectors) {
+      const uint4* src = reinterpret_cast<const uint4*>(x + m * ldx);
+#pragma unroll 4
+      for (int c = tid; c < pitch / 8; c += kThreads) {
+        uint2 o = make_uint2(0, 0);
+        if (c < K / 8) {
+          const uint4 v = src[c];
+          o = s.c != 0.0f ? codes_of_8<true>(v, s) : codes_of_8<false>(v, s);
+        }
+        reinterpret_cast<uint2*>(dst)[c] = o;
+      }
+    } else {
+      for (int c = tid; c < pitch; c += kThreads)
+        dst[c] = m < M && c < K ? static_cast<uint8_t>(code_of_1(x[m * ldx + c], s)) : 0;
+    }
+  }
+  __syncthreads();
+
+  // ---- channels
+  for (; group < groups; group += gridDim.x) {
+    int acc[kRows];
+#pragma unroll
+    for (int m = 0; m < kRows; ++m) acc[m] = 0;
+    for (int c0 = first; c0 < chunks; c0 += step * kAhead) {
+      if (c0 != first) fetch(group, c0);
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        const int c = c0 + step * i;
+        if (c < chunks) {
+#pragma unroll
+          for (int m = 0; m < kRows; ++m)
+            acc[m] = dot16(a[i], *reinterpret_cast<const uint4*>(codes + m * pitch + 16 * c), acc[m]);
+        }
+      }
+    }
+    const int n = group * at_once + mine;
+    if (group + static_cast<int>(gridDim.x) < groups) fetch(group + gridDim.x, first);
+#pragma unroll
+    for (int m = 0; m < kRows; ++m) acc[m] = __reduce_add_sync(0xffffffffu, acc[m]);
+    if (ways > 1) {
+      if (lane == 0) {
+#pragma unroll
+        for (int m = 0; m < kRows; ++m) part[warp][m] = acc[m];
+      }
+      __syncthreads();
+    }
+    if (way == 0 && lane < M && n < N) {
+      int sum = 0;
+      if (ways > 1) {
+        for (int q = 0; q < ways; ++q) sum += part[warp + q][lane];
+      } else {
+#pragma unroll
+        for (int m = 0; m < kRows; ++m) sum = lane == m ? acc[m] : sum;
+      }
+      const float v = (scale[lane] * args.ch_scale0[n]) * static_cast<float>(sum);
+      const size_t at = static_cast<size_t>(lane) * args.out_ld + n;
+      if (args.out_f32)
+        static_cast<float*>(args.out)[at] = v;
+      else
+        static_cast<__nv_bfloat16*>(args.out)[at] = __float2bfloat16_rn(v);
+    }
+    if (ways > 1) __syncthreads();  // the partial sums are read
+  }
+}
+
+template <int kRows>
+cudaError_t launch_rows(const uint16_t* x, int64_t ldx, const int8_t* w, int64_t ldw, const Int8GemmArgs& args,
+                        int num_sms, cudaStream_t stream) {
+  auto kern = int8_few_kernel<kRows>;
+  int dev = 0;
+  cudaError_t st = cudaGetDevice(&dev);
+  if (st != cudaSuccess) return st;
+  static bool done[64] = {};
+  if (dev >= 64 || !done[dev]) {
+    st = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxRowBytes);
+    if (st != cudaSuccess) return st;
+    if (dev < 64) done[dev] = true;
+  }
+  const int N = args.rows_per_expert, K = args.kdim;
+  // few channels: several warps on one, as long as every SM still has work for its CTAs
+  int ways = 1;
+  while (ways < kWarps && static_cast<long long>(N) * 2 * ways <= static_cast<long long>(kWarps) * kCtasPerSm * num_sms &&
+         64 * 16 * ways <= K)
+    ways *= 2;
+  const int groups = (N + kWarps / ways - 1) / (kWarps / ways);
+  const bool vectors = K % 8 == 0 && ldx % 8 == 0 && (reinterpret_cast<uintptr_t>(x) & 15u) == 0;
+  const size_t smem = static_cast<size_t>(kRows) * ((K + 15) / 16 * 16);
+  kern<<<std::min(groups, kCtasPerSm * num_sms), kThreads, smem, stream>>>(x, ldx, vectors, w, ldw, ways, args);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+bool int8_few_takes(int64_t M, int64_t K) {
+  if (M > kMaxRows) return false;
+  return M * ((K + 15) / 16 * 16) <= kMaxRowBytes;
+}
+
+cudaError_t launch_int8_few(const uint16_t* x, int64_t ldx, const int8_t* w, int64_t ldw, const Int8GemmArgs& args,
+                            int num_sms, cudaStream_t stream) {
+  if (args.M <= 1) return launch_rows<1>(x, ldx, w, ldw, args, num_sms, stream);
+  return launch_rows<kMaxRows>(x, ldx, w, ldw, args, num_sms, stream);
+}
+
+}  // namespace moe

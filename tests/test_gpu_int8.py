@@ -114,6 +114,36 @@ def test_linear(M, N, K, out):
     linear_case(M, N, K, out, seed=M + N + K)
 
 
+@pytest.mark.parametrize("M", [1, 2, 3, 9])
+@pytest.mark.parametrize("N,K", [(1, 128), (100, 15), (640, 1792), (5000, 256), (2048, 7168), (257, 8200), (40000, 96),
+                                 (128, 14336), (3, 70000)])
+def test_linear_few_tokens(M, N, K):
+    """One or two tokens: one launch, one or several warps to a channel, odd lengths, too long for it; and the same bits
+    as the two-launch form gives for these rows among others."""
+    linear_case(M, N, K, torch.float32, pad=(K + M) % 3, seed=M + N)
+    x = torch.randn(40, K, generator=gen(M)).to(torch.bfloat16).to(DEV)
+    codes, scales = codes_of(N, K, M)
+    wide = torch.zeros(N, (K + 15) // 16 * 16, dtype=torch.int8, device=DEV)[:, :K]
+    wide.copy_(codes)
+    scales = scales.to(DEV)
+    assert torch.equal(moe.linear_int8(x[:M], wide, scales), moe.linear_int8(x, wide, scales)[:M])
+
+
+@pytest.mark.parametrize("tile", ["0", "32", "96", "256"])
+@pytest.mark.parametrize("M,N,K", [(20, 7, 40), (70, 1000, 300), (600, 2600, 128), (333, 513, 1777)])
+def test_linear_tile_widths(M, N, K, tile, monkeypatch):
+    monkeypatch.setenv("MOE_INT8_TILE", tile)
+    for out in (torch.bfloat16, torch.float32):
+        linear_case(M, N, K, out, seed=M)
+
+
+def test_linear_pairs_many_tiles():
+    """More tiles than pairs of SMs: the pairs take several, their accumulators in turn."""
+    linear_case(2500, 6000, 130, torch.bfloat16, seed=1)
+    linear_case(2500, 6001, 130, torch.bfloat16, seed=2)
+    linear_case(1300, 6000, 400, torch.float32, seed=3)
+
+
 @pytest.mark.parametrize("M", [1, 5, 40, 300])
 @pytest.mark.parametrize("pad,off", [(3, 0), (1, 1), (8, 8), (0, 2)])
 def test_linear_strided_rows(M, pad, off):
@@ -264,10 +294,16 @@ def test_experts(M, H, I, E, K, B, skew):
     check_down(shape, h, plan, mats, iw)
 
 
-@pytest.mark.parametrize("nmax", ["32", "128"])
-def test_experts_token_tile_widths(nmax, monkeypatch):
+@pytest.mark.parametrize("M", [3, 150, 700])
+@pytest.mark.parametrize("nmax,pair,gather", [("32", "0", "0"), ("128", "0", "0"), ("128", "128", "0"),
+                                              ("128", "128", "1"), ("128", "256", "0"), ("128", "256", "1")])
+def test_experts_token_tile_widths(nmax, pair, gather, M, monkeypatch):
+    """Every kernel takes every shape: one tile per CTA of 32 or 128 tokens, pairs of 128 or 256, rows gathered in the
+    GEMM or before it."""
     monkeypatch.setenv("MOE_GEMM_NMAX", nmax)
-    shape = moe.Shape(150, 512, 384, 5, 2, 16)
+    monkeypatch.setenv("MOE_GEMM_PAIR", pair)
+    monkeypatch.setenv("MOE_PAIR_GATHER", gather)
+    shape = moe.Shape(M, 512, 384, 5, 2, 16)
     x, ids, plan, mats, iw = experts_case(shape, seed=3, skew=1.0)
     check_up(shape, x, plan, mats, iw)
     check_down(shape, torch.randn(moe.align_capacity(shape), 384).to(torch.bfloat16).to(DEV), plan, mats, iw)

@@ -51,7 +51,7 @@ def test_quantize_refusals():
     assert q(cols=131073, ld=131073, pitch=131073) == 2
 
 
-def linear(x=FAKE, ldx=64, w=FAKE, ldw=64, sc=FAKE, M=4, N=8, K=64, out=FAKE, ldo=8, dt=1, ws=FAKE, n=1 << 20):
+def linear(x=FAKE, ldx=64, w=FAKE, ldw=64, sc=FAKE, M=40, N=8, K=64, out=FAKE, ldo=8, dt=1, ws=FAKE, n=1 << 20):
     return moe.library().moe_linear_int8(x, ldx, w, ldw, sc, M, N, K, out, ldo, dt, ws, n, None, None)
 
 
@@ -63,7 +63,9 @@ def test_linear_refusals():
     assert linear(M=2 ** 30 + 1) == 2 and linear(M=2 ** 30, N=2 ** 30, ldo=2 ** 30) == 2
     assert linear(ws=None) == 3 and linear(ws=FAKE_MIS) == 3 and linear(n=16) == 3
     assert moe.linear_int8_workspace_size(0, 1, 1) == 0
-    assert moe.linear_int8_workspace_size(4, 8, 65) >= 4 * 80 + 16
+    assert moe.linear_int8_workspace_size(40, 8, 65) >= 40 * 80 + 160
+    assert moe.linear_int8_workspace_size(1, 2048, 7168) == 0  # few tokens: one launch, nothing to keep
+    assert moe.linear_int8_workspace_size(1, 2048, 131072) > 0
 
 
 def test_expert_refusals():
