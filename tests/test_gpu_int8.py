@@ -309,6 +309,14 @@ def test_experts_token_tile_widths(nmax, pair, gather, M, monkeypatch):
     check_down(shape, torch.randn(moe.align_capacity(shape), 384).to(torch.bfloat16).to(DEV), plan, mats, iw)
 
 
+def test_experts_same_expert_twice_for_a_token():
+    ids = torch.tensor([[2, 2, 0], [2, 2, 2]], dtype=torch.int32)
+    shape = moe.Shape(2, 256, 128, 4, 3, 16)
+    x, ids, plan, mats, iw = experts_case(shape, seed=6, ids=ids)
+    check_up(shape, x, plan, mats, iw)
+    check_down(shape, torch.randn(moe.align_capacity(shape), 128).to(torch.bfloat16).to(DEV), plan, mats, iw)
+
+
 def test_experts_without_tokens_and_all_tokens_on_one():
     for ids in (torch.full((70, 1), 3, dtype=torch.int32), torch.tensor([[0], [9]], dtype=torch.int32)):
         shape = moe.Shape(ids.shape[0], 256, 128, 10, 1, 16)
