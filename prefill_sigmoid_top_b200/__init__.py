@@ -306,7 +306,7 @@ def route_logits(logits, bias, top_k, n_group=1, topk_group=1, group_score=GROUP
     topk_ids, topk_w = _routing_out(M, top_k, logits, topk_ids, topk_w)
     opts = _group_opts(n_group, topk_group, group_score, scoring, renormalize, routed_scale)
     _launch(dev, "moe_route_logits", logits.data_ptr(), _DTYPES[logits.dtype], _row_stride(logits, M, E), _adr(bias), M, E,
-            top_k, opts, topk_ids.data_ptr(), topk_w.data_ptr())
+            int(top_k), opts, topk_ids.data_ptr(), topk_w.data_ptr())
     return topk_ids, topk_w
 
 
@@ -659,6 +659,8 @@ def grouped_up_swiglu_int8(x, iw: Int8Weights, plan, shape: Shape, h=None, err_f
     _want(x, torch.bfloat16, (shape.M, shape.H), "x")
     if h is None:
         h = x.new_empty((align_capacity(shape), shape.I))
+    elif h.numel() < align_capacity(shape) * shape.I:
+        raise ValueError("h: expected align_capacity(shape) rows of I")
     if ws is None:
         ws = x.new_empty(max(up_workspace_size(shape, MOE_W_INT8), 1), dtype=torch.uint8)
     _launch(dev, "moe_grouped_up_swiglu", x.data_ptr(), ctypes.byref(iw.c()), ctypes.byref(_plan_struct(plan)),
@@ -670,8 +672,12 @@ def grouped_down_int8(h, iw: Int8Weights, plan, shape: Shape, y=None, err_flag=N
     """int8 form of grouped_down (the real plan rows of h quantised on the fly into ws)."""
     ts = iw.check(shape, "down")
     dev = _device_of(h, *ts, plan["sorted_ids"], y, err_flag, ws)
+    if h.numel() < align_capacity(shape) * shape.I:
+        raise ValueError("h: expected align_capacity(shape) rows of I")
     if y is None:
         y = h.new_empty((shape.M * shape.top_k, shape.H))
+    elif y.numel() != shape.M * shape.top_k * shape.H:
+        raise ValueError("y: expected M * top_k rows of H")
     if ws is None:
         ws = h.new_empty(max(down_workspace_size(shape, MOE_W_INT8), 1), dtype=torch.uint8)
     _launch(dev, "moe_grouped_down", _bf16(h).data_ptr(), ctypes.byref(iw.c()), ctypes.byref(_plan_struct(plan)),
@@ -693,6 +699,12 @@ def layer_int8(x, w_router, bias, iw: Int8Weights, gamma, eps, top_k, block_size
         ws = x.new_empty(max(layer_workspace_size(shape, MOE_W_INT8), 1), dtype=torch.uint8)
     if out is None:
         out = torch.empty_like(x)
+    _want(w_router, torch.bfloat16, (E, H), "w_router")
+    _want(bias, torch.float32, (E,), "bias")
+    _want(gamma, torch.bfloat16, (H,), "gamma")
+    for t, dtype, cols, what in ((out, torch.bfloat16, H, "out"), (residual_out, torch.bfloat16, H, "residual_out"),
+                                 (topk_ids, torch.int32, top_k, "topk_ids"), (topk_w, torch.float32, top_k, "topk_w")):
+        _want(t, dtype, (M, cols), what)
     _launch(dev, "moe_layer", _bf16(x).data_ptr(), _bf16(w_router).data_ptr(), _adr(bias), ctypes.byref(iw.c()),
             _bf16(gamma).data_ptr(), float(eps), shape.c(), out.data_ptr(), _adr(residual_out), _adr(topk_ids),
             _adr(topk_w), ws.data_ptr(), ws.numel())

@@ -108,7 +108,7 @@ def linear_case(M, N, K, out=torch.bfloat16, pad=0, off=0, seed=0):
 @pytest.mark.parametrize("M,N,K", [
     (1, 1, 1), (1, 128, 128), (1, 2048, 7168), (2, 7168, 2048), (3, 131, 77), (16, 257, 129), (17, 640, 1000),
     (31, 129, 4097), (32, 512, 512), (33, 513, 511), (100, 300, 260), (128, 128, 128), (129, 1025, 2047),
-    (255, 96, 33), (256, 1024, 640), (300, 1, 50), (513, 2049, 1777), (1000, 33, 7168), (1, 5, 131072),
+    (255, 96, 33), (256, 1024, 640), (300, 1, 50), (40, 5, 1), (3, 200, 2), (4, 128, 131072), (513, 2049, 1777), (1000, 33, 7168), (1, 5, 131072),
 ])
 def test_linear(M, N, K, out):
     linear_case(M, N, K, out, seed=M + N + K)
@@ -367,6 +367,64 @@ def test_layer_is_its_steps(M):
     y = moe.grouped_down_int8(h, iw, plan, shape)
     want = moe.finalize_rmsnorm(d["x"], y.view(M, cfg.K, cfg.H), w, d["gamma"], cfg.eps)
     assert torch.equal(ids, ids2) and torch.equal(out, want)
+    # every output, no bias, buffers of the caller
+    res, w2 = torch.empty_like(out), torch.empty_like(w)
+    out2 = torch.empty_like(out)
+    moe.layer_int8(d["x"], d["w_router"], None, iw, d["gamma"], cfg.eps, cfg.K, cfg.B, out=out2, residual_out=res,
+                   topk_ids=ids, topk_w=w2)
+    ids3, w3 = moe.route(d["x"], d["w_router"], torch.zeros_like(d["bias"]), cfg.K)
+    plan = moe.align_block_size(ids3, cfg.E, cfg.B)
+    y = moe.grouped_down_int8(moe.grouped_up_swiglu_int8(d["x"], iw, plan, shape), iw, plan, shape)
+    want, want_res = moe.finalize_rmsnorm(d["x"], y.view(M, cfg.K, cfg.H), w3, d["gamma"], cfg.eps, want_residual=True)
+    assert torch.equal(ids, ids3) and torch.equal(w2, w3) and torch.equal(out2, want) and torch.equal(res, want_res)
+
+
+@pytest.mark.parametrize("M", [6, 200])
+def test_experts_on_two_streams_at_once(M):
+    """Two projections at a time, each with its own workspace, give what each gives alone."""
+    shape = moe.Shape(M, 1024, 512, 12, 3, 16)
+    x, ids, plan, mats, iw = experts_case(shape, seed=31)
+    x2 = torch.randn(M, 1024, generator=gen(32)).to(torch.bfloat16).to(DEV)
+    x1 = x.to(DEV)
+    want1, want2 = (moe.grouped_up_swiglu_int8(t, iw, plan, shape) for t in (x1, x2))
+    real = torch.zeros(want1.shape[0], dtype=torch.bool, device=DEV)
+    for e in range(12):
+        o, c = int(plan["expert_offsets"][e]), int(plan["expert_counts"][e])
+        real[o:o + c] = True
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    got = []
+    for _ in range(20):
+        with torch.cuda.stream(side):
+            a = moe.grouped_up_swiglu_int8(x2, iw, plan, shape)
+        got.append((moe.grouped_up_swiglu_int8(x1, iw, plan, shape), a))
+    torch.cuda.synchronize()
+    for a, b in got:
+        assert torch.equal(a[real], want1[real]) and torch.equal(b[real], want2[real])
+
+
+@pytest.mark.parametrize("M", [3, 300])
+def test_experts_with_rows_that_are_not_numbers(M):
+    """A token with an infinity or a NaN spoils its own rows only, a token of zeros gives zeros."""
+    shape = moe.Shape(M, 512, 256, 6, 2, 16)
+    x, ids, plan, mats, iw = experts_case(shape, seed=33)
+    good = moe.grouped_up_swiglu_int8(x.to(DEV), iw, plan, shape)
+    bad = x.clone()
+    bad[0, 5], bad[1, 7], bad[2] = float("inf"), float("nan"), 0.0
+    h = moe.grouped_up_swiglu_int8(bad.to(DEV), iw, plan, shape)
+    y = moe.grouped_down_int8(h, iw, plan, shape).view(M, 2, 512)
+    sid = plan["sorted_ids"].cpu()
+    for e in range(6):
+        o, c = int(plan["expert_offsets"][e]), int(plan["expert_counts"][e])
+        for r in range(o, o + c):
+            t = int(sid[r]) // 2
+            if t < 2:
+                assert h[r].isnan().all()
+            elif t == 2:
+                assert (h[r] == 0).all()
+            else:
+                assert torch.equal(h[r], good[r])
+    assert y[:2].isnan().all() and (y[2] == 0).all() and y[3:].isfinite().all()
 
 
 @pytest.mark.parametrize("M", [1, 37, 300])

@@ -118,6 +118,8 @@ def test_binding_refusals():
     assert len(iw.check(S, "gate")) == 2
     with pytest.raises(ValueError):
         iw.check(S, "up")
+    with pytest.raises(ValueError):
+        moe.layer_int8(cpu, cpu, None, iw, cpu, 1e-5, 2, 16)
     iw.gate_scales = torch.zeros(8, 127)
     with pytest.raises(ValueError):
         iw.check(S, "gate")
