@@ -571,7 +571,7 @@ moe_status_t run_down_nvfp4(const moe_bf16_t* h, const moe_weights_t* w, const m
 // ---------------------------------------------------------------- int8 rows
 // Workspace of an int8 projection: row scales, then codes of the activation rows (pitch bytes each).
 struct Int8Layout {
-  size_t scales, codes, gathered, total;  // gathered (up): codes in plan order
+  size_t scales, codes, total;
 };
 Int8Layout int8_layout(size_t rows, size_t pitch) {
   Int8Layout L{};
@@ -579,17 +579,7 @@ Int8Layout int8_layout(size_t rows, size_t pitch) {
   L.total = align_up(L.codes + rows * pitch);
   return L;
 }
-// Whether the int8 up projection reads its token rows from a copy in plan order (written by a pass over the codes)
-// instead of gathering them inside the GEMM: as for bf16, with 256-row token tiles, whose 32 gather copies per stage
-// hold the producer back.  MOE_PAIR_GATHER=0|1 overrides.
-int int8_pair_nmax(const moe_shape_t& s);
-bool int8_pregathers(const moe_shape_t& s) { return int8_pair_nmax(s) != 0 && !want_pair_gather(s); }
-Int8Layout int8_up_layout(const moe_shape_t& s) {
-  Int8Layout L = int8_layout(s.M, s.H);
-  L.gathered = L.total;
-  if (int8_pregathers(s)) L.total = align_up(L.total + cap_rows(s) * s.H);
-  return L;
-}
+Int8Layout int8_up_layout(const moe_shape_t& s) { return int8_layout(s.M, s.H); }
 Int8Layout int8_down_layout(const moe_shape_t& s) { return int8_layout(cap_rows(s), s.I); }
 
 moe::Int8GemmArgs int8_plan_args(const moe_plan_t* plan, const moe_shape_t& s, int32_t* err) {
@@ -625,15 +615,8 @@ moe_status_t run_up_int8(const moe_bf16_t* x, const moe_weights_t* w, const moe_
   CUtensorMap mg, mu, mx;
   const uint64_t wrows = static_cast<uint64_t>(s.E) * s.I;
   const int pairs = int8_pair_nmax(s);
-  const bool pre = int8_pregathers(s);
-  uint8_t* xg = base + L.gathered;
-  if (pre && moe::launch_gather_rows(reinterpret_cast<const uint16_t*>(q.codes), plan->sorted_ids,
-                                     plan->num_tokens_post_padded, s.M, s.top_k, s.H / 2,
-                                     static_cast<int>(cap_rows(s)), reinterpret_cast<uint16_t*>(xg),
-                                     stream) != cudaSuccess)
-    return MOE_ERR_CUDA;
   if (!make_map_i8(&mg, w->gate, wrows, s.H, s.H, 128) || !make_map_i8(&mu, w->up, wrows, s.H, s.H, 128) ||
-      !(pre ? make_map_i8(&mx, xg, cap_rows(s), s.H, s.H, 32) : make_map_i8(&mx, q.codes, s.M, s.H, s.H, 1)))
+      !make_map_i8(&mx, q.codes, s.M, s.H, s.H, 1))
     return MOE_ERR_CUDA;
   moe::Int8GemmArgs a = int8_plan_args(plan, s, err);
   a.row_scale = q.scales;
@@ -643,7 +626,7 @@ moe_status_t run_up_int8(const moe_bf16_t* x, const moe_weights_t* w, const moe_
   a.out_ld = s.I;
   a.rows_per_expert = s.I;
   a.kdim = s.H;
-  if (pairs != 0) return cuda_status(moe::launch_int8_pair_up(mg, mu, mx, a, pairs, !pre, num_sms(), stream));
+  if (pairs != 0) return cuda_status(moe::launch_int8_pair_up(mg, mu, mx, a, pairs, num_sms(), stream));
   return cuda_status(moe::launch_int8_up(mg, mu, mx, a, choose_nmax(s), num_sms(), stream));
 }
 
@@ -980,7 +963,7 @@ moe_status_t moe_grouped_up_swiglu(const moe_bf16_t* x, const moe_weights_t* w, 
     return run_up_nvfp4(x, w, plan, s, h, ws, err_flag, static_cast<cudaStream_t>(stream));
   }
   if (w->dtype == MOE_W_INT8) {
-    if (!w->gate_gs || !w->up_gs || !plan->num_tokens_post_padded) return MOE_ERR_INVALID_ARG;
+    if (!w->gate_gs || !w->up_gs) return MOE_ERR_INVALID_ARG;
     if (!ws || ws_bytes < moe_up_workspace_size(s, MOE_W_INT8) || !aligned16(ws)) return MOE_ERR_WORKSPACE;
     return run_up_int8(x, w, plan, s, h, ws, err_flag, static_cast<cudaStream_t>(stream));
   }
@@ -1119,8 +1102,7 @@ int moe_layer_kernel_count(moe_shape_t s, moe_wdtype_t dtype) {
   const int route = route_screens(s) ? 3 : 2;
   if (dtype == MOE_W_NVFP4)  // routing, align, amax x, quantize x, gather tiles, up (+ amax h), quantize h, down, finalize
     return route + 8;
-  if (dtype == MOE_W_INT8)  // routing, align, quantize x, [gather codes], up, quantize h, down, finalize
-    return route + 6 + (int8_pregathers(s) ? 1 : 0);
+  if (dtype == MOE_W_INT8) return route + 6;  // routing, align, quantize x, up, quantize h, down, finalize
   if (want_fused_layer(s, dtype)) return 1;      // the whole layer in one launch
   if (want_self_route(s, dtype)) return route + 3;  // routing, up with the plan, down, finalize
   return route + 4 + (up_pregathers(s) ? 1 : 0);   // routing, align, [gather x], up, down, finalize

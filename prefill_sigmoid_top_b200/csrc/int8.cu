@@ -1,8 +1,8 @@
 // bf16 rows to 8-bit codes and scales (int8_rows.cuh has the arithmetic).
 //
 // Bound: memory.  A row is read once into registers (16-byte loads, 8 in flight per thread), reduced and written as
-// codes; rows of up to 2048 columns take a warp, up to 8192 four warps, longer or unaligned ones a loop that reads
-// twice.
+// codes; rows of up to 2048 columns take a warp, up to 8192 four warps; unaligned or longer ones go by elements.
+// Measured: 8192 x 7168 (117 MB in, 59 MB out) 26 us, 6.8 TB/s.
 #include "int8_rows.cuh"
 #include "kernels.h"
 
@@ -65,9 +65,13 @@ __global__ void __launch_bounds__(kQThreads) quantize_rows_kernel(Int8RowsArgs a
     write_codes<false, kRowThreads>(v, s, dst, nvec, tid);
 }
 
-// Any alignment and length: one CTA per row, two passes over it.
-__global__ void __launch_bounds__(kQThreads) quantize_any_kernel(Int8RowsArgs a) {
-  __shared__ uint32_t part[kQThreads / 32];
+// Any alignment: one CTA per row, element loads, up to kElems per thread in flight and kept in registers; longer rows
+// (kKeep false) are read twice.
+constexpr int kElems = 16;
+
+template <int kThreads, bool kKeep>
+__global__ void __launch_bounds__(kThreads) quantize_any_kernel(Int8RowsArgs a) {
+  __shared__ uint32_t part[kThreads / 32];
   grid_launch_dependents();
   const int tid = threadIdx.x;
   const int64_t r = blockIdx.x;
@@ -77,18 +81,30 @@ __global__ void __launch_bounds__(kQThreads) quantize_any_kernel(Int8RowsArgs a)
     if (id < 0 || id >= a.nslots) return;
   }
   const uint16_t* src = a.src + r * a.ld;
+  uint16_t v[kElems];
   uint32_t top = 0;
-  for (int c = tid; c < a.cols; c += kQThreads) top = max(top, static_cast<uint32_t>(src[c] & 0x7fffu));
+  for (int c0 = tid; c0 < a.cols; c0 += kThreads * kElems) {  // once if kKeep
+#pragma unroll
+    for (int i = 0; i < kElems; ++i) v[i] = c0 + kThreads * i < a.cols ? src[c0 + kThreads * i] : 0;
+#pragma unroll
+    for (int i = 0; i < kElems; ++i) top = max(top, static_cast<uint32_t>(v[i] & 0x7fffu));
+  }
   top = __reduce_max_sync(0xffffffffu, top);
   if ((tid & 31) == 0) part[tid >> 5] = top;
   __syncthreads();
 #pragma unroll
-  for (int q = 0; q < kQThreads / 32; ++q) top = max(top, part[q]);
+  for (int q = 0; q < kThreads / 32; ++q) top = max(top, part[q]);
   if (tid == 0) a.scales[r] = scale_value(top);
   const RowScale s = row_scale_of(top);
   int8_t* dst = a.codes + r * a.pitch;
-  for (int c = tid; c < a.cols; c += kQThreads) {
-    dst[c] = code_of_1(src[c], s);
+  for (int c0 = tid; c0 < a.cols; c0 += kThreads * kElems) {
+    if (!kKeep) {
+#pragma unroll
+      for (int i = 0; i < kElems; ++i) v[i] = c0 + kThreads * i < a.cols ? src[c0 + kThreads * i] : 0;
+    }
+#pragma unroll
+    for (int i = 0; i < kElems; ++i)
+      if (c0 + kThreads * i < a.cols) dst[c0 + kThreads * i] = code_of_1(v[i], s);
   }
 }
 
@@ -104,7 +120,13 @@ cudaError_t launch_quantize_int8(const Int8RowsArgs& a, cudaStream_t stream) {
   } else if (vectors && a.cols <= kQThreads * 8 * kVecs) {
     quantize_rows_kernel<kQThreads><<<static_cast<unsigned>(a.rows), kQThreads, 0, stream>>>(a);
   } else {
-    quantize_any_kernel<<<static_cast<unsigned>(a.rows), kQThreads, 0, stream>>>(a);
+    const unsigned rows = static_cast<unsigned>(a.rows);
+    if (a.cols <= 128 * kElems)
+      quantize_any_kernel<128, true><<<rows, 128, 0, stream>>>(a);
+    else if (a.cols <= 512 * kElems)
+      quantize_any_kernel<512, true><<<rows, 512, 0, stream>>>(a);
+    else
+      quantize_any_kernel<512, false><<<rows, 512, 0, stream>>>(a);
   }
   return cudaGetLastError();
 }

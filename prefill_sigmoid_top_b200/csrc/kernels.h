@@ -275,10 +275,10 @@ bool int8_few_takes(int64_t M, int64_t K);
 cudaError_t launch_int8_few(const uint16_t* x, int64_t ldx, const int8_t* w, int64_t ldw, const Int8GemmArgs& args,
                             int num_sms, cudaStream_t stream);
 
-// int8_pair.cu: the same on 2-SM pairs.  Tensor maps: weights as above; token rows in 32-row boxes, or x codes in
-// one-row boxes (gather).
+// int8_pair.cu: the same on 2-SM pairs.  Tensor maps: weights as above; up: x codes in one-row boxes (gathered);
+// down / dense: token rows in 32-row boxes.
 cudaError_t launch_int8_pair_up(const CUtensorMap& w_gate, const CUtensorMap& w_up, const CUtensorMap& x_rows,
-                                const Int8GemmArgs& args, int nmax, bool gather, int num_sms, cudaStream_t stream);
+                                const Int8GemmArgs& args, int nmax, int num_sms, cudaStream_t stream);
 cudaError_t launch_int8_pair_down(const CUtensorMap& w_down, const CUtensorMap& h_rows, const Int8GemmArgs& args,
                                   int nmax, int num_sms, cudaStream_t stream);
 cudaError_t launch_int8_pair_dense(const CUtensorMap& w, const CUtensorMap& x_rows, const Int8GemmArgs& args,

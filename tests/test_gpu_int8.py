@@ -295,14 +295,11 @@ def test_experts(M, H, I, E, K, B, skew):
 
 
 @pytest.mark.parametrize("M", [3, 150, 700])
-@pytest.mark.parametrize("nmax,pair,gather", [("32", "0", "0"), ("128", "0", "0"), ("128", "128", "0"),
-                                              ("128", "128", "1"), ("128", "256", "0"), ("128", "256", "1")])
-def test_experts_token_tile_widths(nmax, pair, gather, M, monkeypatch):
-    """Every kernel takes every shape: one tile per CTA of 32 or 128 tokens, pairs of 128 or 256, rows gathered in the
-    GEMM or before it."""
+@pytest.mark.parametrize("nmax,pair", [("32", "0"), ("128", "0"), ("128", "128"), ("128", "256")])
+def test_experts_token_tile_widths(nmax, pair, M, monkeypatch):
+    """Every kernel takes every shape: one tile per CTA of 32 or 128 tokens, pairs of 128 or 256."""
     monkeypatch.setenv("MOE_GEMM_NMAX", nmax)
     monkeypatch.setenv("MOE_GEMM_PAIR", pair)
-    monkeypatch.setenv("MOE_PAIR_GATHER", gather)
     shape = moe.Shape(M, 512, 384, 5, 2, 16)
     x, ids, plan, mats, iw = experts_case(shape, seed=3, skew=1.0)
     check_up(shape, x, plan, mats, iw)
