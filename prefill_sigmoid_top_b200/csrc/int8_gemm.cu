@@ -98,8 +98,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int first = static_cast<int>(blockIdx.x) / split, step = static_cast<int>(gridDim.x) / split;
   const int dense_tiles = (args.M + kNmax - 1) / kNmax;
 
-  if (kMode != kDense)
-    for (int e = tid; e < args.E; e += kThreads) cnt[e] = args.counts[e];
+  // the counts' loads are under way while barriers and tensor memory are set up
+  if (kMode != kDense && warp != kMmaWarp)
+    for (int e = tid; e < args.E; e += 32 * kMmaWarp) cnt[e] = args.counts[e];
+  if (warp == kMmaWarp) {
+    tmem_alloc(tmem_slot, C::kTmemCols);
+    tmem_relinquish();
+  }
   if (tid == 0) {
     *abort_flag = 0;
     for (int s = 0; s < kStages; ++s) {
@@ -112,21 +117,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     fence_mbar_init();
   }
+  tc_fence_before_sync();
   __syncthreads();
   if (kMode != kDense) {
     if (warp == 0) build_tile_prefix<kNmax>(cnt, prefix, args.E, W, lane);
     __syncthreads();
   }
   const int total = kMode == kDense ? W * dense_tiles : prefix[args.E];
-  if (first >= total) return;  // the whole cluster leaves
-  if (warp == kMmaWarp) {
-    tmem_alloc(tmem_slot, C::kTmemCols);
-    tmem_relinquish();
-  }
-  tc_fence_before_sync();
-  __syncthreads();
   tc_fence_after_sync();
   const uint32_t tmem = *tmem_slot;
+  if (first >= total) {  // the whole cluster leaves
+    if (warp == kMmaWarp) tmem_dealloc(tmem, C::kTmemCols);
+    return;
+  }
   const int nk_all = (args.kdim + kBK - 1) / kBK;
   const int k_lo = nk_all * rank / split, k_hi = nk_all * (rank + 1) / split;  // split <= nk_all
   const int nslots = args.M * args.top_k;
