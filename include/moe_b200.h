@@ -382,7 +382,7 @@ MOE_API moe_status_t moe_quantize_int8(const moe_bf16_t* src, int64_t ld, int64_
  * [N, K] codes, row n at w + n * ldw, w 16-byte aligned, ldw >= K a multiple of
  * 16 (codes between K and ldw are not read as values); w_scale: fp32 [N]; out:
  * row m at out + m * ldo elements, ldo >= N; ws: moe_linear_int8_workspace_size
- * bytes, 16-byte aligned (0, and ws may be null, where one or two tokens take
+ * bytes, 16-byte aligned (0, and ws may be null, where a few tokens take
  * one launch that quantises x itself); err_flag (nullable) as everywhere.
  * Accepted: 1 <= M, N <= 2^30 with (M/32 + 1) * (N/128 + 1) < 2^31;
  * 1 <= K <= MOE_INT8_MAX_K; else UNSUPPORTED. */

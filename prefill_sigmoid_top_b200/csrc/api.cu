@@ -678,7 +678,7 @@ int64_t linear_int8_pitch(int64_t K) { return (K + 15) / 16 * 16; }
 //   pairs:   4 + rounds of tiles over the pairs x (nk (0.48 + 0.0016 t) + 2) for t tokens per tile: whole tiles of
 //            256 leave a last round short, so t is chosen too;
 //   one CTA, split over a cluster of S:  nk/S (0.3 + 0.0045 t) + 6 + 0.05 t;  unsplit: rounds x (0.35 nk + 4.3).
-// Up to 32 tokens the weight stream of the CTAs wins throughout.
+// Up to 32 tokens the weight stream of the CTAs wins throughout (a few tokens: int8_few.cu).
 int linear_int8_tile(int64_t M, int64_t N, int64_t K) {
   if (const char* env = std::getenv("MOE_INT8_TILE")) {
     const int v = std::atoi(env);
@@ -1189,7 +1189,7 @@ moe_status_t moe_quantize_int8(const moe_bf16_t* src, int64_t ld, int64_t rows, 
 }
 
 size_t moe_linear_int8_workspace_size(int64_t M, int64_t N, int64_t K) {
-  if (!linear_int8_shape_ok(M, N, K) || moe::int8_few_takes(M, K)) return 0;
+  if (!linear_int8_shape_ok(M, N, K) || moe::int8_few_takes(M, N, K)) return 0;
   return int8_layout(M, linear_int8_pitch(K)).total;
 }
 
@@ -1200,7 +1200,7 @@ moe_status_t moe_linear_int8(const moe_bf16_t* x, int64_t ldx, const int8_t* w, 
   if (!x || !w || !w_scale || !out) return MOE_ERR_INVALID_ARG;
   if (out_dtype != MOE_DT_F32 && out_dtype != MOE_DT_BF16) return MOE_ERR_INVALID_ARG;
   if (ldx < K || ldw < K || ldo < N || ldw % 16 != 0 || !aligned16(w)) return MOE_ERR_INVALID_ARG;
-  const bool few = moe::int8_few_takes(M, K);
+  const bool few = moe::int8_few_takes(M, N, K);
   if (!few && (!ws || ws_bytes < moe_linear_int8_workspace_size(M, N, K) || !aligned16(ws))) return MOE_ERR_WORKSPACE;
   auto cs = static_cast<cudaStream_t>(stream);
   moe::Int8GemmArgs a{};

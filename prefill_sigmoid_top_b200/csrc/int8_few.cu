@@ -1,15 +1,18 @@
-// The dense int8 product for one or two tokens in ONE launch, without the tensor cores: a decode step's projection reads
+// The dense int8 product for a few tokens in ONE launch, without the tensor cores: a decode step's projection reads
 // little but its weights (2048 x 7168: 2.2 us at HBM speed), so what counts is the chain from launch to result.  A
-// quantiser of its own, TMA rings, tensor memory and a split over a cluster make that chain 8.7 us (two launches) or
-// 9.2 us (one, with the rows quantised inside and the sums joined through distributed shared memory); this kernel
-// takes the weights straight into registers and multiplies with dp4a: 5.7 us.  (40000 x 7168: 44.6 us, 6.4 TB/s.)
-// Every CTA's own pass over the rows costs more with each row (2048 x 7168: 2 tokens 10.4 us, 4 16 us, 8 26 us; as two
-// launches 10.0 us for any of these), so two tokens, where one launch less on the host decides, are the end of it.
+// quantiser of its own, TMA rings, tensor memory and a split over a cluster make that chain 8.7 us (two launches);
+// this kernel takes the weights straight into registers and multiplies with dp4a.
 //
-// Every CTA quantises the token rows for itself into shared memory (14 KB read per row of 7168, from L2), while its
-// first weight loads are on their way.  Then its 8 warps take output channels: 8 / kWays channels at a time, kWays
-// warps on one channel, each lane 16 codes at a time against every token's codes (dp4a: four exact products added to
-// an int32 sum).  Codes, scales and sums are those of the other forms, so the results are the same bits.
+// One CTA of 32 warps per SM.  It issues its first weight loads, quantises the token rows for itself into shared
+// memory (each thread one 16-byte vector of each row; 14 KB read per row of 7168, from L2), then its warps take output
+// channels: kWays warps on one channel, each lane 16 codes at a time against every token's codes (dp4a: four exact
+// products added to an int32 sum).  Codes, scales and sums are those of the other forms, so the results are the same
+// bits.
+//
+// Bound: the chain; then HBM, and with more tokens the shared-memory reads of their codes beside it.  Measured, this
+// form / two launches (us): 2048 x 7168, 1 token 5.0 / 8.7, 2 tokens 6.2 / 10, 4 tokens 8.6 / 9.4, 8 tokens 13.6 / 9.6;
+// 7168 x 7168, 1 token 9.4 / 12.3, 4 tokens 16.3 / 12.5; 40000 x 7168, 1 token 45.5 (6.3 TB/s).  So it is taken for one
+// or two tokens, and for up to four where the weights are at most 16 MB (int8_few_takes).
 #include <algorithm>
 
 #include "int8_rows.cuh"
@@ -18,12 +21,10 @@
 namespace moe {
 namespace {
 
-constexpr int kWarps = 8;
+constexpr int kWarps = 32;
 constexpr int kThreads = 32 * kWarps;
-constexpr int kMaxRows = 2;
-constexpr int kAhead = 8;               // 16-byte weight loads in flight per lane
+constexpr int kMaxWays = 8;
 constexpr int kMaxRowBytes = 64 * 1024;  // codes of all rows in shared memory
-constexpr int kCtasPerSm = 4;
 
 __device__ __forceinline__ uint4 load_weights(const int8_t* p) {
   uint4 v;
@@ -40,16 +41,17 @@ __device__ __forceinline__ int dot16(const uint4& a, const uint4& b, int c) {
   return __dp4a(static_cast<int>(a.w), static_cast<int>(b.w), c);
 }
 
-// kRows: tokens.
+// kRows: tokens, rounded up to a power of two (the codes of absent ones are 0).
 template <int kRows>
-__global__ void __launch_bounds__(kThreads) int8_few_kernel(const uint16_t* __restrict__ x, int64_t ldx, bool vectors,
-                                                            const int8_t* __restrict__ w, int64_t ldw, int ways,
-                                                            const Int8GemmArgs args) {
+__global__ void __launch_bounds__(kThreads, 1) int8_few_kernel(const uint16_t* __restrict__ x, int64_t ldx, bool vectors,
+                                                               const int8_t* __restrict__ w, int64_t ldw, int ways,
+                                                               const Int8GemmArgs args) {
   extern __shared__ __align__(16) uint8_t codes[];  // [kRows][chunks * 16]
-  __shared__ uint32_t top[kWarps][kRows];
+  __shared__ uint32_t top[kRows][kWarps];
   __shared__ RowScale row_scale[kRows];
   __shared__ float scale[kRows];
   __shared__ int part[kWarps][kRows];
+  constexpr int kAhead = 8;  // 16-byte weight loads in flight per lane
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int M = args.M, N = args.rows_per_expert, K = args.kdim;
   const int chunks = (K + 15) / 16;  // of 16 codes
@@ -71,49 +73,56 @@ __global__ void __launch_bounds__(kThreads) int8_few_kernel(const uint16_t* __re
   fetch(group, first);
 
   // ---- token rows -> codes
+  const bool keep = vectors && K <= 8 * kThreads;  // a vector of each row per thread, read once
+  uint4 v[kRows];
+  if (keep) {
+#pragma unroll
+    for (int m = 0; m < kRows; ++m)
+      v[m] = m < M && tid < K / 8 ? reinterpret_cast<const uint4*>(x + m * ldx)[tid] : make_uint4(0, 0, 0, 0);
+  }
 #pragma unroll
   for (int m = 0; m < kRows; ++m) {
     uint32_t t = 0;
-    if (m < M) {
-      if (vectors) {
-        const uint4* src = reinterpret_cast<const uint4*>(x + m * ldx);
-#pragma unroll 4
-        for (int c = tid; c < K / 8; c += kThreads) {
-          const uint4 v = src[c];
-          t = max_bits(max_bits(max_bits(max_bits(t, v.x), v.y), v.z), v.w);
-        }
-      } else {
-        for (int c = tid; c < K; c += kThreads) t = max(t, static_cast<uint32_t>(x[m * ldx + c] & 0x7fffu));
+    if (keep) {
+      t = max_bits(max_bits(max_bits(max_bits(0, v[m].x), v[m].y), v[m].z), v[m].w);
+    } else if (m < M && vectors) {
+      const uint4* src = reinterpret_cast<const uint4*>(x + m * ldx);
+      for (int c = tid; c < K / 8; c += kThreads) {
+        const uint4 q = src[c];
+        t = max_bits(max_bits(max_bits(max_bits(t, q.x), q.y), q.z), q.w);
       }
+    } else if (m < M) {
+#pragma unroll 4
+      for (int c = tid; c < K; c += kThreads) t = max(t, static_cast<uint32_t>(x[m * ldx + c] & 0x7fffu));
     }
     t = __reduce_max_sync(0xffffffffu, t);
-    if (lane == 0) top[warp][m] = t;
+    if (lane == 0) top[m][warp] = t;
   }
   __syncthreads();
-  if (tid < kRows) {
-    uint32_t t = 0;
-#pragma unroll
-    for (int q = 0; q < kWarps; ++q) t = max(t, top[q][tid]);
-    row_scale[tid] = row_scale_of(t);
-    scale[tid] = scale_value(t);
+  if (warp < kRows) {
+    const uint32_t t = __reduce_max_sync(0xffffffffu, top[warp][lane]);
+    if (lane == 0) {
+      row_scale[warp] = row_scale_of(t);
+      scale[warp] = scale_value(t);
+    }
   }
   __syncthreads();
 #pragma unroll
   for (int m = 0; m < kRows; ++m) {
     uint8_t* dst = codes + m * pitch;
     const RowScale s = row_scale[m];
-    if (m < M && vectors) {
+    if (vectors) {
       const uint4* src = reinterpret_cast<const uint4*>(x + m * ldx);
-#pragma unroll 4
       for (int c = tid; c < pitch / 8; c += kThreads) {
         uint2 o = make_uint2(0, 0);
-        if (c < K / 8) {
-          const uint4 v = src[c];
-          o = s.c != 0.0f ? codes_of_8<true>(v, s) : codes_of_8<false>(v, s);
+        if (m < M && c < K / 8) {
+          const uint4 q = keep ? v[m] : src[c];
+          o = s.c != 0.0f ? codes_of_8<true>(q, s) : codes_of_8<false>(q, s);
         }
         reinterpret_cast<uint2*>(dst)[c] = o;
       }
     } else {
+#pragma unroll 4
       for (int c = tid; c < pitch; c += kThreads)
         dst[c] = m < M && c < K ? static_cast<uint8_t>(code_of_1(x[m * ldx + c], s)) : 0;
     }
@@ -156,12 +165,12 @@ __global__ void __launch_bounds__(kThreads) int8_few_kernel(const uint16_t* __re
 #pragma unroll
         for (int m = 0; m < kRows; ++m) sum = lane == m ? acc[m] : sum;
       }
-      const float v = (scale[lane] * args.ch_scale0[n]) * static_cast<float>(sum);
+      const float r = (scale[lane] * args.ch_scale0[n]) * static_cast<float>(sum);
       const size_t at = static_cast<size_t>(lane) * args.out_ld + n;
       if (args.out_f32)
-        static_cast<float*>(args.out)[at] = v;
+        static_cast<float*>(args.out)[at] = r;
       else
-        static_cast<__nv_bfloat16*>(args.out)[at] = __float2bfloat16_rn(v);
+        static_cast<__nv_bfloat16*>(args.out)[at] = __float2bfloat16_rn(r);
     }
     if (ways > 1) __syncthreads();  // the partial sums are read
   }
@@ -181,29 +190,31 @@ cudaError_t launch_rows(const uint16_t* x, int64_t ldx, const int8_t* w, int64_t
     if (dev < 64) done[dev] = true;
   }
   const int N = args.rows_per_expert, K = args.kdim;
-  // few channels: several warps on one, as long as every SM still has work for its CTAs
+  // few channels: several warps on one, as long as there are warps for all of them and each has a load for every lane
   int ways = 1;
-  while (ways < kWarps && static_cast<long long>(N) * 2 * ways <= static_cast<long long>(kWarps) * kCtasPerSm * num_sms &&
-         64 * 16 * ways <= K)
+  while (ways < kMaxWays && static_cast<long long>(N) * 2 * ways <= static_cast<long long>(kWarps) * num_sms &&
+         2 * 32 * 16 * ways <= K)
     ways *= 2;
   const int groups = (N + kWarps / ways - 1) / (kWarps / ways);
   const bool vectors = K % 8 == 0 && ldx % 8 == 0 && (reinterpret_cast<uintptr_t>(x) & 15u) == 0;
   const size_t smem = static_cast<size_t>(kRows) * ((K + 15) / 16 * 16);
-  kern<<<std::min(groups, kCtasPerSm * num_sms), kThreads, smem, stream>>>(x, ldx, vectors, w, ldw, ways, args);
+  kern<<<std::min(groups, num_sms), kThreads, smem, stream>>>(x, ldx, vectors, w, ldw, ways, args);
   return cudaGetLastError();
 }
 
 }  // namespace
 
-bool int8_few_takes(int64_t M, int64_t K) {
-  if (M > kMaxRows) return false;
-  return M * ((K + 15) / 16 * 16) <= kMaxRowBytes;
+bool int8_few_takes(int64_t M, int64_t N, int64_t K) {
+  if (M > 4 || (M > 2 && N * K > (16ll << 20))) return false;
+  const int64_t rows = M <= 2 ? M : 4;
+  return rows * ((K + 15) / 16 * 16) <= kMaxRowBytes;
 }
 
 cudaError_t launch_int8_few(const uint16_t* x, int64_t ldx, const int8_t* w, int64_t ldw, const Int8GemmArgs& args,
                             int num_sms, cudaStream_t stream) {
   if (args.M <= 1) return launch_rows<1>(x, ldx, w, ldw, args, num_sms, stream);
-  return launch_rows<kMaxRows>(x, ldx, w, ldw, args, num_sms, stream);
+  if (args.M <= 2) return launch_rows<2>(x, ldx, w, ldw, args, num_sms, stream);
+  return launch_rows<4>(x, ldx, w, ldw, args, num_sms, stream);
 }
 
 }  // namespace moe

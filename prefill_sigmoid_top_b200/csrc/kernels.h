@@ -270,8 +270,8 @@ cudaError_t launch_int8_dense(const CUtensorMap& w, const CUtensorMap& x_rows, c
 // least two of the nk steps.
 int int8_tile_split(long long tiles, int nk, int num_sms);
 
-// int8_few.cu: the dense product of one or two tokens in one launch, quantising x itself (row_scale unused).
-bool int8_few_takes(int64_t M, int64_t K);
+// int8_few.cu: the dense product of a few tokens in one launch, quantising x itself (row_scale unused).
+bool int8_few_takes(int64_t M, int64_t N, int64_t K);
 cudaError_t launch_int8_few(const uint16_t* x, int64_t ldx, const int8_t* w, int64_t ldw, const Int8GemmArgs& args,
                             int num_sms, cudaStream_t stream);
 

@@ -114,11 +114,11 @@ def test_linear(M, N, K, out):
     linear_case(M, N, K, out, seed=M + N + K)
 
 
-@pytest.mark.parametrize("M", [1, 2, 3, 9])
+@pytest.mark.parametrize("M", [1, 2, 3, 4, 5])
 @pytest.mark.parametrize("N,K", [(1, 128), (100, 15), (640, 1792), (5000, 256), (2048, 7168), (257, 8200), (40000, 96),
-                                 (128, 14336), (3, 70000)])
+                                 (128, 14336), (3, 70000), (300, 9000)])
 def test_linear_few_tokens(M, N, K):
-    """One or two tokens: one launch, one or several warps to a channel, odd lengths, too long for it; and the same bits
+    """A few tokens: one launch, one or several warps to a channel, odd lengths, too long for it; and the same bits
     as the two-launch form gives for these rows among others."""
     linear_case(M, N, K, torch.float32, pad=(K + M) % 3, seed=M + N)
     x = torch.randn(40, K, generator=gen(M)).to(torch.bfloat16).to(DEV)
