@@ -30,6 +30,7 @@ _PKG = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_PKG, "libmoe_b200.so")
 _lock = threading.Lock()
 _lib = None
+_fast = None  # the extension that marshals the short calls
 
 STATUS = {0: "MOE_OK", 1: "MOE_ERR_INVALID_ARG", 2: "MOE_ERR_UNSUPPORTED", 3: "MOE_ERR_WORKSPACE",
           4: "MOE_ERR_INVALID_INPUT", 5: "MOE_ERR_TIMEOUT", 6: "MOE_ERR_CUDA"}
@@ -71,7 +72,6 @@ class _GroupOpts(ctypes.Structure):
 
 SCORE_SOFTMAX, SCORE_SIGMOID = 0, 1
 GROUP_MAX, GROUP_TOP2 = 0, 1
-_DTYPES = {torch.float32: 0, torch.bfloat16: 1}  # moe_dtype_t
 
 _LAYOUT_FIELDS = ["err_flag", "logits", "topk_ids", "topk_w", "sorted_ids", "block_expert", "expert_counts",
                   "expert_offsets", "num_tokens_post_padded", "h", "y", "act_scratch", "sync", "total"]
@@ -155,6 +155,20 @@ def library():
             _declare(L)
             _lib = L
     return _lib
+
+
+def _load_binding():
+    """The loaded _binding.so (built in-tree, like the library, on first use if it is missing)."""
+    global _fast
+    library()
+    with _lock:
+        if _fast is None:
+            if not os.path.exists(os.path.join(_PKG, "_binding.so")):
+                from . import build as _build
+                _build.build_binding()
+            from . import _binding
+            _fast = _binding
+    return _fast
 
 
 def status_string(status: int) -> str:
@@ -298,16 +312,11 @@ def route_logits(logits, bias, top_k, n_group=1, topk_group=1, group_score=GROUP
     """Top-k routing from logits [M,E] (fp32 or bf16, rows may be strided) with the experts in ``n_group``
     groups of which ``topk_group`` stay -> (topk_ids int32 [M,K], topk_w fp32 [M,K]).  The selection key is the
     score (sigmoid or softmax) plus ``bias`` [E]; the weights come from the scores without it."""
-    if logits.dim() != 2 or logits.dtype not in _DTYPES or (logits.shape[1] > 1 and logits.stride(1) != 1):
-        raise ValueError("logits: expected an fp32 or bf16 [M, E] tensor with contiguous rows")
-    M, E = logits.shape
-    dev = _device_of(logits, bias, topk_ids, topk_w)
-    _want(bias, torch.float32, (E,), "bias")
-    topk_ids, topk_w = _routing_out(M, top_k, logits, topk_ids, topk_w)
-    opts = _group_opts(n_group, topk_group, group_score, scoring, renormalize, routed_scale)
-    _launch(dev, "moe_route_logits", logits.data_ptr(), _DTYPES[logits.dtype], _row_stride(logits, M, E), _adr(bias), M, E,
-            int(top_k), opts, topk_ids.data_ptr(), topk_w.data_ptr())
-    return topk_ids, topk_w
+    r = (_fast or _load_binding()).route_logits(logits, bias, top_k, n_group, topk_group, group_score, scoring, renormalize,
+                                           routed_scale, topk_ids, topk_w)
+    if type(r) is int:
+        raise MoEError(r, "moe_route_logits")
+    return r
 
 
 def route_group(x, w_router, bias, top_k, n_group=1, topk_group=1, group_score=GROUP_TOP2, scoring=SCORE_SIGMOID,
@@ -326,11 +335,6 @@ def route_group(x, w_router, bias, top_k, n_group=1, topk_group=1, group_score=G
     _launch(dev, "moe_route_group", _bf16(x).data_ptr(), w_router.data_ptr(), _adr(bias), shape.c(), opts,
             topk_ids.data_ptr(), topk_w.data_ptr(), ws.data_ptr(), ws.numel())
     return topk_ids, topk_w
-
-
-def _row_stride(t, rows, cols):
-    """Elements between the rows of t [rows, cols] (any value fits a single row)."""
-    return t.stride(0) if rows > 1 else cols
 
 
 def _routing_out(M, top_k, like, topk_ids, topk_w):
@@ -628,61 +632,32 @@ def linear_int8_workspace_size(M: int, N: int, K: int) -> int:
 def linear_int8(x, codes, scales, out=None, out_dtype=torch.bfloat16, ws=None, err_flag=None):
     """out[M,N] = x . W^T with W given as 8-bit codes [N,K] (rows a multiple of 16 bytes apart) and channel
     scales [N]; x bf16 [M,K] (rows may be strided) is quantised per row on the fly.  out: bf16 or fp32."""
-    if x.dim() != 2 or x.dtype is not torch.bfloat16 or (x.shape[1] > 1 and x.stride(1) != 1):
-        raise ValueError("x: expected a bf16 [M, K] tensor with contiguous rows")
-    M, K = x.shape
-    N = codes.shape[0]
-    if codes.dtype is not torch.int8 or codes.shape != (N, K) or (K > 1 and codes.stride(1) != 1):
-        raise ValueError("codes: expected an int8 [N, K] tensor with contiguous rows")
-    dev = _device_of(x, codes, scales, out, ws, err_flag)
-    _want(scales, torch.float32, (N,), "scales")
-    if out is None:
-        if out_dtype not in _DTYPES:
-            raise ValueError("out_dtype: expected torch.bfloat16 or torch.float32")
-        out = torch.empty((M, N), dtype=out_dtype, device=x.device)
-    elif out.dtype not in _DTYPES or out.shape != (M, N) or (N > 1 and out.stride(1) != 1):
-        raise ValueError("out: expected a bf16 or fp32 [M, N] tensor with contiguous rows")
-    ldw = codes.stride(0) if N > 1 else (max(codes.stride(0), K) + 15) // 16 * 16
-    need = linear_int8_workspace_size(M, N, K)
-    if ws is None and need:
-        ws = x.new_empty(need, dtype=torch.uint8)
-    _launch(dev, "moe_linear_int8", x.data_ptr(), _row_stride(x, M, K), codes.data_ptr(), ldw, scales.data_ptr(), M, N, K,
-            out.data_ptr(), _row_stride(out, M, N), _DTYPES[out.dtype], _adr(ws), 0 if ws is None else ws.numel(),
-            _adr(err_flag))
-    return out
+    r = (_fast or _load_binding()).linear_int8(x, codes, scales, out, out_dtype, ws, err_flag)
+    if type(r) is int:
+        raise MoEError(r, "moe_linear_int8")
+    return r
 
 
 def grouped_up_swiglu_int8(x, iw: Int8Weights, plan, shape: Shape, h=None, err_flag=None, ws=None):
     """int8 form of grouped_up_swiglu (every token's x quantised on the fly into ws)."""
-    ts = iw.check(shape, "gate", "up")
-    dev = _device_of(x, *ts, plan["sorted_ids"], h, err_flag, ws)
-    _want(x, torch.bfloat16, (shape.M, shape.H), "x")
-    if h is None:
-        h = x.new_empty((align_capacity(shape), shape.I))
-    elif h.numel() < align_capacity(shape) * shape.I:
-        raise ValueError("h: expected align_capacity(shape) rows of I")
-    if ws is None:
-        ws = x.new_empty(max(up_workspace_size(shape, MOE_W_INT8), 1), dtype=torch.uint8)
-    _launch(dev, "moe_grouped_up_swiglu", x.data_ptr(), ctypes.byref(iw.c()), ctypes.byref(_plan_struct(plan)),
-            shape.c(), _bf16(h).data_ptr(), ws.data_ptr(), ws.numel(), _adr(err_flag))
-    return h
+    r = (_fast or _load_binding()).grouped_up_swiglu_int8(
+        x, shape.M, shape.H, shape.I, shape.E, shape.top_k, shape.block_size, iw.gate, iw.gate_scales, iw.up,
+        iw.up_scales, plan["sorted_ids"], plan["block_expert"], plan["expert_counts"], plan["expert_offsets"],
+        plan["num_tokens_post_padded"], h, err_flag, ws)
+    if type(r) is int:
+        raise MoEError(r, "moe_grouped_up_swiglu")
+    return r
 
 
 def grouped_down_int8(h, iw: Int8Weights, plan, shape: Shape, y=None, err_flag=None, ws=None):
     """int8 form of grouped_down (the real plan rows of h quantised on the fly into ws)."""
-    ts = iw.check(shape, "down")
-    dev = _device_of(h, *ts, plan["sorted_ids"], y, err_flag, ws)
-    if h.numel() < align_capacity(shape) * shape.I:
-        raise ValueError("h: expected align_capacity(shape) rows of I")
-    if y is None:
-        y = h.new_empty((shape.M * shape.top_k, shape.H))
-    elif y.numel() != shape.M * shape.top_k * shape.H:
-        raise ValueError("y: expected M * top_k rows of H")
-    if ws is None:
-        ws = h.new_empty(max(down_workspace_size(shape, MOE_W_INT8), 1), dtype=torch.uint8)
-    _launch(dev, "moe_grouped_down", _bf16(h).data_ptr(), ctypes.byref(iw.c()), ctypes.byref(_plan_struct(plan)),
-            shape.c(), _bf16(y).data_ptr(), ws.data_ptr(), ws.numel(), _adr(err_flag))
-    return y
+    r = (_fast or _load_binding()).grouped_down_int8(
+        h, shape.M, shape.H, shape.I, shape.E, shape.top_k, shape.block_size, iw.down, iw.down_scales,
+        plan["sorted_ids"], plan["block_expert"], plan["expert_counts"], plan["expert_offsets"],
+        plan["num_tokens_post_padded"], y, err_flag, ws)
+    if type(r) is int:
+        raise MoEError(r, "moe_grouped_down")
+    return r
 
 
 def layer_int8(x, w_router, bias, iw: Int8Weights, gamma, eps, top_k, block_size, ws=None, out=None,

@@ -27,6 +27,31 @@ def _stale(out: str, deps: list[str]) -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+BINDING = os.path.join(PKG, "_binding.so")
+
+
+def build_binding(force: bool = False) -> str:
+    """Compile the CPython extension that marshals the short calls (csrc/binding.cpp), against libmoe_b200.so beside it."""
+    src, header = os.path.join(CSRC, "binding.cpp"), os.path.join(ROOT, "include", "moe_b200.h")
+    if force or _stale(BINDING, [src, header]):
+        import sysconfig
+
+        import torch
+        tdir = os.path.dirname(torch.__file__)
+        tmp = BINDING + f".tmp{os.getpid()}"
+        subprocess.check_call([
+            os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", sysconfig.get_paths()["include"],
+            "-isystem", os.path.join(tdir, "include"),
+            "-isystem", os.path.join(tdir, "include", "torch", "csrc", "api", "include"),
+            "-isystem", os.path.join(os.path.dirname(os.path.dirname(NVCC)), "include"),
+            "-I", os.path.join(ROOT, "include"), src, "-o", tmp, "-L", PKG, "-l:libmoe_b200.so",
+            "-L", os.path.join(tdir, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda",
+            "-Wl,-rpath,$ORIGIN"])
+        os.replace(tmp, BINDING)
+    return BINDING
+
+
 TRACE_LIB = os.path.join(PKG, "libmoe_b200_trace.so")
 
 
@@ -60,6 +85,8 @@ def build(force: bool = False, verbose: bool = False, extra_flags: list[str] | N
         tmp = lib + f".tmp{os.getpid()}"
         subprocess.check_call([NVCC, "-gencode", "arch=compute_100a,code=sm_100a", "-shared", *objs, "-o", tmp])
         os.replace(tmp, lib)
+    if not trace:
+        build_binding(force)
     return lib
 
 

@@ -461,6 +461,48 @@ def test_group_routed_layer_with_a_shared_expert(M):
     within(shared, want, 2.0 ** -8 + 5 * 2.0 ** -24)
 
 
+def test_refusals_by_name():
+    """What the binding refuses on CUDA tensors: types, shapes, strides, devices, missing matrices; and the statuses of
+    the library as MoEError.  None of it launches anything."""
+    x = torch.zeros(4, 64, dtype=torch.bfloat16, device=DEV)
+    c, s = torch.zeros(8, 64, dtype=torch.int8, device=DEV), torch.zeros(8, device=DEV)
+    z = torch.zeros(4, 8, device=DEV)
+    shape = moe.Shape(4, 256, 128, 2, 1, 16)
+    plan = moe.align_block_size(torch.zeros(4, 1, dtype=torch.int32, device=DEV), 2, 16)
+    xe = torch.zeros(4, 256, dtype=torch.bfloat16, device=DEV)
+    h = torch.zeros(moe.align_capacity(shape), 128, dtype=torch.bfloat16, device=DEV)
+    iw = moe.int8_weights(*(torch.zeros(2, *d, dtype=torch.bfloat16, device=DEV) for d in ((128, 256), (128, 256), (256, 128))))
+    for call in (lambda: moe.linear_int8(x.float(), c, s), lambda: moe.linear_int8(x, c.float(), s),
+                 lambda: moe.linear_int8(x, c[:, :32], s), lambda: moe.linear_int8(x, c, s[:4]),
+                 lambda: moe.linear_int8(x, c, s.double()), lambda: moe.linear_int8(x.t(), c, s),
+                 lambda: moe.linear_int8(x, c, s, out_dtype=torch.float16), lambda: moe.linear_int8(x, c, s, out=z.t()),
+                 lambda: moe.linear_int8(x, c, s, out=z.double()), lambda: moe.linear_int8(x, c, s.cpu()),
+                 lambda: moe.linear_int8(x[0], c, s), lambda: moe.route_logits(z.half(), None, 2),
+                 lambda: moe.route_logits(z, s[:4], 2), lambda: moe.route_logits(z, s.cpu(), 2),
+                 lambda: moe.route_logits(z, None, 2, topk_ids=z), lambda: moe.route_logits(z[:, ::2], None, 2),
+                 lambda: moe.grouped_up_swiglu_int8(xe, moe.Int8Weights(), plan, shape),
+                 lambda: moe.grouped_up_swiglu_int8(xe[:3], iw, plan, shape),
+                 lambda: moe.grouped_up_swiglu_int8(xe, iw, plan, shape, h=h[:3]),
+                 lambda: moe.grouped_up_swiglu_int8(xe, iw, dict(plan, sorted_ids=z), shape),
+                 lambda: moe.grouped_down_int8(h[:3], iw, plan, shape),
+                 lambda: moe.grouped_down_int8(h, iw, plan, shape, y=xe[:2]),
+                 lambda: moe.grouped_down_int8(h, moe.Int8Weights(down=iw.gate, down_scales=iw.gate_scales), plan, shape)):
+        with pytest.raises(ValueError):
+            call()
+    for call, status in ((lambda: moe.route_logits(z, None, 9), 2), (lambda: moe.route_logits(z, None, 2, 3), 2),
+                         (lambda: moe.route_logits(z, None, 2, routed_scale=0.0), 1),
+                         (lambda: moe.linear_int8(x[:0], c, s), 2), (lambda: moe.linear_int8(x, c[:, :63], s), 0),
+                         (lambda: moe.linear_int8(x[:, :40], c.flatten()[:8 * 40].view(8, 40), s), 1),
+                         (lambda: moe.linear_int8(x.repeat(10, 1), c, s, ws=torch.zeros(16, dtype=torch.uint8, device=DEV)), 3)):
+        if status == 0:
+            with pytest.raises(ValueError):
+                call()
+            continue
+        with pytest.raises(moe.MoEError) as e:
+            call()
+        assert e.value.status == status
+
+
 def test_layer_against_bf16_layer():
     """8 bits instead of bf16: the layer's output moves by the quantisation error only (two roundings of at most
     half of 1/127 of a row's largest value in each product: a few percent of the RMS)."""

@@ -11,6 +11,7 @@ from prefill_sigmoid_top_b200 import _GroupOpts, _Plan, _Weights
 FAKE = ctypes.c_void_p(0x10000)       # aligned non-null address, never dereferenced
 FAKE_MIS = ctypes.c_void_p(0x10008)   # 8-byte aligned only
 P = 0x10000
+PLAN = ("sorted_ids", "block_expert", "expert_counts", "expert_offsets", "num_tokens_post_padded")
 S = moe.Shape(M=16, H=256, I=128, E=8, top_k=2, block_size=16)
 
 
@@ -109,7 +110,9 @@ def test_binding_refusals():
                  lambda: moe.linear_int8(cpu.to(torch.bfloat16), cpu.to(torch.int8)[:, :32], cpu[:, 0]),
                  lambda: moe.linear_int8(cpu.to(torch.bfloat16), cpu.to(torch.int8), cpu[:, 0]),
                  lambda: moe.quantize_int8(cpu),
-                 lambda: moe.grouped_up_swiglu_int8(cpu, moe.Int8Weights(), {}, S),
+                 lambda: moe.grouped_up_swiglu_int8(cpu, moe.Int8Weights(), dict.fromkeys(PLAN, cpu), S),
+                 lambda: moe.grouped_down_int8(cpu, moe.Int8Weights(), dict.fromkeys(PLAN, cpu), S),
+                 lambda: moe.route_logits(None, None, 2), lambda: moe.route_logits("logits", None, 2),
                  lambda: moe.layer_int8(cpu, cpu, None, moe.Int8Weights(), cpu, 1e-5, 2, 16)):
         with pytest.raises(ValueError):
             call()
