@@ -12,13 +12,19 @@
 // Channels past the expert's last row are computed and not stored.
 //
 // Warps (640 threads): 0..2 = producers, 3 = MMA issuer (leader), 4..19 = epilogue.  A stage holds the weight boxes
-// and the token rows of one k-step; the producer warps take stages in turn.  One producer thread per operand,
-// as the bf16 pair kernels have, needs about 0.7 us for a stage however wide its tokens and wherever the weights are
-// (the wake-up of its wait and the issue of its copies in series): that alone held 8192 x 7168 x 7168 at 0.69 us per
-// k-step.
+// and the token rows of one k-step; the producer warps take stages in turn.  One producer thread per operand, as the
+// bf16 pair kernels have, needs about 0.7 us for a stage however wide its tokens (the wake-up of its wait and the issue
+// of its copies in series); with three: 8192 x 7168 x 7168 314 -> 299 us, prefill up 1467 -> 1403 us, batch up 1128 ->
+// 1102 us.
+//
+// Measured: 8192 x 7168 x 7168 299 us with its quantiser (2.8 Pop/s; 356 us under the power cap of a long run), batch
+// up (512 tokens, 256 experts) 1.12 ms at 6.8 TB/s, skewed prefill (2048 tokens) up 1.42 ms, down 0.80 ms.  Bound: HBM
+// for the experts with few tokens, power and the operand feed for the busy ones (tensor pipe 67% active at
+// 4096 x 7168 x 7168).
+//
 // The launch overlaps the kernel before it (programmatic dependent launch): set-up and the first weight boxes come
-// before the wait for it.  Every mbarrier wait is bounded; a timeout sets the error word and unwinds, and both CTAs still meet at the last cluster
-// barrier.
+// before the wait for it.  Every mbarrier wait is bounded; a timeout sets the error word and unwinds, and both CTAs
+// still meet at the last cluster barrier.
 #include "common.cuh"
 #include "kernels.h"
 #include "pair_ptx.cuh"
