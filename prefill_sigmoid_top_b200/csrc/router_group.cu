@@ -29,8 +29,10 @@
 //            rcp.approx within 2^-23; the scaled argument of the exponential adds |z| 2^-23.4 relative)
 //   softmax: relative 2^-19 + |z - max| 2^-23, and p <= e^-|z - max| / denom: below 2^-18 / denom
 // plus 2^-23 of each sum that follows.  Of bf16 logits, two that are nearer than their spacing are equal: a tie.
-// Keys below the range share the lowest integer: a choice that reaches them goes to fp64 (about 1 token in 1000 of
-// normal logits and a small bias).
+// Keys below the range share the lowest integer.  About 1 token in 1000 of normal logits and a small bias has two
+// neighbours too near (2 in 100 with 1024 experts and K = 32).  Where that is all, the K + 1 listed keys are computed
+// exactly, one per lane, and put in order; the rest goes to the fp64 path as a whole, whose 10 to 40 us for one token
+// would otherwise be the tail of every large call.
 //
 // Measured (256 experts in 8 groups, 4 kept, K = 8, sigmoid and bias, fp32): 8 tokens 2.7 us, 32767 tokens 27 us
 // (1.3 TB/s; 656 instructions per token, 81% of the issue slots in use); 2048 tokens of bf16 logits, softmax, K = 16:
@@ -80,6 +82,8 @@ __device__ __forceinline__ double exp_score(double z, double zmax) {
   if (zmax == INFINITY) return z == INFINITY ? 1.0 : 0.0;
   return exp(z - zmax);
 }
+
+__device__ __noinline__ double sigmoid_fp64(double z) { return 1.0 / (1.0 + exp(-z)); }
 
 // Which experts a lane holds: 32 / n_group lanes (rounded down to a power of two) per group, neighbours in each.
 struct Share {
@@ -345,7 +349,7 @@ __global__ void __launch_bounds__(32 * kWarps) route_group_kernel(const void* __
       return apart == 0 || clear_of_limits(zhi, zlo);  // different ones are further apart than 4 steps and 2^-28
     return static_cast<float>(apart - 2) * sure > 0x1p-30f && clear_of_limits(zhi, zlo);
   };
-  bool good = true;
+  bool groups_good = true;
 
   // ---- 3. groups
   if (groups) {
@@ -379,12 +383,12 @@ __global__ void __launch_bounds__(32 * kWarps) route_group_kernel(const void* __
     const uint32_t slo = __shfl_sync(0xffffffffu, s, (__ffs(next) - 1) & 31);
     const int apart = static_cast<int>(shi - slo);
     if (!by_logit) {
-      good = static_cast<float>(apart - 4) * sure > 4.0f * off_key;
+      groups_good = static_cast<float>(apart - 4) * sure > 4.0f * off_key;
     } else if (group_sums) {
       const float fhi = __uint_as_float(shi);
-      good = fhi - __uint_as_float(slo) > 4.0f * (off_key + 6.0f * step) + fhi * 0x1p-22f;
+      groups_good = fhi - __uint_as_float(slo) > 4.0f * (off_key + 6.0f * step) + fhi * 0x1p-22f;
     } else {
-      good = logits_clear(shi, apart, value_of(shi), value_of(slo));
+      groups_good = logits_clear(shi, apart, value_of(shi), value_of(slo));
     }
     if (!(real && before < o.topk_group)) {
 #pragma unroll
@@ -413,20 +417,57 @@ __global__ void __launch_bounds__(32 * kWarps) route_group_kernel(const void* __
   }
   // every choice against the next one: lane k compares rounds k and k + 1 (round 32 is in no lane)
   auto id_of = [&](uint32_t x) { return min(static_cast<int>(id_mask - (x & id_mask)), E - 1); };
-  const int sel = id_of(mine);
-  const float zsel = lane < rounds ? raw_logit<kBf16>(row, sel) : 0.0f;
+  int sel = id_of(mine);
+  float zsel = lane < rounds ? raw_logit<kBf16>(row, sel) : 0.0f;
   const uint32_t below = __shfl_down_sync(0xffffffffu, mine, 1);
   float zlo = __shfl_down_sync(0xffffffffu, zsel, 1);
+  bool good = true;
   if (lane + 1 < rounds) {
     const uint32_t other = lane < 31 ? below : top;
     if (lane == 31) zlo = raw_logit<kBf16>(row, id_of(other));
     const int apart = static_cast<int>(mine >> id_bits) - static_cast<int>(other >> id_bits);
-    good = good && (by_logit ? logits_clear(mine >> id_bits, apart, zsel, zlo)
-                             : static_cast<float>(apart - 2) * sure > 2.0f * off_key);
+    good = by_logit ? logits_clear(mine >> id_bits, apart, zsel, zlo)
+                    : static_cast<float>(apart - 2) * sure > 2.0f * off_key;
   }
   // scores far below the fp32 range are the fp64 path's
-  if (lane < K) good = good && !((softmax ? zsel - zmax : zsel) < -80.0f);
-  if (!__all_sync(0xffffffffu, good && whole == 0.0f)) {
+  const bool plain = groups_good && whole == 0.0f && !(lane < K && (softmax ? zsel - zmax : zsel) < -80.0f);
+  bool settled = __all_sync(0xffffffffu, plain && good);
+  if (!settled && __all_sync(0xffffffffu, plain) && (by_logit || !softmax) && K < 32) {
+    // only neighbours in the list are too near: put the list in order by exact keys.  Nothing outside it can belong
+    // to the choice if the best of the rest is clear of the K-th.
+    const int listed = rounds;
+    bool ok = true;
+    if (o.topk_group * gs > listed) {
+      uint32_t rest = u[0][0];
+#pragma unroll
+      for (int c = 1; c < kLists; ++c) rest = max(rest, u[c][0]);
+      rest = __reduce_max_sync(0xffffffffu, rest);
+      const int apart = static_cast<int>(__shfl_sync(0xffffffffu, mine, K - 1) >> id_bits) - static_cast<int>(rest >> id_bits);
+      ok = static_cast<float>(apart - 2) * sure > (by_logit ? 0x1p-30f : 2.0f * off_key);
+    }
+    if (ok) {
+      double exact = zsel;  // the score grows with it
+      if (!by_logit) exact = sigmoid_fp64(zsel) + static_cast<double>(bias[lane < listed ? sel : 0]);
+      int place = 0, moved = sel;
+      for (int j = 0; j < listed; ++j) {
+        const double other = __shfl_sync(0xffffffffu, exact, j);
+        const int id = __shfl_sync(0xffffffffu, sel, j);
+        place += other > exact || (other == exact && id < sel);
+      }
+      for (int j = 0; j < listed; ++j) {
+        const int at = __shfl_sync(0xffffffffu, place, j), id = __shfl_sync(0xffffffffu, sel, j);
+        if (at == lane) moved = id;
+      }
+      sel = moved;
+      if (lane < listed) zsel = raw_logit<kBf16>(row, sel);
+      zlo = __shfl_down_sync(0xffffffffu, zsel, 1);
+      if (by_logit && lane + 1 < listed)
+        ok = zsel == zlo || (zsel - zlo > 0x1p-30f && clear_of_limits(zsel, zlo));
+      ok = ok && !(lane < K && (softmax ? zsel - zmax : zsel) < -80.0f);
+    }
+    settled = __all_sync(0xffffffffu, ok);
+  }
+  if (!settled) {
     route_token_fp64<kBf16, kPer>(row, bias, E, K, o, ids, w);
     return;
   }
