@@ -720,7 +720,7 @@ moe_status_t check_group_route(int32_t M, int32_t E, int32_t top_k, const moe_gr
 }
 
 moe::RouteGroupOpts group_opts(const moe_group_opts_t& o) {
-  return {o.scoring, o.renormalize != 0 ? 1 : 0, o.n_group, o.topk_group, o.group_score, o.routed_scale, 0, 0};
+  return {o.scoring, o.renormalize != 0 ? 1 : 0, o.n_group, o.topk_group, o.group_score, o.routed_scale, 0, 0, false, false};
 }
 
 // Counters of the single-launch layer: grid barrier, work counter, finalize

@@ -218,7 +218,9 @@ cudaError_t launch_nvfp4_pair_down(const CUtensorMap& down_codes, const CUtensor
 struct RouteGroupOpts {
   int scoring, renormalize, n_group, topk_group, group_score;
   float routed_scale;
-  int group_size, lanes_log;  // set by launch_route_group: E / n_group, log2 of the lanes that hold a group
+  // set by launch_route_group: E / n_group, log2 of the lanes that hold a group, four logits (biases) per load
+  int group_size, lanes_log;
+  bool logits_by_4, bias_by_4;
 };
 cudaError_t launch_route_group(const void* logits, bool bf16, int64_t ld, const float* bias, int M, int E, int K,
                                const RouteGroupOpts& o, int32_t* topk_ids, float* topk_w, cudaStream_t stream);

@@ -75,15 +75,21 @@ __device__ __forceinline__ float rcp_approx(float x) {
   return y;
 }
 
-// e^(z - zmax) with the limits: a row whose largest logit is +inf shares among its +inf entries, a row of
-// -inf only has no scores.
-__device__ __forceinline__ double exp_score(double z, double zmax) {
-  if (zmax == -INFINITY) return 0.0;
-  if (zmax == INFINITY) return z == INFINITY ? 1.0 : 0.0;
-  return exp(z - zmax);
+// e^(z - zmax) at the limits: a row whose largest logit is +inf shares among its +inf entries, a row of -inf only has
+// no scores.
+__device__ __forceinline__ double exp_limits(double z, double zmax) {
+  return zmax == INFINITY && z == INFINITY ? 1.0 : 0.0;
 }
 
-__device__ __noinline__ double sigmoid_fp64(double z) { return 1.0 / (1.0 + exp(-z)); }
+// The score of one logit (softmax: from the row's maximum and sum; sigmoid: denom 0).  Not inlined: the fp64 path runs
+// cold, and its time is that of fetching its code.
+__device__ __noinline__ double score_fp64(double z, double zmax, double denom) {
+  const bool sigmoid = denom == 0.0;
+  const bool limits = !sigmoid && !(fabs(zmax) < INFINITY);
+  const double e = exp(sigmoid ? -z : z - zmax);
+  if (sigmoid) return 1.0 / (1.0 + e);
+  return (limits ? exp_limits(z, zmax) : e) / denom;
+}
 
 // Which experts a lane holds: 32 / n_group lanes (rounded down to a power of two) per group, neighbours in each.
 struct Share {
@@ -110,7 +116,7 @@ __device__ __noinline__ void route_token_fp64(const void* row, const float* bias
   const Share me(lane, o);
   const bool softmax = o.scoring == MOE_SCORE_SOFTMAX;
   double v[kPer];
-  double zmax = -INFINITY, denom = 1.0;
+  double zmax = -INFINITY, denom = 0.0;
 #pragma unroll
   for (int i = 0; i < kPer; ++i) v[i] = i < me.n ? load_logit<kBf16>(row, me.e0 + i) : -INFINITY;
   if (softmax) {
@@ -119,13 +125,11 @@ __device__ __noinline__ void route_token_fp64(const void* row, const float* bias
     for (int off = 16; off >= 1; off >>= 1) zmax = fmax(zmax, shfl_xor_d(zmax, off));
     denom = 0.0;
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) denom += i < me.n ? exp_score(v[i], zmax) : 0.0;
+    for (int i = 0; i < kPer; ++i) denom += i < me.n ? score_fp64(v[i], zmax, 1.0) : 0.0;
     for (int off = 16; off >= 1; off >>= 1) denom += shfl_xor_d(denom, off);
+    if (!(denom > 0.0)) denom = 1.0;  // a row of -inf only: every score is 0
   }
-  auto score = [&](double z) {
-    if (softmax) return denom > 0.0 ? exp_score(z, zmax) / denom : 0.0;
-    return 1.0 / (1.0 + exp(-z));
-  };
+  auto score = [&](double z) { return score_fp64(z, zmax, denom); };
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
     const double p = score(v[i]);
@@ -268,6 +272,22 @@ __global__ void __launch_bounds__(32 * kWarps) route_group_kernel(const void* __
 #pragma unroll
       for (int i = 0; i < kPer; ++i) v[i] = raw_logit<kBf16>(row, e0 + i);
     }
+  } else if (kPer >= 4 && o.logits_by_4) {
+#pragma unroll
+    for (int i = 0; i + 3 < kPer; i += 4) {
+      float q[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+      if (i < n) {
+        if (kBf16) {
+          const uint2 x = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(static_cast<const void*>(row)) + e0 + i);
+          q[0] = bf16_lo(x.x), q[1] = bf16_hi(x.x), q[2] = bf16_lo(x.y), q[3] = bf16_hi(x.y);
+        } else {
+          const float4 x = *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(row) + e0 + i);
+          q[0] = x.x, q[1] = x.y, q[2] = x.z, q[3] = x.w;
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u) v[i + u] = q[u];
+    }
   } else {
 #pragma unroll
     for (int i = 0; i < kPer; ++i) v[i] = i < n ? raw_logit<kBf16>(row, e0 + i) : 0.0f;
@@ -297,9 +317,21 @@ __global__ void __launch_bounds__(32 * kWarps) route_group_kernel(const void* __
     return softmax ? exp2_approx((z - zmax) * kLog2e) * inv_denom : rcp_approx(1.0f + exp2_approx(-z * kLog2e));
   };
   if (!by_logit) {
+    if (kPer >= 4 && o.bias_by_4) {  // a lane's experts are neighbours: one by one its loads would touch 32 lines each
 #pragma unroll
-    for (int i = 0; i < kPer; ++i)
-      if (kFull || i < n) v[i] = score32(v[i]) + bias[e0 + i];
+      for (int i = 0; i + 3 < kPer; i += 4)
+        if (kFull || i < n) {
+          const float4 b = *reinterpret_cast<const float4*>(bias + e0 + i);
+          v[i] = score32(v[i]) + b.x;
+          v[i + 1] = score32(v[i + 1]) + b.y;
+          v[i + 2] = score32(v[i + 2]) + b.z;
+          v[i + 3] = score32(v[i + 3]) + b.w;
+        }
+    } else {
+#pragma unroll
+      for (int i = 0; i < kPer; ++i)
+        if (kFull || i < n) v[i] = score32(v[i]) + bias[e0 + i];
+    }
   }
   float hi = -INFINITY;
 #pragma unroll
@@ -346,7 +378,7 @@ __global__ void __launch_bounds__(32 * kWarps) route_group_kernel(const void* __
   // Two logits with the integers q and q - apart: a tie, or apart as above (in the lowest integer anything may be).
   auto logits_clear = [&](uint32_t q, int apart, float zhi, float zlo) {
     if (kBf16 && q > 2 && fabsf(zhi) > 0x1p-20f && 5.0f * step < fabsf(zhi) * 0x1p-8f)
-      return apart == 0 || clear_of_limits(zhi, zlo);  // different ones are further apart than 4 steps and 2^-28
+      return clear_of_limits(zhi, zlo);  // equal, or further apart than 4 steps and 2^-28
     return static_cast<float>(apart - 2) * sure > 0x1p-30f && clear_of_limits(zhi, zlo);
   };
   bool groups_good = true;
@@ -442,12 +474,14 @@ __global__ void __launch_bounds__(32 * kWarps) route_group_kernel(const void* __
 #pragma unroll
       for (int c = 1; c < kLists; ++c) rest = max(rest, u[c][0]);
       rest = __reduce_max_sync(0xffffffffu, rest);
-      const int apart = static_cast<int>(__shfl_sync(0xffffffffu, mine, K - 1) >> id_bits) - static_cast<int>(rest >> id_bits);
+      const int apart =
+          static_cast<int>(__shfl_sync(0xffffffffu, mine, K - 1) >> id_bits) - static_cast<int>(rest >> id_bits);
       ok = static_cast<float>(apart - 2) * sure > (by_logit ? 0x1p-30f : 2.0f * off_key);
+      if (by_logit) ok = ok && clear_of_limits(__shfl_sync(0xffffffffu, zsel, K - 1), value_of(rest >> id_bits));
     }
     if (ok) {
       double exact = zsel;  // the score grows with it
-      if (!by_logit) exact = sigmoid_fp64(zsel) + static_cast<double>(bias[lane < listed ? sel : 0]);
+      if (!by_logit) exact = score_fp64(zsel, 0.0, 0.0) + static_cast<double>(bias[lane < listed ? sel : 0]);
       int place = 0, moved = sel;
       for (int j = 0; j < listed; ++j) {
         const double other = __shfl_sync(0xffffffffu, exact, j);
@@ -517,7 +551,13 @@ cudaError_t launch_typed(const void* logits, int64_t ld, const float* bias, int 
   o.group_size = E / o.n_group;
   o.lanes_log = 0;
   while ((2 << o.lanes_log) * o.n_group <= 32) ++o.lanes_log;
-  const int per = (o.group_size + (1 << o.lanes_log) - 1) >> o.lanes_log;  // experts per lane: at most 60 (17 groups, one lane each)
+  const int per = (o.group_size + (1 << o.lanes_log) - 1) >> o.lanes_log;
+  // whether every lane's experts start and end at a multiple of four, and the rows (the bias) can be read so
+  const bool fours = per % 4 == 0 && o.group_size % 4 == 0;
+  const int size = kBf16 ? 2 : 4;
+  o.logits_by_4 = fours && ld % 4 == 0 && (reinterpret_cast<uintptr_t>(logits) & (4 * size - 1)) == 0;
+  o.bias_by_4 = fours && (reinterpret_cast<uintptr_t>(bias) & 15u) == 0;
+  // experts per lane: at most 60 (17 groups, one lane each)
   auto run = [&](auto f) { return f(logits, ld, bias, M, E, K, o, topk_ids, topk_w, stream); };
   if (per <= 1) return run(launch_per<kBf16, 1>);
   if (per <= 2) return run(launch_per<kBf16, 2>);

@@ -143,6 +143,17 @@ def test_far_logits():
     z = torch.tensor([[-100.0, -101.0, -102.0, -103.0] * 4, [100.0, 90.0, 80.0, 70.0] * 4, [-800.0] * 16])
     check(z, None, 4, 4, 2)
     check(z, None, 4, 4, 2, scoring=moe.SCORE_SOFTMAX)
+    for K in (1, 2, 3, 5, 7):  # scores that are 1 (or 0) in fp64 whatever the logit: the lower id, with and without groups
+        check(z, None, K)
+        check(z, None, K, scoring=moe.SCORE_SOFTMAX)
+        check(z, torch.zeros(16), K, 4, 2)
+    z = torch.full((2, 64), 38.0)
+    z[0, 40:50] = 45.0
+    z[1, 5:] = -700.0
+    z[1, 20:30] = -690.0
+    for K in (1, 4, 9, 10, 11):
+        check(z, None, K)
+        check(z.to(torch.bfloat16), None, K)
 
 
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["fp32", "bf16"])
