@@ -168,8 +168,8 @@ MOE_API moe_status_t moe_route_ex(const moe_bf16_t* x, const moe_bf16_t* w_route
  *   topk_ids[t,0..K) = the K largest keys among their experts, descending, ties
  *           -> lower id;  topk_w[t,k] = w_k * routed_scale with w_k = p_k, or
  *           p_k / sum_j p_j over the K selected (renormalize; 0 if that sum is 0).
- * p, keys and group scores are those of fp64 arithmetic; weights are rounded
- * to fp32 once.  A NaN logit counts as -inf, a NaN key or group score ranks as
+ * The selection is that of fp64 arithmetic (p, keys and group scores in fp64);
+ * the weights are within 2^-20 (relative) of exact ones.  A NaN logit counts as -inf, a NaN key or group score ranks as
  * -inf; with +inf among softmax logits the +inf entries share the scores, and
  * a row of -inf only has scores 0.  The ids are always K different experts of
  * the chosen groups, also where keys are -inf.
@@ -307,6 +307,7 @@ MOE_API moe_status_t moe_finalize_rmsnorm(const moe_bf16_t* x, const moe_bf16_t*
  * (moe_grouped_up_swiglu_routed); moe_layer also takes it by itself when the
  * single launch cannot be made (a GPU shared with other work that cannot
  * hold one CTA per SM at once).
+ * MOE_W_INT8 and MOE_W_NVFP4 weights take separate launches at every shape.
  * Intermediates live in ws (moe_layer_workspace_size bytes, 256-byte aligned);
  * the first int32 of ws is the layer's device error word (cleared by each
  * call; read it with moe_get_device_error((const int32_t*)ws, ...)).

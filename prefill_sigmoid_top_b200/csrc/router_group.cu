@@ -34,10 +34,10 @@
 // exactly, one per lane, and put in order; the rest goes to the fp64 path as a whole, whose 10 to 40 us for one token
 // would otherwise be the tail of every large call.
 //
-// Measured (256 experts in 8 groups, 4 kept, K = 8, sigmoid and bias, fp32): 8 tokens 2.7 us, 32767 tokens 27 us
-// (1.3 TB/s; 656 instructions per token, 81% of the issue slots in use); 2048 tokens of bf16 logits, softmax, K = 16:
-// 4.0 us.  Tried and slower: persistent warps that fetch their next token ahead (35 us), keys and ids in shared memory
-// with two warp reductions per choice (50 us).
+// Measured (256 experts in 8 groups, 4 kept, K = 8, sigmoid and bias, fp32): 8 tokens 2.6 us, 32767 tokens 23.6 us
+// (1.5 TB/s; about 650 instructions per token, 81% of the issue slots in use); 2048 tokens of bf16 logits, softmax,
+// K = 16: 3.9 us.  Tried and slower: persistent warps that fetch their next token ahead (35 us), keys and ids in
+// shared memory with two warp reductions per choice (50 us).
 #include "common.cuh"
 #include "kernels.h"
 
