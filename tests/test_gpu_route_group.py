@@ -117,6 +117,26 @@ def test_keys_that_fp32_cannot_tell_apart():
     check(z2[:1], (0.75 - p[0]).float(), 16, 4, 2)
 
 
+@pytest.mark.parametrize("group_score", [moe.GROUP_MAX, moe.GROUP_TOP2])
+@pytest.mark.parametrize("G,gs,TG", [(8, 32, 4), (4, 16, 1), (16, 16, 7), (2, 64, 1), (5, 24, 2)])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["fp32", "bf16"])
+def test_groups_that_fp32_cannot_tell_apart(G, gs, TG, group_score, dtype):
+    """Groups that are permutations of each other up to a few steps of fp32 (or exactly), with and without a bias; some
+    with three or more nearly equal best experts."""
+    g = torch.Generator().manual_seed(G * gs)
+    M = 64
+    one = torch.randn(M, gs, generator=g)
+    one[16:32, :5] = one[16:32].amax(1, keepdim=True) + torch.arange(5) * 2.0 ** -22
+    z = torch.stack([one[:, torch.randperm(gs, generator=g)] for _ in range(G)], 1)
+    z += torch.randint(-3, 4, z.shape, generator=g) * 2.0 ** -24 * (torch.arange(M) % 4 > 0)[:, None, None]
+    z = z.reshape(M, G * gs).to(dtype)
+    b = torch.full((G * gs,), 0.125)
+    b2 = b + torch.randint(-2, 3, (G * gs,), generator=g) * 2.0 ** -26
+    for bias in (None, b, b2):
+        check(z, bias, 6, G, TG, group_score)
+        check(z, bias, 6, G, TG, group_score, moe.SCORE_SOFTMAX)
+
+
 @pytest.mark.parametrize("scoring", [moe.SCORE_SIGMOID, moe.SCORE_SOFTMAX])
 def test_infinities_and_nan(scoring):
     inf, nan = float("inf"), float("nan")
