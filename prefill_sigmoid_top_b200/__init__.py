@@ -300,6 +300,12 @@ def _want(t, dtype, shape, what):
     return t
 
 
+def _ws_bytes(ws):
+    if not ws.is_contiguous():
+        raise ValueError("ws: expected a contiguous tensor")
+    return ws.nbytes
+
+
 @functools.lru_cache(maxsize=256)
 def _group_opts(n_group, topk_group, group_score, scoring, renormalize, routed_scale):
     """The options as the library takes them (it only reads them): built once for each setting."""
@@ -333,7 +339,7 @@ def route_group(x, w_router, bias, top_k, n_group=1, topk_group=1, group_score=G
         ws = x.new_empty(max(route_workspace_size(shape), 1), dtype=torch.uint8)
     opts = _group_opts(n_group, topk_group, group_score, scoring, renormalize, routed_scale)
     _launch(dev, "moe_route_group", _bf16(x).data_ptr(), w_router.data_ptr(), _adr(bias), shape.c(), opts,
-            topk_ids.data_ptr(), topk_w.data_ptr(), ws.data_ptr(), ws.numel())
+            topk_ids.data_ptr(), topk_w.data_ptr(), ws.data_ptr(), _ws_bytes(ws))
     return topk_ids, topk_w
 
 
@@ -682,7 +688,7 @@ def layer_int8(x, w_router, bias, iw: Int8Weights, gamma, eps, top_k, block_size
         _want(t, dtype, (M, cols), what)
     _launch(dev, "moe_layer", _bf16(x).data_ptr(), _bf16(w_router).data_ptr(), _adr(bias), ctypes.byref(iw.c()),
             _bf16(gamma).data_ptr(), float(eps), shape.c(), out.data_ptr(), _adr(residual_out), _adr(topk_ids),
-            _adr(topk_w), ws.data_ptr(), ws.numel())
+            _adr(topk_w), ws.data_ptr(), _ws_bytes(ws))
     return out
 
 

@@ -1152,6 +1152,7 @@ moe_status_t moe_route_logits(const void* logits, moe_dtype_t dtype, int64_t ld,
   if (st != MOE_OK) return st;
   if (!logits || !topk_ids || !topk_w) return MOE_ERR_INVALID_ARG;
   if ((dtype != MOE_DT_F32 && dtype != MOE_DT_BF16) || ld < E) return MOE_ERR_INVALID_ARG;
+  if ((reinterpret_cast<uintptr_t>(logits) & (dtype == MOE_DT_F32 ? 3u : 1u)) != 0) return MOE_ERR_INVALID_ARG;
   return cuda_status(moe::launch_route_group(logits, dtype == MOE_DT_BF16, ld, bias, M, E, top_k, group_opts(*opts),
                                              topk_ids, topk_w, static_cast<cudaStream_t>(stream)));
 }
@@ -1164,7 +1165,7 @@ moe_status_t moe_route_group(const moe_bf16_t* x, const moe_bf16_t* w_router, co
   if ((st = check_group_route(s.M, s.E, s.top_k, opts)) != MOE_OK) return st;
   if (!x || !w_router || !topk_ids || !topk_w) return MOE_ERR_INVALID_ARG;
   if (!aligned16(x) || !aligned16(w_router)) return MOE_ERR_INVALID_ARG;
-  if (!ws || ws_bytes < moe_route_workspace_size(s)) return MOE_ERR_WORKSPACE;
+  if (!ws || ws_bytes < moe_route_workspace_size(s) || !aligned16(ws)) return MOE_ERR_WORKSPACE;
   auto cs = static_cast<cudaStream_t>(stream);
   auto* logits = static_cast<float*>(ws);
   if ((st = cuda_status(moe::launch_router_logits(x, w_router, nullptr, s.M, s.H, s.E, logits, cs))) != MOE_OK)

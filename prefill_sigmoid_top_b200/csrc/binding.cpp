@@ -139,7 +139,7 @@ PyObject* route_logits(PyObject*, PyObject* const* a, Py_ssize_t n) {
     o.routed_scale = static_cast<float>(in.real());
     const Tensor* ids_in = in.tensor_or_none();
     const Tensor* w_in = in.tensor_or_none();
-    const int64_t k = K < 0 ? 0 : K;
+    const int64_t k = K < 0 || K > E ? 0 : K;  // what the entry point refuses gets no memory
     if (ids_in) want(*ids_in, at::kInt, {M, k}, "topk_ids");
     if (w_in) want(*w_in, at::kFloat, {M, k}, "topk_w");
     const c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(in.device));

@@ -132,6 +132,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after_sync();
   const uint32_t tmem = *tmem_slot;
   if (first >= total) {  // the whole cluster leaves
+    if (total == 0) grid_dependency_wait();  // someone has to wait: the launch must not end before the quantiser
     if (warp == kMmaWarp) tmem_dealloc(tmem, C::kTmemCols);
     return;
   }
@@ -277,7 +278,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == kMmaWarp) {
     // ------------------------------------------------ MMA issuer
     if (lane == 0) {
-      int it = 0, j = 0;
+      int it = 0, j = 0, committed = 0;  // tiles
       bool alive = true;
       for (int tile = first; tile < total && alive; tile += step, ++j) {
         const uint32_t idesc = umma_idesc_s8(kBM, tile_at(tile).N);
@@ -310,7 +311,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           umma_commit(&empty[s]);
         }
         umma_commit(&acc_full[buf]);  // also after an abort, so that the epilogue is not left waiting
+        committed = j + 1;
       }
+      // after an abort nobody else waits for the products under way, which still read the ring
+      if (*abort_flag && committed > 0)
+        mbar_wait_bounded(&acc_full[(committed - 1) % kBufs], ((committed - 1) / kBufs) & 1, nullptr);
     }
     __syncwarp();
   } else {

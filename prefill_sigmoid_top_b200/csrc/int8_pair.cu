@@ -42,6 +42,7 @@ constexpr int kMmaWarp = 3;
 constexpr int kFirstEpi = 4;
 constexpr int kEpiWarps = 16;
 constexpr int kThreads = 32 * (kFirstEpi + kEpiWarps);
+constexpr uint64_t kDrainNs = 10ull * 1000ull * 1000ull;  // after an abort
 
 enum Mode { kUp = 0, kDown = 1, kDense = 2 };
 
@@ -112,7 +113,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   __syncthreads();
   const int total = kMode == kDense ? W * dense_tiles : prefix[E];
-  if (pair >= total) return;  // both CTAs of a pair see the same count
+  if (pair >= total) {  // both CTAs of a pair see the same count
+    if (total == 0) grid_dependency_wait();  // someone has to wait: the launch must not end before the quantiser
+    return;
+  }
   if (warp == kMmaWarp) {
     tmem_alloc_pair(tmem_slot, 512);
     tmem_relinquish_pair();
@@ -228,11 +232,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     }
+    // After an abort nobody waits for the copies under way, and the leader's barriers count both CTAs' copies, of which
+    // the other may have issued fewer.  So they get time to land: a ring of 192 KB needs some microseconds.
+    if ((!alive || *abort_flag) && lane == 0)
+      for (const uint64_t t0 = global_timer_ns(); global_timer_ns() - t0 < kDrainNs;) {
+      }
     __syncwarp();
   } else if (warp == kMmaWarp) {
     // ------------------------------------------------ MMA issuer (leader only)
     if (leader && lane == 0) {
-      int it = 0, j = 0;
+      int it = 0, j = 0, committed = 0;  // tiles
       bool alive = true;
       for (int tile = pair; tile < total && alive; tile += npairs, ++j) {
         const uint32_t idesc = umma_idesc_s8(2 * kBM, tile_at(tile).N);
@@ -266,7 +275,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           umma_commit_pair(&empty[s]);
         }
         umma_commit_pair(&acc_full[buf]);  // also on an abort, so neither epilogue is left waiting
+        committed = j + 1;
       }
+      // after an abort nobody else waits for the products under way, which still read both rings
+      if (*abort_flag && committed > 0)
+        mbar_wait_bounded(&acc_full[(committed - 1) % C::kAccBufs], ((committed - 1) / C::kAccBufs) & 1, nullptr);
     }
     __syncwarp();
   } else {

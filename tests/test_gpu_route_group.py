@@ -244,3 +244,20 @@ def test_captured_replayed_and_on_another_stream():
     torch.cuda.synchronize()
     ids_r, _ = reference(z2.numpy(), b.numpy(), 8, 8, 4, moe.GROUP_TOP2, moe.SCORE_SIGMOID, True, 1.0)
     assert np.array_equal(out[0].cpu().numpy(), ids_r)
+
+
+def test_refused_sizes_and_workspaces():
+    z = torch.randn(5, 64, device=DEV)
+    for K in (65, 2 ** 30):
+        with pytest.raises(moe.MoEError) as e:
+            moe.route_logits(z, None, K)
+        assert e.value.status == 2
+    x, w = torch.randn(5, 256, device=DEV).bfloat16(), torch.randn(64, 256, device=DEV).bfloat16()
+    with pytest.raises(ValueError):  # one byte that claims to be many
+        moe.route_group(x, w, None, 4, 8, 4, ws=torch.zeros(1, dtype=torch.uint8, device=DEV).expand(1 << 20))
+    ws = torch.zeros((1 << 20) + 16, dtype=torch.uint8, device=DEV)
+    with pytest.raises(moe.MoEError) as e:
+        moe.route_group(x, w, None, 4, 8, 4, ws=ws[2:])
+    assert e.value.status == 3
+    a, b = moe.route_group(x, w, None, 4, 8, 4, ws=ws[16:]), moe.route_group(x, w, None, 4, 8, 4)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])

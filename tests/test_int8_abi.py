@@ -24,6 +24,7 @@ def test_route_logits_refusals():
     inf, nan = float("inf"), float("nan")
     assert route(logits=None) == 1 and route(ids=None) == 1 and route(w=None) == 1 and route(o=None) == 1
     assert route(dtype=2) == 1 and route(dtype=-1) == 1 and route(ld=63) == 1
+    assert route(logits=ctypes.c_void_p(P + 2)) == 1 and route(logits=ctypes.c_void_p(P + 1), dtype=1) == 1
     for o in [(2, 1, 8, 4, 1, 1.0), (1, 1, 8, 4, 2, 1.0), (1, 1, 8, 4, -1, 1.0), (1, 1, 8, 4, 1, 0.0),
               (1, 1, 8, 4, 1, inf), (1, 1, 8, 4, 1, nan), (1, 1, 8, 4, 1, -1.0)]:
         assert route(o=o) == 1
@@ -39,7 +40,7 @@ def test_route_group_refusals():
     call = lambda x=FAKE, s=S, o=ctypes.byref(o), ws=FAKE, n=1 << 20: L.moe_route_group(  # noqa: E731
         x, FAKE, None, s.c(), o, FAKE, FAKE, ws, n, None)
     assert call(x=None) == 1 and call(x=FAKE_MIS) == 1 and call(o=None) == 1
-    assert call(ws=None) == 3 and call(n=4) == 3
+    assert call(ws=None) == 3 and call(n=4) == 3 and call(ws=FAKE_MIS) == 3
     assert call(o=ctypes.byref(_GroupOpts(1, 1, 3, 2, 1, 1.0))) == 2
     assert call(s=moe.Shape(16, 255, 128, 8, 2, 16)) == 2
 
