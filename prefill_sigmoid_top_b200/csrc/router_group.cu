@@ -401,18 +401,33 @@ __global__ void __launch_bounds__(32 * kWarps) route_group_kernel(const void* __
     // as an integer in every lane of the group: steps, or the bits of a (positive) sum of scores
     uint32_t s = a;
     if (group_sums) s = by_logit ? __float_as_uint(score32(value_of(a)) + score32(value_of(b))) : a + b;
-    int before = 0;  // groups ahead of this lane's
-#pragma unroll 4
-    for (int q = 0; q < o.n_group; ++q) {
-      const uint32_t x = __shfl_sync(0xffffffffu, s, q << lanes_log);
-      before += x > s || (x == s && q < group);
-    }
-    // the last group that stays against the first that does not
+    // the last group that stays (shi) and the first that does not (slo), ties to the lower group
     const bool real = group < o.n_group;
-    const unsigned last = __ballot_sync(0xffffffffu, real && before == o.topk_group - 1);
-    const unsigned next = __ballot_sync(0xffffffffu, real && before == o.topk_group);
-    const uint32_t shi = __shfl_sync(0xffffffffu, s, (__ffs(last) - 1) & 31);
-    const uint32_t slo = __shfl_sync(0xffffffffu, s, (__ffs(next) - 1) & 31);
+    bool stays;
+    uint32_t shi = 0, slo;
+    if (!(group_sums && by_logit)) {  // integers below 2^26: with the inverted group below, a maximum per group
+      const uint32_t key = real ? (s << 5) + (31u - group) : 0u;
+      uint32_t left = key, best = 0;
+      for (int k = 0; k < o.topk_group; ++k) {
+        best = __reduce_max_sync(0xffffffffu, left);
+        left = left == best ? 0u : left;
+      }
+      stays = key >= best;
+      shi = best >> 5;
+      slo = __reduce_max_sync(0xffffffffu, left) >> 5;
+    } else {
+      int before = 0;  // groups ahead of this lane's
+#pragma unroll 4
+      for (int q = 0; q < o.n_group; ++q) {
+        const uint32_t x = __shfl_sync(0xffffffffu, s, q << lanes_log);
+        before += x > s || (x == s && q < group);
+      }
+      const unsigned last = __ballot_sync(0xffffffffu, real && before == o.topk_group - 1);
+      const unsigned next = __ballot_sync(0xffffffffu, real && before == o.topk_group);
+      shi = __shfl_sync(0xffffffffu, s, (__ffs(last) - 1) & 31);
+      slo = __shfl_sync(0xffffffffu, s, (__ffs(next) - 1) & 31);
+      stays = real && before < o.topk_group;
+    }
     const int apart = static_cast<int>(shi - slo);
     if (!by_logit) {
       groups_good = static_cast<float>(apart - 4) * sure > 4.0f * off_key;
@@ -422,7 +437,10 @@ __global__ void __launch_bounds__(32 * kWarps) route_group_kernel(const void* __
     } else {
       groups_good = logits_clear(shi, apart, value_of(shi), value_of(slo));
     }
-    if (!(real && before < o.topk_group)) {
+    // the lowest integer stands for anything below the range: a sum with it is an upper bound, which will do for a
+    // group that goes (the lowest key comes out as 1 or 2)
+    if (group_sums && stays && b <= 2) groups_good = false;
+    if (!stays) {
 #pragma unroll
       for (int i = 0; i < kPer; ++i) u[i / kLen][i % kLen] = 0;
     }
@@ -431,7 +449,8 @@ __global__ void __launch_bounds__(32 * kWarps) route_group_kernel(const void* __
   // ---- 4. experts
   const int rounds = min(K + 1, o.topk_group * gs);
   uint32_t mine = 0, top = 0;  // of round `lane`; of the last round
-  for (int k = 0; k < rounds; ++k) {
+  // of a list that gave `top` away, what `needed` more rounds can ask for moves up
+  auto round = [&](int k, int needed) {
     uint32_t best = u[0][0];
 #pragma unroll
     for (int c = 1; c < kLists; ++c) best = max(best, u[c][0]);
@@ -441,11 +460,21 @@ __global__ void __launch_bounds__(32 * kWarps) route_group_kernel(const void* __
       for (int c = 0; c < kLists; ++c)
         if (kLists == 1 || u[c][0] == top) {
 #pragma unroll
-          for (int i = 1; i < kLen; ++i) u[c][i - 1] = u[c][i];
-          u[c][kLen - 1] = 0;
+          for (int i = 1; i < kLen; ++i)
+            if (i <= needed) u[c][i - 1] = u[c][i];
+          if (needed >= kLen) u[c][kLen - 1] = 0;
         }
     }
     if (lane == k) mine = top;
+  };
+  constexpr int kFew = 9;
+  if (kLists == 1 && rounds <= kFew && rounds + 3 > kFew) {
+    // 6 to 8 choices: nine rounds without a loop (one too many costs less than leaving early), each of which needs one
+    // less of every list
+#pragma unroll
+    for (int k = 0; k < kFew; ++k) round(k, kFew - k);
+  } else {
+    for (int k = 0; k < rounds; ++k) round(k, kLen);
   }
   // every choice against the next one: lane k compares rounds k and k + 1 (round 32 is in no lane)
   auto id_of = [&](uint32_t x) { return min(static_cast<int>(id_mask - (x & id_mask)), E - 1); };
@@ -473,6 +502,8 @@ __global__ void __launch_bounds__(32 * kWarps) route_group_kernel(const void* __
       uint32_t rest = u[0][0];
 #pragma unroll
       for (int c = 1; c < kLists; ++c) rest = max(rest, u[c][0]);
+      const uint32_t extra = __shfl_sync(0xffffffffu, mine, listed & 31);  // of a round too many
+      if (listed < 32) rest = max(rest, extra);
       rest = __reduce_max_sync(0xffffffffu, rest);
       const int apart =
           static_cast<int>(__shfl_sync(0xffffffffu, mine, K - 1) >> id_bits) - static_cast<int>(rest >> id_bits);

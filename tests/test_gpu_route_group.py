@@ -261,3 +261,24 @@ def test_refused_sizes_and_workspaces():
     assert e.value.status == 3
     a, b = moe.route_group(x, w, None, 4, 8, 4, ws=ws[16:]), moe.route_group(x, w, None, 4, 8, 4)
     assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+@pytest.mark.parametrize("scoring", [moe.SCORE_SIGMOID, moe.SCORE_SOFTMAX])
+@pytest.mark.parametrize("far", [-6.0, -20.0, -60.0, -1e30, float(torch.finfo(torch.float32).min), -float("inf")])
+@pytest.mark.parametrize("G,gs,TG,K", [(8, 32, 4, 4), (4, 16, 1, 1), (2, 4, 1, 1), (16, 64, 5, 5), (5, 7, 2, 2)])
+def test_groups_with_one_expert_in_reach(G, gs, TG, K, far, scoring):
+    """Groups of which one expert or a few are near the best and the others far below it, by their logits or by the
+    bias: a sum of two keys has to see how far below."""
+    g = torch.Generator().manual_seed(G * gs + 1)
+    M = 96
+    near = torch.rand(M, G, gs, generator=g) < 1.5 / gs
+    near[:, :, 0] |= torch.rand(M, G, generator=g) < 0.5
+    z = torch.randn(M, G, gs, generator=g) * 2.0
+    hidden = torch.where(near, z, torch.full_like(z, far)).reshape(M, G * gs)
+    check(hidden, None, K, G, TG, moe.GROUP_TOP2, scoring)
+    check(hidden, None, K, G, TG, moe.GROUP_MAX, scoring)
+    check(hidden, 0.05 * torch.randn(G * gs, generator=g), K, G, TG, moe.GROUP_TOP2, scoring)
+    bias = torch.where(near[0], torch.zeros(G, gs), torch.full((G, gs), far))
+    bias += torch.where(torch.arange(G)[:, None] % 2 == 1, -1.5 * (bias == 0), torch.zeros(G, gs))
+    check(z.reshape(M, G * gs), bias.reshape(-1), K, G, TG, moe.GROUP_TOP2, scoring)
+    check(z.reshape(M, G * gs), bias.reshape(-1), K, G, TG, moe.GROUP_MAX, scoring)
