@@ -371,9 +371,9 @@ __global__ void __launch_bounds__(32 * kWarps) route_group_kernel(const void* __
   auto value_of = [&](uint32_t q) { return fmaf(static_cast<float>(q), step, kmax - range); };
 
   // Two logits give scores that fp64 tells apart, in their order: they differ by more than 2^-30, and neither score
-  // is so near to 1 or to 0 that the difference is lost there.
+  // is so near to 1 or to 0 that the difference is lost there (e^-80 is above whatever lies below e^-600).
   auto clear_of_limits = [&](float zhi, float zlo) {
-    return softmax ? zlo - zmax > -600.0f : (zhi < 12.0f && zlo > -600.0f);
+    return softmax ? (zlo - zmax > -600.0f || zhi - zmax > -80.0f) : (zhi < 12.0f && (zlo > -600.0f || zhi > -80.0f));
   };
   // Two logits with the integers q and q - apart: a tie, or apart as above (in the lowest integer anything may be).
   auto logits_clear = [&](uint32_t q, int apart, float zhi, float zlo) {
@@ -490,8 +490,17 @@ __global__ void __launch_bounds__(32 * kWarps) route_group_kernel(const void* __
     good = by_logit ? logits_clear(mine >> id_bits, apart, zsel, zlo)
                     : static_cast<float>(apart - 2) * sure > 2.0f * off_key;
   }
+  // Not finite: an expert masked by -inf, in its logit or its bias, has the lowest integer like all that is far below;
+  // +inf and NaN, and rows without a finite key, are the fp64 path's.
+  bool usable = whole == 0.0f;
+  if (!__all_sync(0xffffffffu, usable)) {
+    usable = fabsf(kmax) < INFINITY && fabsf(zmax) < INFINITY;
+#pragma unroll 1
+    for (int i = 0; i < n; ++i)
+      usable = usable && raw_logit<kBf16>(row, e0 + i) < INFINITY && (by_logit || bias[e0 + i] < INFINITY);
+  }
   // scores far below the fp32 range are the fp64 path's
-  const bool plain = groups_good && whole == 0.0f && !(lane < K && (softmax ? zsel - zmax : zsel) < -80.0f);
+  const bool plain = groups_good && usable && !(lane < K && (softmax ? zsel - zmax : zsel) < -80.0f);
   bool settled = __all_sync(0xffffffffu, plain && good);
   if (!settled && __all_sync(0xffffffffu, plain) && (by_logit || !softmax) && K < 32) {
     // only neighbours in the list are too near: put the list in order by exact keys.  Nothing outside it can belong

@@ -282,3 +282,21 @@ def test_groups_with_one_expert_in_reach(G, gs, TG, K, far, scoring):
     bias += torch.where(torch.arange(G)[:, None] % 2 == 1, -1.5 * (bias == 0), torch.zeros(G, gs))
     check(z.reshape(M, G * gs), bias.reshape(-1), K, G, TG, moe.GROUP_TOP2, scoring)
     check(z.reshape(M, G * gs), bias.reshape(-1), K, G, TG, moe.GROUP_MAX, scoring)
+
+
+@pytest.mark.parametrize("scoring", [moe.SCORE_SIGMOID, moe.SCORE_SOFTMAX])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["fp32", "bf16"])
+@pytest.mark.parametrize("part", [0.02, 0.5, 0.97])
+@pytest.mark.parametrize("G,gs,TG,K", [(8, 32, 4, 8), (1, 64, 1, 4), (4, 16, 2, 10), (16, 64, 8, 16), (3, 5, 2, 3)])
+def test_experts_masked_by_infinities(G, gs, TG, K, part, dtype, scoring):
+    """A part of the experts masked by -inf in their logits, in the bias, or both; a few rows with +inf or NaN too."""
+    g = torch.Generator().manual_seed(int(G * gs + 100 * part))
+    z, b = rand(64, G * gs, G * gs + K, dtype)
+    zm, bm = z.clone(), b.clone()
+    zm[torch.rand(z.shape, generator=g) < part] = -float("inf")
+    bm[torch.rand(b.shape, generator=g) < part] = -float("inf")
+    zm[5, 2], zm[9, 1] = float("inf"), float("nan")
+    for group_score in (moe.GROUP_MAX, moe.GROUP_TOP2):
+        for logits, bias in ((zm, None), (zm, b), (z, bm), (zm, bm)):
+            check(logits, bias, K, G, TG, group_score, scoring)
+            check(logits, bias, K, G, TG, group_score, scoring, renorm=False)
