@@ -10,7 +10,7 @@
 // The choice is a comparison of rounded numbers, so it is defined in fp64: p, keys and group scores.  fp64 arithmetic
 // is slow (a token of 256 experts: 20 us alone, and 168 us for 32767 tokens), so a token is first routed in fp32 with
 // a bound on what fp32 may be off by, and only where two candidates next to each other are nearer than that (or a
-// number is not finite, or far out) its warp computes it again in fp64.  The result is the fp64 one either way.
+// number is NaN, +inf or far out) its warp computes it again in fp64.  The result is the fp64 one either way.
 //
 // fp32 path, one warp per token, no shared memory.  What bounds it is the ALU pipe (compare, select, minimum and
 // integer logic issue at half rate), so keys are shaped with multiply-adds and compared as few times as can be:
@@ -19,7 +19,8 @@
 //  2. a key becomes an integer, its place between kmax - range and kmax in 2^23 (2^22) steps, with the inverted expert
 //     id below: two multiply-adds and one integer multiply-add.  All are different; larger key first, lower id first.
 //     A lane sorts its own in lists of 8 (Batcher's network: one minimum and one maximum per exchange).
-//  3. group scores from the two first integers of each lane, joined over the group's lanes by shuffles.
+//  3. group scores from the two first integers of each lane, joined over the group's lanes by shuffles; the groups that
+//     stay by one warp maximum each.
 //  4. top_k + 1 rounds of ONE warp maximum (redux) over the lists' first integers; the owner moves its list up.  The
 //     round past the last shows the gap behind the choice.
 //  5. weights from the K logits.
@@ -29,14 +30,15 @@
 //            rcp.approx within 2^-23; the scaled argument of the exponential adds |z| 2^-23.4 relative)
 //   softmax: relative 2^-19 + |z - max| 2^-23, and p <= e^-|z - max| / denom: below 2^-18 / denom
 // plus 2^-23 of each sum that follows.  Of bf16 logits, two that are nearer than their spacing are equal: a tie.
-// Keys below the range share the lowest integer.  About 1 token in 1000 of normal logits and a small bias has two
+// Keys below the range, -inf among them, share the lowest integer: where one counts in the sum of a group that stays,
+// the token is fp64's.  About 1 token in 1000 of normal logits and a small bias has two
 // neighbours too near (2 in 100 with 1024 experts and K = 32).  Where that is all, the K + 1 listed keys are computed
 // exactly, one per lane, and put in order; the rest goes to the fp64 path as a whole, whose 10 to 40 us for one token
 // would otherwise be the tail of every large call.
 //
-// Measured (256 experts in 8 groups, 4 kept, K = 8, sigmoid and bias, fp32): 8 tokens 2.6 us, 32767 tokens 23.6 us
-// (1.5 TB/s; about 650 instructions per token, 81% of the issue slots in use); 2048 tokens of bf16 logits, softmax,
-// K = 16: 3.9 us.  Tried and slower: persistent warps that fetch their next token ahead (35 us), keys and ids in
+// Measured (256 experts in 8 groups, 4 kept, K = 8, sigmoid and bias, fp32): 8 tokens 2.6 us, 32767 tokens 21.6 us
+// (1.6 TB/s; 577 instructions per token, 79% of the issue slots in use; more warps per SM change nothing); 2048 tokens of bf16 logits, softmax,
+// K = 16: 3.9 us; a part of the experts masked by -inf changes nothing (softmax: 32 -> 40 us).  Tried and slower: persistent warps that fetch their next token ahead (35 us), keys and ids in
 // shared memory with two warp reductions per choice (50 us).
 #include "common.cuh"
 #include "kernels.h"
@@ -292,9 +294,6 @@ __global__ void __launch_bounds__(32 * kWarps) route_group_kernel(const void* __
 #pragma unroll
     for (int i = 0; i < kPer; ++i) v[i] = i < n ? raw_logit<kBf16>(row, e0 + i) : 0.0f;
   }
-  float whole = 0.0f;  // NaN as soon as a logit (later: a key) is not finite
-#pragma unroll
-  for (int i = 0; i < kPer; ++i) whole = fmaf(v[i], 0.0f, whole);
   float zmax = 0.0f, denom = 1.0f;
   if (softmax) {
     zmax = -INFINITY;
@@ -338,10 +337,11 @@ __global__ void __launch_bounds__(32 * kWarps) route_group_kernel(const void* __
   for (int i = 0; i < kPer; ++i)
     if (kFull || i < n) hi = fmaxf(hi, v[i]);
   const float kmax = from_order_bits(__reduce_max_sync(0xffffffffu, order_bits(hi)));
-  if (!by_logit) {
+  // NaN as soon as a key is not finite; what a logit's NaN, or under softmax +inf, does to its key (a sigmoid of an
+  // infinity is 0 or 1)
+  float whole = 0.0f;
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) whole = fmaf(v[i], 0.0f, whole);
-  }
+  for (int i = 0; i < kPer; ++i) whole = fmaf(v[i], 0.0f, whole);
 
   // ---- 2. integers
   const int id_bits = max(8, 32 - __clz(E - 1));  // E <= 1024: at most 10
@@ -560,8 +560,12 @@ __global__ void __launch_bounds__(32 * kWarps) route_group_kernel(const void* __
     }
   }
   float total = p;
+  if (K > 8) {
+    total += __shfl_xor_sync(0xffffffffu, total, 16);
+    total += __shfl_xor_sync(0xffffffffu, total, 8);
+  }
 #pragma unroll
-  for (int off = 16; off >= 1; off >>= 1) total += __shfl_xor_sync(0xffffffffu, total, off);
+  for (int off = 4; off >= 1; off >>= 1) total += __shfl_xor_sync(0xffffffffu, total, off);
   if (lane < K) {
     ids[lane] = sel;
     w[lane] = p * rcp_approx(o.renormalize ? total : denom) * o.routed_scale;
