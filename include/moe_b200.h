@@ -168,9 +168,10 @@ MOE_API moe_status_t moe_route_ex(const moe_bf16_t* x, const moe_bf16_t* w_route
  *   topk_ids[t,0..K) = the K largest keys among their experts, descending, ties
  *           -> lower id;  topk_w[t,k] = w_k * routed_scale with w_k = p_k, or
  *           p_k / sum_j p_j over the K selected (renormalize; 0 if that sum is 0).
- * The selection is that of fp64 arithmetic (p, keys and group scores in fp64);
- * the weights are within 2^-20 (relative) of exact ones.  A NaN logit counts as -inf, a NaN key or group score ranks as
- * -inf; with +inf among softmax logits the +inf entries share the scores, and
+ * The selection is that of fp64 arithmetic (p, keys and group scores in fp64,
+ * the softmax sum in any order);
+ * the weights are within 2^-19 (relative) of exact ones.  A NaN logit counts as
+ * -inf, a NaN key or group score ranks as -inf; with +inf among softmax logits the +inf entries share the scores, and
  * a row of -inf only has scores 0.  The ids are always K different experts of
  * the chosen groups, also where keys are -inf.
  * logits: fp32 or bf16 (dtype) [M, E], row t at logits + t * ld elements, ld >= E;

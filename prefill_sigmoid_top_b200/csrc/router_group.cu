@@ -29,7 +29,9 @@
 //   sigmoid: |p32 - p| <= p (1 - p) (|z| 2^-23.4 + 2^-22) + p (2^-24 + 2^-23) < 1.5 * 2^-22 (ex2.approx is within 2^-22,
 //            rcp.approx within 2^-23; the scaled argument of the exponential adds |z| 2^-23.4 relative)
 //   softmax: relative 2^-19 + |z - max| 2^-23, and p <= e^-|z - max| / denom: below 2^-18 / denom
-// plus 2^-23 of each sum that follows.  Of bf16 logits, two that are nearer than their spacing are equal: a tie.
+//            (exponentials 2^-22, their sum 11 roundings, reciprocal and product 2^-22: less than 2^-19)
+// plus 2^-23 of each sum that follows.  Weights: an exponential and a denominator of such (sigmoid: a sum of K <= 32
+// scores in 5 levels), at most 24 roundings of 2^-24: within 2^-19.  Of bf16 logits, two that are nearer than their spacing are equal: a tie.
 // Keys below the range, -inf among them, share the lowest integer: where one counts in the sum of a group that stays,
 // the token is fp64's.  About 1 token in 1000 of normal logits and a small bias has two
 // neighbours too near (2 in 100 with 1024 experts and K = 32).  Where that is all, the K + 1 listed keys are computed
@@ -228,6 +230,15 @@ __device__ __forceinline__ void sort_descending(uint32_t (&v)[kN]) {
           }
 }
 
+// f(from) + .. + f(from + kN - 1) in pairs: log2(kN) roundings deep.
+template <int kN, class F>
+__device__ __forceinline__ float tree_sum(const F& f, int from = 0) {
+  if constexpr (kN == 1)
+    return f(from);
+  else
+    return tree_sum<kN / 2>(f, from) + tree_sum<kN / 2>(f, from + kN / 2);
+}
+
 // kPer: experts per lane, rounded up to a power of two.  kFull: every lane has exactly kPer, and every lane's logits
 // start at a multiple of 16 bytes (or 8 experts or fewer at one of their own size).
 template <bool kBf16, int kPer, bool kFull>
@@ -302,10 +313,7 @@ __global__ void __launch_bounds__(32 * kWarps) route_group_kernel(const void* __
       if (kFull || i < n) zmax = fmaxf(zmax, v[i]);
     zmax = from_order_bits(__reduce_max_sync(0xffffffffu, order_bits(zmax)));
     if (!by_logit || group_sums || !o.renormalize) {
-      denom = 0.0f;
-#pragma unroll
-      for (int i = 0; i < kPer; ++i)
-        if (kFull || i < n) denom += expf(v[i] - zmax);
+      denom = tree_sum<kPer>([&](int i) { return kFull || i < n ? expf(v[i] - zmax) : 0.0f; });
 #pragma unroll
       for (int off = 16; off >= 1; off >>= 1) denom += __shfl_xor_sync(0xffffffffu, denom, off);
     }
