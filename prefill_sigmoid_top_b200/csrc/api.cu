@@ -671,38 +671,49 @@ bool linear_int8_shape_ok(int64_t M, int64_t N, int64_t K) {
 }
 int64_t linear_int8_pitch(int64_t K) { return (K + 15) / 16 * 16; }
 
-// Tokens per tile of the dense product on pairs (512 channels each), or 0 for the kernel with 128 channels x up to 128
-// tokens per CTA.  By estimated time, from measurements of both on 22 sizes (33 to 8192 tokens, 512 to 7168 channels
-// and columns; the estimates are within about 20 percent, the choice right or within 10 percent of the better one).
-// In us, nk = K / 128 steps:
-//   pairs:   4 + rounds of tiles over the pairs x (nk (0.48 + 0.0016 t) + 2) for t tokens per tile: whole tiles of
-//            256 leave a last round short, so t is chosen too;
-//   one CTA, split over a cluster of S:  nk/S (0.3 + 0.0045 t) + 6 + 0.05 t;  unsplit: rounds x (0.35 nk + 4.3).
-// Up to 32 tokens the weight stream of the CTAs wins throughout (a few tokens: int8_few.cu).
-int linear_int8_tile(int64_t M, int64_t N, int64_t K) {
+// Shape of the dense product's tiles: on pairs (256 channels per box of each CTA) with t tokens, or, with tokens 0,
+// the kernel with 128 channels x up to 128 tokens per CTA.  By estimated time, fitted to measurements of all forms on
+// 22 sizes (33 to 8192 tokens, 512 to 7168 channels and columns): the choice was within 2 percent of the best form on
+// each.  In us beside the quantiser, nk = K / 128 steps, a round = one tile for every pair (CTA):
+//   two boxes:  rounds x (0.45 nk + 0.6 + 0.025 t), one accumulator set, so a tile's epilogue holds the next one up;
+//   one box:    rounds x ((0.31 + 0.0001 t) nk + 1.2) + 0.005 t, two sets;
+//   one CTA, split over a cluster of S:  rounds x nk/S (0.14 + 0.0023 t) + 1.7 + 0.054 t;
+//   unsplit:    rounds x (0.25 nk + 5.7).
+// Two boxes read less per product (8192 x 7168 x 7168 needs them); one fits small sizes better: 2048 x 2048 x 7168 36
+// us against 44, 1000 x 2048 x 2048 15 against 17.  Up to 32 tokens the weight stream of the single CTAs wins
+// throughout (a few tokens: int8_few.cu).
+struct Int8Tile {
+  int tokens, boxes;  // tokens 0: not on pairs
+};
+Int8Tile linear_int8_tile(int64_t M, int64_t N, int64_t K) {
   if (const char* env = std::getenv("MOE_INT8_TILE")) {
     const int v = std::atoi(env);
-    if (v == 0 || (v >= 32 && v <= 256 && v % 32 == 0)) return v;
+    if (v == 0 || (v >= 32 && v <= 256 && v % 32 == 0)) return {v, std::strstr(env, "x1") != nullptr ? 1 : 2};
   }
-  if (M <= 32) return 0;
+  if (M <= 32) return {0, 0};
   const int sms = num_sms();
-  const int64_t pairs = sms / 2, W = (N + 511) / 512, nk = (K + 127) / 128;
-  int best = 0;
+  const int64_t pairs = sms / 2, nk = (K + 127) / 128;
+  Int8Tile best{0, 0};
   double best_cost = 0.0;
-  for (int t = 64; t <= 256; t += 32) {
-    const double rounds = static_cast<double>((W * ((M + t - 1) / t) + pairs - 1) / pairs);
-    const double cost = 4.0 + rounds * (nk * (0.48 + 0.0016 * t) + 2.0);
-    if (best == 0 || cost < best_cost) {
-      best = t;
-      best_cost = cost;
+  for (int boxes = 1; boxes <= 2; ++boxes) {
+    const int64_t W = (N + 256 * boxes - 1) / (256 * boxes);
+    for (int t = 64; t <= 256; t += 32) {
+      const double rounds = static_cast<double>((W * ((M + t - 1) / t) + pairs - 1) / pairs);
+      const double cost = boxes == 2 ? rounds * (0.45 * nk + 0.6 + 0.025 * t)
+                                     : rounds * ((0.31 + 0.0001 * t) * nk + 1.2) + 0.005 * t;
+      if (best.tokens == 0 || cost < best_cost) {
+        best = {t, boxes};
+        best_cost = cost;
+      }
     }
   }
   const int64_t tiles = (N + 127) / 128 * ((M + 127) / 128);
   const int split = moe::int8_tile_split(tiles, static_cast<int>(nk), sms);
   const double t = static_cast<double>(M >= 128 ? 128 : M);
-  const double single = split > 1 ? nk / split * (0.3 + 0.0045 * t) + 6.0 + 0.05 * t
-                                  : static_cast<double>((tiles + sms - 1) / sms) * (0.35 * nk + 4.3);
-  return best_cost < single ? best : 0;
+  const double rounds = static_cast<double>((tiles * split + sms - 1) / sms);
+  const double single = split > 1 ? rounds * nk / split * (0.14 + 0.0023 * t) + 1.7 + 0.054 * t
+                                  : rounds * (0.25 * nk + 5.7);
+  return best_cost < single ? best : Int8Tile{0, 0};
 }
 
 // moe_route_logits' options, shape and logits: MOE_OK or the status of the call.
@@ -1230,14 +1241,15 @@ moe_status_t moe_linear_int8(const moe_bf16_t* x, int64_t ldx, const int8_t* w, 
   q.scales = reinterpret_cast<float*>(base + L.scales);
   a.row_scale = q.scales;
   if (moe::launch_quantize_int8(q, cs) != cudaSuccess) return MOE_ERR_CUDA;
-  const int tile_n = linear_int8_tile(M, N, K);
+  const Int8Tile tile = linear_int8_tile(M, N, K);
   CUtensorMap mw, mx;
-  if (!make_map_i8(&mw, w, N, K, ldw, 128) || !make_map_i8(&mx, q.codes, M, K, pitch, tile_n != 0 ? 32 : 16))
+  if (!make_map_i8(&mw, w, N, K, ldw, 128) || !make_map_i8(&mx, q.codes, M, K, pitch, tile.tokens != 0 ? 32 : 16))
     return MOE_ERR_CUDA;
   // 16-byte row stores need whole, aligned vectors of 8 bf16 values
   a.out_plain = a.out_f32 || N % 8 != 0 || ldo % 8 != 0 || !aligned16(out);
-  a.tile_n = tile_n;
-  if (tile_n != 0) return cuda_status(moe::launch_int8_pair_dense(mw, mx, a, num_sms(), cs));
+  a.tile_n = tile.tokens;
+  a.tile_boxes = tile.boxes;
+  if (tile.tokens != 0) return cuda_status(moe::launch_int8_pair_dense(mw, mx, a, num_sms(), cs));
   return cuda_status(moe::launch_int8_dense(mw, mx, a, M <= 32 ? 32 : 128, num_sms(), cs));
 }
 

@@ -8,6 +8,8 @@
 // Tile: a weight block w of one expert x up to kNmax tokens; CTA r of the pair holds two boxes of 128 weight rows:
 //   up:          rows 256 w + 128 r.. of W_gate and of W_up (the two accumulators of silu(gate) * up);
 //   down, dense: rows 512 w + 128 r.. and 512 w + 256 + 128 r.. (two accumulators of M = 256 each);
+//   dense with one box: rows 256 w + 128 r.. (one accumulator of M = 256, so two sets of 256 tokens; smaller tiles fill
+//                the pairs better, 2048 x 2048 x 7168 44 -> 36 us; the down projection with it: 812 -> 882 us);
 // and token rows [r N/2, (r + 1) N/2) of the tile's N (its tokens rounded up to 32, the width step of this MMA).
 // Channels past the expert's last row are computed and not stored.
 //
@@ -46,13 +48,14 @@ constexpr uint64_t kDrainNs = 10ull * 1000ull * 1000ull;  // after an abort
 
 enum Mode { kUp = 0, kDown = 1, kDense = 2 };
 
-template <int kNmax, int kStages>
+template <int kNmax, int kStages, int kBoxes>
 struct PCfg {
   static constexpr int kHalf = kNmax / 2;
-  static constexpr int kABytes = 2 * kBoxBytes;
+  static constexpr int kABytes = kBoxes * kBoxBytes;
   static constexpr int kStage = kABytes + kHalf * kBK;
-  static constexpr int kAccCols = 2 * kNmax;
+  static constexpr int kAccCols = kBoxes * kNmax;
   static constexpr int kAccBufs = 512 / kAccCols;
+  static_assert(kAccBufs == 1 || kAccBufs == 2, "barriers for two accumulator sets");
   static constexpr int kMisc = 10240;  // barriers, flags, counts and tile prefix over the experts (E <= 1024)
   static constexpr int kSmem = 1024 + kStages * kStage + kMisc;
   static_assert(kNmax == 128 || kNmax == 256, "token-tile widths");
@@ -66,11 +69,12 @@ struct PCfg {
 // Up gathers its token rows from the codes of x by token id (tile::gather4); down and dense read consecutive rows.  With
 // the copies spread over three producer warps the gather costs no more than a copy of the codes in plan order made
 // before (prefill, 256-row tiles: 1434 us against 1454 with that pass; batch, 128-row tiles: 1099 against 1176).
-template <int kMode, int kNmax, int kStages>
+template <int kMode, int kNmax, int kStages, int kBoxes>
 __global__ void __launch_bounds__(kThreads, 1)
     int8_pair_kernel(const __grid_constant__ CUtensorMap tm_a0, const __grid_constant__ CUtensorMap tm_a1,
                      const __grid_constant__ CUtensorMap tm_b, const Int8GemmArgs args) {
-  using C = PCfg<kNmax, kStages>;
+  using C = PCfg<kNmax, kStages, kBoxes>;
+  static_assert(kBoxes == 2 || (kBoxes == 1 && kMode == kDense), "weight boxes per CTA");
   constexpr bool kGather = kMode == kUp;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -90,7 +94,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int pair = static_cast<int>(blockIdx.x) >> 1;
   const int npairs = static_cast<int>(gridDim.x) >> 1;
   const int E = args.E;
-  constexpr int kBlock = kMode == kUp ? 2 * kBM : 4 * kBM;  // channels of a weight block
+  constexpr int kBlock = kMode == kUp ? 2 * kBM : 2 * kBoxes * kBM;  // channels of a weight block
   const int W = (args.rows_per_expert + kBlock - 1) / kBlock;
   const int tw = kMode == kDense ? args.tile_n : kNmax;     // tokens per tile
   const int dense_tiles = (args.M + tw - 1) / tw;
@@ -173,7 +177,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (leader && lane == 0)
           mbar_arrive_expect_tx(&full[k], 2u * (C::kABytes + (kGather ? half : nbox * kBRows) * kBK));
         __syncwarp();
-        if (lane < 2)
+        if (lane < kBoxes)
           tma_load_2d_pair(kMode == kUp && lane == 1 ? &tm_a1 : &tm_a0, cluster_addr(&full[k], 0),
                            ring + k * C::kStage + lane * kBoxBytes, k * kBK, lane == 0 ? row_a0 : row_a1, pol);
       }
@@ -220,7 +224,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         uint8_t* st = ring + s * C::kStage;
         const uint32_t bar = cluster_addr(&full[s], 0);
-        if (boxes && lane < 2)
+        if (boxes && lane < kBoxes)
           tma_load_2d_pair(kMode == kUp && lane == 1 ? &tm_a1 : &tm_a0, bar, st + lane * kBoxBytes, k * kBK,
                            lane == 0 ? row_a0 : row_a1, pol);
         if (kGather) {
@@ -270,7 +274,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int kk = 0; kk < kBK / 32; ++kk) {
             const uint32_t acc = (k | kk) != 0 ? 1u : 0u;
             umma_s8_pair(d0, da0 + 2 * kk, db + 2 * kk, idesc, acc);
-            umma_s8_pair(d1, da1 + 2 * kk, db + 2 * kk, idesc, acc);
+            if (kBoxes == 2) umma_s8_pair(d1, da1 + 2 * kk, db + 2 * kk, idesc, acc);
           }
           umma_commit_pair(&empty[s]);
         }
@@ -296,10 +300,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int colbase = c.w * kBlock + static_cast<int>(rank) * kBM + q * 32;  // this warp's first channel
       // what the scaling needs, loaded while the tile is still being computed: the lane's channel scales, and in
       // lane i < 16 the scale and output row of the chunk's token i
-      const int ch0 = colbase + lane, ch1 = kMode == kUp ? ch0 : ch0 + 2 * kBM;
+      const int ch0 = colbase + lane, ch1 = kMode == kUp ? ch0 : ch0 + 2 * kBM;  // one box: there is no ch1
       const size_t ch_at = static_cast<size_t>(c.e) * args.rows_per_expert;
       const float s0 = ch0 < args.rows_per_expert ? args.ch_scale0[ch_at + ch0] : 0.0f;
-      const float s1 = ch1 < args.rows_per_expert ? (kMode == kUp ? args.ch_scale1 : args.ch_scale0)[ch_at + ch1] : 0.0f;
+      const float s1 = kBoxes == 2 && ch1 < args.rows_per_expert ? (kMode == kUp ? args.ch_scale1 : args.ch_scale0)[ch_at + ch1] : 0.0f;
       float tok_s[kChunks];
       int tok_row[kChunks];
 #pragma unroll
@@ -340,7 +344,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int cb = 16 * part_c + 64 * i;
           if (cb >= c.N) break;
 #pragma unroll
-          for (int half = 0; half < 2; ++half) {
+          for (int half = 0; half < kBoxes; ++half) {
             uint32_t v[16];
             tmem_load_16(lane_base + half * kNmax + cb, v);
             tmem_load_wait();
@@ -366,7 +370,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       // 1. drain: lane l holds channel ch0 (ch1) for the tokens of its chunks; scaled and packed as bf16 token
       //    pairs, then the accumulator is released at once, so the next tile's MMAs run while this one is stored
-      constexpr int kWords = kMode == kUp ? 8 : 16;
+      constexpr int kOuts = kMode == kUp ? 1 : kBoxes;  // output halves
+      constexpr int kWords = 8 * kOuts;
       uint32_t pk[kChunks][kWords];
 #pragma unroll
       for (int i = 0; i < kChunks; ++i) {
@@ -374,7 +379,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (cb >= c.N) break;
         uint32_t v0[16], v1[16];
         tmem_load_16(lane_base + cb, v0);
-        tmem_load_16(lane_base + kNmax + cb, v1);
+        if (kBoxes == 2) tmem_load_16(lane_base + kNmax + cb, v1);
         tmem_load_wait();
 #pragma unroll
         for (int p = 0; p < 8; ++p) {
@@ -383,13 +388,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int u = 0; u < 2; ++u) {
             const float sx = __shfl_sync(0xffffffffu, tok_s[i], 2 * p + u);
             a[u] = (sx * s0) * static_cast<float>(static_cast<int>(v0[2 * p + u]));
-            b[u] = (sx * s1) * static_cast<float>(static_cast<int>(v1[2 * p + u]));
+            b[u] = kBoxes == 2 ? (sx * s1) * static_cast<float>(static_cast<int>(v1[2 * p + u])) : 0.0f;
           }
           if (kMode == kUp) {
             pk[i][p] = pack_bf16x2(silu_mul(a[0], b[0]), silu_mul(a[1], b[1]));
           } else {
             pk[i][p] = pack_bf16x2(a[0], a[1]);
-            pk[i][kWords - 8 + p] = pack_bf16x2(b[0], b[1]);
+            if (kBoxes == 2) pk[i][kWords - 8 + p] = pack_bf16x2(b[0], b[1]);
           }
         }
       }
@@ -406,7 +411,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int d0 = __shfl_sync(0xffffffffu, tok_row[i], 2 * b8);
         const int d1 = __shfl_sync(0xffffffffu, tok_row[i], 2 * b8 + 1);
 #pragma unroll
-        for (int half = 0; half < (kMode == kUp ? 1 : 2); ++half) {
+        for (int half = 0; half < kOuts; ++half) {
           uint32_t w[8];
 #pragma unroll
           for (int p = 0; p < 8; ++p) w[p] = pk[i][8 * half + p];
@@ -430,11 +435,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == kMmaWarp) tmem_dealloc_pair(tmem, 512);
 }
 
-template <int kMode, int kNmax, int kStages>
+template <int kMode, int kNmax, int kStages, int kBoxes = 2>
 cudaError_t launch_pairs(const CUtensorMap& a0, const CUtensorMap& a1, const CUtensorMap& b, const Int8GemmArgs& args,
                          int num_sms, cudaStream_t stream) {
-  using C = PCfg<kNmax, kStages>;
-  auto kern = int8_pair_kernel<kMode, kNmax, kStages>;
+  using C = PCfg<kNmax, kStages, kBoxes>;
+  auto kern = int8_pair_kernel<kMode, kNmax, kStages, kBoxes>;
   int dev = 0;
   cudaError_t st = cudaGetDevice(&dev);
   if (st != cudaSuccess) return st;
@@ -478,6 +483,7 @@ cudaError_t launch_int8_pair_down(const CUtensorMap& w_down, const CUtensorMap& 
 cudaError_t launch_int8_pair_dense(const CUtensorMap& w, const CUtensorMap& x_rows, const Int8GemmArgs& args,
                                    int num_sms, cudaStream_t stream) {
   if (args.tile_n < 32 || args.tile_n > 256 || args.tile_n % 32 != 0) return cudaErrorInvalidValue;
+  if (args.tile_boxes == 1) return launch_pairs<kDense, 256, 6, 1>(w, w, x_rows, args, num_sms, stream);
   return launch_pairs<kDense, 256, 4>(w, w, x_rows, args, num_sms, stream);
 }
 

@@ -254,6 +254,7 @@ struct Int8GemmArgs {
   int out_plain;              // dense: element stores (fp32, or rows that take no 16-byte stores)
   int split;                  // int8_gemm.cu sets it: CTAs that share a tile's K
   int tile_n;                 // dense on pairs: tokens per tile, a multiple of 32 up to 256
+  int tile_boxes;             // dense on pairs: boxes of 128 channels per CTA, 1 or 2
   int32_t* err;
   int M, E, top_k;
   int rows_per_expert;        // up: I; down: H; dense: N

@@ -529,3 +529,12 @@ def test_layer_captured_and_replayed():
         graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("tile", ["32x1", "64x1", "128x1", "224x1", "256x1"])
+@pytest.mark.parametrize("M,N,K", [(20, 7, 40), (70, 1000, 300), (600, 2600, 128), (333, 513, 1777), (2600, 5400, 200)])
+def test_linear_tiles_of_256_channels(M, N, K, tile, monkeypatch):
+    """One box of 128 channels per CTA: two accumulator sets, which tiles take in turn."""
+    monkeypatch.setenv("MOE_INT8_TILE", tile)
+    for out in (torch.bfloat16, torch.float32):
+        linear_case(M, N, K, out, seed=M + 1)
