@@ -594,9 +594,17 @@ moe::Int8GemmArgs int8_plan_args(const moe_plan_t* plan, const moe_shape_t& s, i
   return a;
 }
 
-// Token-tile width of the int8 projections on 2-SM pairs, or 0 for the one-tile-per-CTA kernels (decode shapes).
-// MOE_GEMM_PAIR overrides as for bf16.
-int int8_pair_nmax(const moe_shape_t& s) { return want_persistent(s) ? pair_nmax(s) : 0; }
+// Token-tile width of the int8 projections on 2-SM pairs, or 0 for the kernels of single CTAs (decode shapes).  Pairs
+// from 16 tokens per expert: at 20 they cost 2 percent where tokens are spread evenly (up, 32 experts of 7168 x 2048:
+// 157 us against 154) and gain 10 to 20 where they are not (up 159 against 177, down 87 against 98; down of 64 experts
+// of 2048 x 1024 33 against 41), since an expert of more than 32 tokens has its weights read twice by single CTAs; at
+// 12 they lose (up 58 against 51).  MOE_GEMM_PAIR, MOE_GEMM_PERSISTENT and MOE_GEMM_NMAX override as for bf16 (single
+// CTAs take tiles of 32 tokens in any case: of 128 they are slower than pairs at every size).
+int int8_pair_nmax(const moe_shape_t& s) {
+  const bool forced = std::getenv("MOE_GEMM_PERSISTENT") != nullptr || std::getenv("MOE_GEMM_NMAX") != nullptr;
+  const bool pairs = forced ? want_persistent(s) : static_cast<long long>(s.M) * s.top_k >= 16ll * s.E;
+  return pairs ? pair_nmax(s) : 0;
+}
 
 // int8 up: x -> codes and scale of every token -> GEMM with the rows gathered by token.
 moe_status_t run_up_int8(const moe_bf16_t* x, const moe_weights_t* w, const moe_plan_t* plan, const moe_shape_t& s,
@@ -627,7 +635,7 @@ moe_status_t run_up_int8(const moe_bf16_t* x, const moe_weights_t* w, const moe_
   a.rows_per_expert = s.I;
   a.kdim = s.H;
   if (pairs != 0) return cuda_status(moe::launch_int8_pair_up(mg, mu, mx, a, pairs, num_sms(), stream));
-  return cuda_status(moe::launch_int8_up(mg, mu, mx, a, choose_nmax(s), num_sms(), stream));
+  return cuda_status(moe::launch_int8_up(mg, mu, mx, a, num_sms(), stream));
 }
 
 // int8 down: the real plan rows of h -> codes and scales -> GEMM scattered to slots.
@@ -661,7 +669,7 @@ moe_status_t run_down_int8(const moe_bf16_t* h, const moe_weights_t* w, const mo
   a.rows_per_expert = s.H;
   a.kdim = s.I;
   if (pairs != 0) return cuda_status(moe::launch_int8_pair_down(md, mh, a, pairs, num_sms(), stream));
-  return cuda_status(moe::launch_int8_down(md, mh, a, choose_nmax(s), num_sms(), stream));
+  return cuda_status(moe::launch_int8_down(md, mh, a, num_sms(), stream));
 }
 
 // moe_linear_int8's arguments that its workspace size depends on.

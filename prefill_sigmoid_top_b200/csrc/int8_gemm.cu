@@ -468,15 +468,13 @@ int int8_tile_split(long long tiles, int nk, int num_sms) {
 }
 
 cudaError_t launch_int8_up(const CUtensorMap& w_gate, const CUtensorMap& w_up, const CUtensorMap& x_rows,
-                           const Int8GemmArgs& args, int nmax, int num_sms, cudaStream_t stream) {
-  if (nmax <= 32) return launch_form<kUp, 32, 5, 2, 2>(w_gate, w_up, x_rows, args, num_sms, stream);
-  return launch_form<kUp, 128, 4, 4, 1>(w_gate, w_up, x_rows, args, num_sms, stream);
+                           const Int8GemmArgs& args, int num_sms, cudaStream_t stream) {
+  return launch_form<kUp, 32, 5, 2, 2>(w_gate, w_up, x_rows, args, num_sms, stream);
 }
 
-cudaError_t launch_int8_down(const CUtensorMap& w_down, const CUtensorMap& h_rows, const Int8GemmArgs& args, int nmax,
+cudaError_t launch_int8_down(const CUtensorMap& w_down, const CUtensorMap& h_rows, const Int8GemmArgs& args,
                              int num_sms, cudaStream_t stream) {
-  if (nmax <= 32) return launch_form<kDown, 32, 10, 4, 2>(w_down, w_down, h_rows, args, num_sms, stream);
-  return launch_form<kDown, 128, 6, 3, 2>(w_down, w_down, h_rows, args, num_sms, stream);
+  return launch_form<kDown, 32, 10, 4, 2>(w_down, w_down, h_rows, args, num_sms, stream);
 }
 
 cudaError_t launch_int8_dense(const CUtensorMap& w, const CUtensorMap& x_rows, const Int8GemmArgs& args, int nmax,

@@ -263,8 +263,8 @@ struct Int8GemmArgs {
 // Tensor maps: weights in 128-row boxes of 128 bytes; up: x codes [M, H] in one-row boxes (gathered by token);
 // down / dense: h codes [cap, I] / x codes [M, K] in 16-row boxes.
 cudaError_t launch_int8_up(const CUtensorMap& w_gate, const CUtensorMap& w_up, const CUtensorMap& x_rows,
-                           const Int8GemmArgs& args, int nmax, int num_sms, cudaStream_t stream);
-cudaError_t launch_int8_down(const CUtensorMap& w_down, const CUtensorMap& h_rows, const Int8GemmArgs& args, int nmax,
+                           const Int8GemmArgs& args, int num_sms, cudaStream_t stream);
+cudaError_t launch_int8_down(const CUtensorMap& w_down, const CUtensorMap& h_rows, const Int8GemmArgs& args,
                              int num_sms, cudaStream_t stream);
 cudaError_t launch_int8_dense(const CUtensorMap& w, const CUtensorMap& x_rows, const Int8GemmArgs& args, int nmax,
                               int num_sms, cudaStream_t stream);
