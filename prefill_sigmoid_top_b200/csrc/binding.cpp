@@ -158,6 +158,15 @@ PyObject* route_logits(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// The error word (nullable).
+int32_t* read_err_flag(Args& in) {
+  const Tensor* t = in.tensor_or_none();
+  if (t == nullptr) return nullptr;
+  want(*t, at::kInt, t->sizes(), "err_flag");
+  if (t->numel() < 1) refuse("err_flag: expected at least one int32");
+  return static_cast<int32_t*>(t->data_ptr());
+}
+
 // x, codes, scales, out, out_dtype, ws, err_flag
 PyObject* linear_int8(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded([&]() -> PyObject* {
@@ -183,8 +192,7 @@ PyObject* linear_int8(PyObject*, PyObject* const* a, Py_ssize_t n) {
     }
     if (type != at::kFloat && type != at::kBFloat16) refuse("out: expected bf16 or fp32");
     const Tensor* ws_in = in.tensor_or_none();
-    const Tensor* err = in.tensor_or_none();
-    if (err) want(*err, at::kInt, err->sizes(), "err_flag");
+    int32_t* err = read_err_flag(in);
     if (ws_in && !ws_in->is_contiguous()) refuse("ws: expected a contiguous tensor");
     const c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(in.device));
     const Tensor out = out_in ? *out_in : at::empty({M, N}, x.options().dtype(type));
@@ -201,18 +209,31 @@ PyObject* linear_int8(PyObject*, PyObject* const* a, Py_ssize_t n) {
         static_cast<const moe_bf16_t*>(x.data_ptr()), ldx, static_cast<const int8_t*>(codes.data_ptr()), ldw,
         static_cast<const float*>(scales.data_ptr()), M, N, K, out.data_ptr(), ldo,
         type == at::kFloat ? MOE_DT_F32 : MOE_DT_BF16, ws.defined() ? ws.data_ptr() : nullptr, ws_bytes,
-        static_cast<int32_t*>(address(err)), c10::cuda::getCurrentCUDAStream(in.device).stream());
+        err, c10::cuda::getCurrentCUDAStream(in.device).stream());
     return st != MOE_OK ? PyLong_FromLong(st) : wrap(out);
   });
 }
 
-// sorted_ids, block_expert, expert_counts, expert_offsets, num_tokens_post_padded
-moe_plan_t read_plan(Args& in) {
+// The plan's arrays, each with as many entries as moe_align_block_size writes for this shape (more are fine, as buffers
+// kept for a larger one have).  A shape that the library refuses has no capacity, and its call launches nothing.
+moe_plan_t read_plan(Args& in, const moe_shape_t& s, int64_t cap) {
+  const int64_t blocks = cap > 0 ? cap / s.block_size : 0;
+  const struct {
+    const char* name;
+    int64_t entries;
+  } arrays[5] = {{"sorted_ids", cap},
+                 {"block_expert", blocks},
+                 {"expert_counts", s.E},
+                 {"expert_offsets", int64_t{s.E} + 1},
+                 {"num_tokens_post_padded", 1}};
   const int32_t* p[5];
-  for (auto& q : p) {
+  for (int i = 0; i < 5; ++i) {
     const Tensor& t = in.tensor("plan");
     want(t, at::kInt, t.sizes(), "plan");
-    q = static_cast<const int32_t*>(t.data_ptr());
+    if (t.numel() < arrays[i].entries)
+      refuse(std::string("plan: ") + arrays[i].name + " has " + std::to_string(t.numel()) + " entries, the shape needs " +
+             std::to_string(arrays[i].entries));
+    p[i] = static_cast<const int32_t*>(t.data_ptr());
   }
   return {p[0], p[1], p[2], p[3], p[4]};
 }
@@ -252,20 +273,19 @@ PyObject* grouped_up_swiglu_int8(PyObject*, PyObject* const* a, Py_ssize_t n) {
     w.dtype = MOE_W_INT8;
     read_matrix(in, "gate", s.E, s.I, s.H, &w.gate, &w.gate_gs);
     read_matrix(in, "up", s.E, s.I, s.H, &w.up, &w.up_gs);
-    const moe_plan_t plan = read_plan(in);
-    const Tensor* h_in = in.tensor_or_none();
-    const Tensor* err = in.tensor_or_none();
-    const Tensor* ws_in = in.tensor_or_none();
     const int64_t cap = static_cast<int64_t>(moe_align_capacity(s));
+    const moe_plan_t plan = read_plan(in, s, cap);
+    const Tensor* h_in = in.tensor_or_none();
+    int32_t* err = read_err_flag(in);
+    const Tensor* ws_in = in.tensor_or_none();
     if (h_in && (h_in->scalar_type() != at::kBFloat16 || !h_in->is_contiguous() || h_in->numel() < cap * s.I))
       refuse("h: expected align_capacity(shape) contiguous bf16 rows of I");
-    if (err) want(*err, at::kInt, err->sizes(), "err_flag");
     const c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(in.device));
     const Tensor h = h_in ? *h_in : at::empty({cap, s.I < 0 ? 0 : s.I}, x.options());
     const Tensor ws = workspace(ws_in, x, moe_up_workspace_size(s, MOE_W_INT8));
     const moe_status_t st = moe_grouped_up_swiglu(
         static_cast<const moe_bf16_t*>(x.data_ptr()), &w, &plan, s, static_cast<moe_bf16_t*>(h.data_ptr()),
-        ws.data_ptr(), static_cast<size_t>(ws.nbytes()), static_cast<int32_t*>(address(err)),
+        ws.data_ptr(), static_cast<size_t>(ws.nbytes()), err,
         c10::cuda::getCurrentCUDAStream(in.device).stream());
     return st != MOE_OK ? PyLong_FromLong(st) : wrap(h);
   });
@@ -283,20 +303,19 @@ PyObject* grouped_down_int8(PyObject*, PyObject* const* a, Py_ssize_t n) {
     moe_weights_t w{};
     w.dtype = MOE_W_INT8;
     read_matrix(in, "down", s.E, s.H, s.I, &w.down, &w.down_gs);
-    const moe_plan_t plan = read_plan(in);
+    const moe_plan_t plan = read_plan(in, s, cap);
     const Tensor* y_in = in.tensor_or_none();
-    const Tensor* err = in.tensor_or_none();
+    int32_t* err = read_err_flag(in);
     const Tensor* ws_in = in.tensor_or_none();
     const int64_t slots = static_cast<int64_t>(s.M) * s.top_k;
     if (y_in && (y_in->scalar_type() != at::kBFloat16 || !y_in->is_contiguous() || y_in->numel() != slots * s.H))
       refuse("y: expected M * top_k contiguous bf16 rows of H");
-    if (err) want(*err, at::kInt, err->sizes(), "err_flag");
     const c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(in.device));
     const Tensor y = y_in ? *y_in : at::empty({slots < 0 ? 0 : slots, s.H < 0 ? 0 : s.H}, h.options());
     const Tensor ws = workspace(ws_in, h, moe_down_workspace_size(s, MOE_W_INT8));
     const moe_status_t st = moe_grouped_down(
         static_cast<const moe_bf16_t*>(h.data_ptr()), &w, &plan, s, static_cast<moe_bf16_t*>(y.data_ptr()),
-        ws.data_ptr(), static_cast<size_t>(ws.nbytes()), static_cast<int32_t*>(address(err)),
+        ws.data_ptr(), static_cast<size_t>(ws.nbytes()), err,
         c10::cuda::getCurrentCUDAStream(in.device).stream());
     return st != MOE_OK ? PyLong_FromLong(st) : wrap(y);
   });

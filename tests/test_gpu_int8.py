@@ -538,3 +538,41 @@ def test_linear_tiles_of_256_channels(M, N, K, tile, monkeypatch):
     monkeypatch.setenv("MOE_INT8_TILE", tile)
     for out in (torch.bfloat16, torch.float32):
         linear_case(M, N, K, out, seed=M + 1)
+
+
+PLAN = ("sorted_ids", "block_expert", "expert_counts", "expert_offsets", "num_tokens_post_padded")
+
+
+@pytest.mark.parametrize("M,E,B", [(4, 2, 16), (60, 3, 64)])
+def test_plans_of_another_shape_are_refused(M, E, B):
+    """A plan array with fewer entries than the shape's plan has (one missing, none, that of fewer tokens, experts or a
+    smaller block), and an error word without room, are refused before anything is launched."""
+    shape = moe.Shape(M, 256, 128, E, 1, B)
+    x, ids, plan, mats, iw = experts_case(shape, seed=41)
+    xd = x.to(DEV)
+    h = torch.zeros(moe.align_capacity(shape), 128, dtype=torch.bfloat16, device=DEV)
+    need = dict(sorted_ids=moe.align_capacity(shape), block_expert=moe.align_capacity(shape) // B, expert_counts=E,
+                expert_offsets=E + 1, num_tokens_post_padded=1)
+    plans = [dict(plan, **{n: plan[n][:k]}) for n in PLAN for k in {0, need[n] - 1}]
+    plans.append(moe.align_block_size(ids[:-1].to(DEV), E, B))
+    plans.append(moe.align_block_size(torch.zeros_like(ids).to(DEV), E - 1, B))
+    if B > 16:
+        plans.append(moe.align_block_size(ids.to(DEV), E, B // 2))
+    for p in plans:
+        with pytest.raises(ValueError):
+            moe.grouped_up_swiglu_int8(xd, iw, p, shape)
+        with pytest.raises(ValueError):
+            moe.grouped_down_int8(h, iw, p, shape)
+    none = torch.zeros(0, dtype=torch.int32, device=DEV)
+    codes, scales = (t.to(DEV) for t in codes_of(8, 256, 1))
+    for call in (lambda: moe.grouped_up_swiglu_int8(xd, iw, plan, shape, err_flag=none),
+                 lambda: moe.grouped_down_int8(h, iw, plan, shape, err_flag=none),
+                 lambda: moe.linear_int8(xd, codes, scales, err_flag=none)):
+        with pytest.raises(ValueError):
+            call()
+    # exactly as many entries as the shape needs, and more, are taken
+    want = moe.grouped_down_int8(h, iw, plan, shape)
+    exact = {n: plan[n][:need[n]] for n in PLAN}
+    more = {n: torch.cat([plan[n], plan[n].new_zeros(5)]) for n in PLAN}
+    for p in (exact, more):
+        assert torch.equal(moe.grouped_down_int8(h, iw, p, shape), want)
