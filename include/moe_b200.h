@@ -237,7 +237,11 @@ MOE_API size_t moe_align_capacity(moe_shape_t s); /* M*top_k + E*(block_size-1) 
  * single SMs otherwise or with MOE_NVFP4_PAIR=0 in the environment, with the
  * same bits either way.  MOE_W_INT8: every token's x is quantised on the fly
  * (moe_quantize_int8's codes and scale) into ws (required); g and u are the
- * exact integer products times the token's and the channel's scale. */
+ * exact integer products times the token's and the channel's scale.  With
+ * MOE_W_INT8 (here and in moe_grouped_down) a plan of another shape moves no
+ * read or store out of the buffers of this one: counts outside [0, M*K], rows
+ * outside [0, moe_align_capacity(s)) and slots outside [0, M*K) set
+ * MOE_ERR_INVALID_INPUT in err_flag and are left out. */
 MOE_API moe_status_t moe_grouped_up_swiglu(const moe_bf16_t* x, const moe_weights_t* w, const moe_plan_t* plan,
                                    moe_shape_t s, moe_bf16_t* h, void* ws, size_t ws_bytes, int32_t* err_flag,
                                    moe_stream_t stream);

@@ -591,6 +591,7 @@ moe::Int8GemmArgs int8_plan_args(const moe_plan_t* plan, const moe_shape_t& s, i
   a.M = s.M;
   a.E = s.E;
   a.top_k = s.top_k;
+  a.cap = static_cast<int>(cap_rows(s));
   return a;
 }
 

@@ -26,6 +26,7 @@
 #include <algorithm>
 
 #include "common.cuh"
+#include "int8_plan.cuh"
 #include "kernels.h"
 #include "pair_ptx.cuh"
 #include "tile_list.cuh"
@@ -105,7 +106,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   // the counts' loads are under way while barriers and tensor memory are set up
   if (kMode != kDense && warp != kMmaWarp)
-    for (int e = tid; e < args.E; e += 32 * kMmaWarp) cnt[e] = args.counts[e];
+    for (int e = tid; e < args.E; e += 32 * kMmaWarp) cnt[e] = plan_count(args, e);
   if (warp == kMmaWarp) {
     tmem_alloc(tmem_slot, C::kTmemCols);
     tmem_relinquish();
@@ -138,7 +139,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   const int nk_all = (args.kdim + kBK - 1) / kBK;
   const int k_lo = nk_all * rank / split, k_hi = nk_all * (rank + 1) / split;  // split <= nk_all
-  const int nslots = args.M * args.top_k;
 
   struct Tile {
     int e, w, row0, nrows, N, count;
@@ -172,8 +172,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       scale = args.row_scale[r];
       row = r;
     } else {
-      const int id = args.sorted_ids[r];
-      if (id >= 0 && id < nslots) {
+      const int id = plan_slot(args, r);
+      if (id >= 0) {
         scale = args.row_scale[kMode == kUp ? id / args.top_k : r];
         row = kMode == kUp ? r : id;
       } else {
@@ -228,8 +228,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int u = 0; u < 4; ++u)
           if (4 * lane + u < c.nrows) {
-            const int id = args.sorted_ids[c.row0 + 4 * lane + u];
-            tok[u] = (id >= 0 && id < nslots) ? id / args.top_k : 0;
+            const int id = plan_slot(args, c.row0 + 4 * lane + u);
+            tok[u] = id >= 0 ? id / args.top_k : 0;
           }
       }
       for (int i = (warp - it0) & (kProducers - 1); i < nk; i += kProducers) {

@@ -28,6 +28,7 @@
 // before the wait for it.  Every mbarrier wait is bounded; a timeout sets the error word and unwinds, and both CTAs
 // still meet at the last cluster barrier.
 #include "common.cuh"
+#include "int8_plan.cuh"
 #include "kernels.h"
 #include "pair_ptx.cuh"
 #include "tile_list.cuh"
@@ -100,7 +101,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int dense_tiles = (args.M + tw - 1) / tw;
 
   if (kMode != kDense)
-    for (int e = tid; e < E; e += kThreads) cnt[e] = args.counts[e];
+    for (int e = tid; e < E; e += kThreads) cnt[e] = plan_count(args, e);
   if (tid == 0) *abort_flag = 0;
   __syncthreads();
   if (kMode != kDense && warp == 0) build_tile_prefix<kNmax>(cnt, prefix, E, W, lane);
@@ -130,7 +131,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after_sync();
   const uint32_t tmem = *tmem_slot;
   const int nk = (args.kdim + kBK - 1) / kBK;
-  const int nslots = args.M * args.top_k;
 
   struct Tile {
     int e, w, row0, nrows, N, count;
@@ -199,8 +199,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int u = 0; u < 4; ++u) {
           const int r = 4 * lane + u;
           if (r < half && static_cast<int>(rank) * half + r < c.nrows) {
-            const int id = args.sorted_ids[row0 + r];
-            tok[u] = (id >= 0 && id < nslots) ? id / args.top_k : 0;
+            const int id = plan_slot(args, row0 + r);
+            tok[u] = id >= 0 ? id / args.top_k : 0;
           }
         }
       }
@@ -317,8 +317,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             tok_s[i] = args.row_scale[row];
             tok_row[i] = row;
           } else {
-            const int id = args.sorted_ids[row];
-            if (id >= 0 && id < nslots) {
+            const int id = plan_slot(args, row);
+            if (id >= 0) {
               tok_s[i] = args.row_scale[kMode == kUp ? id / args.top_k : row];
               tok_row[i] = kMode == kUp ? row : id;
             } else {

@@ -257,6 +257,7 @@ struct Int8GemmArgs {
   int tile_boxes;             // dense on pairs: boxes of 128 channels per CTA, 1 or 2
   int32_t* err;
   int M, E, top_k;
+  int cap;                    // rows of the plan (moe_align_capacity); what a plan holds beyond it is not touched
   int rows_per_expert;        // up: I; down: H; dense: N
   int kdim;
 };

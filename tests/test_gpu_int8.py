@@ -576,3 +576,48 @@ def test_plans_of_another_shape_are_refused(M, E, B):
     more = {n: torch.cat([plan[n], plan[n].new_zeros(5)]) for n in PLAN}
     for p in (exact, more):
         assert torch.equal(moe.grouped_down_int8(h, iw, p, shape), want)
+
+
+def set_widths(monkeypatch, nmax, pair):
+    """The kernel for the expert projections: single CTAs (pair "0"), or pairs with tiles of this many tokens."""
+    monkeypatch.setenv("MOE_GEMM_NMAX", nmax)
+    monkeypatch.setenv("MOE_GEMM_PAIR", pair)
+
+
+@pytest.mark.parametrize("nmax,pair", [("32", "0"), ("128", "128"), ("128", "256")])
+def test_plans_that_reach_beyond_the_buffers(nmax, pair, monkeypatch):
+    """Plans with enough entries whose contents belong to another shape (more tokens, a wider block, counts and offsets
+    that are no such): rows behind the shape's capacity keep what they held, the error word says INVALID_INPUT, rows of
+    experts that are in order keep their values."""
+    set_widths(monkeypatch, nmax, pair)
+    shape = moe.Shape(4, 256, 128, 2, 1, 16)
+    cap = moe.align_capacity(shape)
+    x, ids, plan, mats, iw = experts_case(shape, seed=42, ids=torch.tensor([[1], [1], [1], [0]], dtype=torch.int32))
+    xd = x.to(DEV)
+    good = moe.grouped_up_swiglu_int8(xd, iw, plan, shape, h=torch.zeros(cap, 128, dtype=torch.bfloat16, device=DEV))
+    hin = torch.randn(cap, 128, generator=gen(43)).to(torch.bfloat16).to(DEV)
+
+    def run(p, first_expert_intact):
+        err = torch.zeros(1, dtype=torch.int32, device=DEV)
+        h = torch.full((cap + 300, 128), -3.0, dtype=torch.bfloat16, device=DEV)
+        moe.grouped_up_swiglu_int8(xd, iw, p, shape, h=h, err_flag=err)
+        assert moe.get_device_error(err) == 4
+        assert (h[cap:] == -3.0).all()
+        if first_expert_intact:
+            assert torch.equal(h[0], good[0])
+        err.zero_()
+        y = moe.grouped_down_int8(hin, iw, p, shape, err_flag=err)
+        assert moe.get_device_error(err) == 4 and tuple(y.shape) == (4, 256)
+
+    more = torch.zeros(40, 1, dtype=torch.int32)
+    more[:20] = 1
+    run(moe.align_block_size(more.to(DEV), 2, 16), False)  # tokens 0 to 3 at rows 32 to 35 of 34
+    wide = torch.tensor([[0], [1], [1], [1]], dtype=torch.int32)
+    run(moe.align_block_size(wide.to(DEV), 2, 64), False)  # expert 1 from row 64 on
+    for name, values in (("expert_counts", (-1, -2 ** 31, 5, 10 ** 6, 2 ** 31 - 1)),
+                         ("expert_offsets", (-1, -40, cap, 2 ** 31 - 1, -2 ** 31))):
+        for v in values:
+            bad = plan[name].clone()
+            bad[1] = v
+            # the first expert's row 0 keeps its value unless it is one of the second's rows v .. v + 2 too
+            run(dict(plan, **{name: bad}), not (name == "expert_offsets" and -3 < v <= 0))
