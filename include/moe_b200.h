@@ -369,8 +369,10 @@ MOE_API size_t moe_nvfp4_blob_bytes(moe_shape_t s, int which);
  * Rows of bf16 as symmetric 8-bit codes with one fp32 scale per row:
  *   a = max |v| of the row;  scale = a / 127;  code = rint(127 v / a), ties to
  *   even (a = 0: scale 0, codes 0)
- * the codes are those of exact arithmetic.  A row that holds an infinity or a
- * NaN gets codes 0 and the scale NaN: every product with it is NaN.
+ * the codes are those of exact arithmetic.  The scale is a / 127 rounded to fp32:
+ * of a row below 127 * 2^-126 a subnormal, with as few bits as it has there.  A
+ * row that holds an infinity or a NaN gets codes 0 and the scale NaN: every
+ * product with it is NaN.
  * src: bf16, row r at src + r * ld elements; codes: int8, row r at codes +
  * r * pitch (bytes from cols to the pitch are left as they were); scales: fp32
  * [rows].  Any alignment.  rows, cols >= 1, ld >= cols, pitch >= cols; rows < 2^31,
@@ -383,7 +385,9 @@ MOE_API moe_status_t moe_quantize_int8(const moe_bf16_t* src, int64_t ld, int64_
  * as a shared expert's):
  *   out[m,n] = sx[m] * w_scale[n] * sum_k xq[m,k] * w[n,k]
  * with xq, sx of x as moe_quantize_int8 (on the fly into ws), the sum exact in
- * int32, the scaling in fp32, rounded to out_dtype (bf16 or fp32) at the end.
+ * int32, the scaling in fp32 (sx * w_scale first; in fp64 where that product is
+ * no normal number of fp32, so that only the result's own range counts), rounded
+ * to out_dtype (bf16 or fp32) at the end.  The int8 expert projections scale alike.
  * x: bf16, row m at x + m * ldx elements (any alignment, ldx >= K); w: int8
  * [N, K] codes, row n at w + n * ldw, w 16-byte aligned, ldw >= K a multiple of
  * 16 (codes between K and ldw are not read as values); w_scale: fp32 [N]; out:

@@ -165,7 +165,7 @@ __global__ void __launch_bounds__(kThreads, 1) int8_few_kernel(const uint16_t* _
 #pragma unroll
         for (int m = 0; m < kRows; ++m) sum = lane == m ? acc[m] : sum;
       }
-      const float r = (scale[lane] * args.ch_scale0[n]) * static_cast<float>(sum);
+      const float r = int8_value(scale[lane], args.ch_scale0[n], sum);
       const size_t at = static_cast<size_t>(lane) * args.out_ld + n;
       if (args.out_f32)
         static_cast<float*>(args.out)[at] = r;

@@ -3,7 +3,7 @@
 // activation scales, and the dense product.
 //
 //   acc[n, j] = sum_k xq[n, k] wq[j, k]       exact: |codes| <= 127, so k <= 131072 terms stay below 2^31
-//   value     = (sx[n] * sw[j]) * acc          fp32 (acc rounded once to 24 bits)
+//   value     = (sx[n] * sw[j]) * acc          fp32 (acc rounded once to 24 bits; int8_value has the range's ends)
 //   up:    h[row, j]  = bf16(silu(gate) * up)      down: y[slot, j] = bf16(value)      dense: y[n, j]
 //
 // As in the bf16 kernels the weight rows are the M side of the MMA (128 per CTA) and the tokens its N side, one
@@ -27,6 +27,7 @@
 
 #include "common.cuh"
 #include "int8_plan.cuh"
+#include "int8_rows.cuh"
 #include "kernels.h"
 #include "pair_ptx.cuh"
 #include "tile_list.cuh"
@@ -182,8 +183,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   };
   auto store = [&](int row, int ch, float s0, float s1, float sx, int a0, int a1) {
-    float v = (sx * s0) * static_cast<float>(a0);
-    if (kMode == kUp) v = silu_mul(v, (sx * s1) * static_cast<float>(a1));
+    float v = int8_value(sx, s0, a0);
+    if (kMode == kUp) v = silu_mul(v, int8_value(sx, s1, a1));
     const size_t at = static_cast<size_t>(row) * args.out_ld + ch;
     if (kMode == kDense && args.out_f32)
       static_cast<float*>(args.out)[at] = v;

@@ -29,6 +29,7 @@
 // still meet at the last cluster barrier.
 #include "common.cuh"
 #include "int8_plan.cuh"
+#include "int8_rows.cuh"
 #include "kernels.h"
 #include "pair_ptx.cuh"
 #include "tile_list.cuh"
@@ -153,6 +154,25 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     t.N = (t.nrows + 31) & ~31;
     return t;
+  };
+  // Scale and output row (-1: none) of row n of a tile.
+  auto token_at = [&](const Tile& t, int n, float& scale, int& to) {
+    scale = 0.0f;
+    to = -1;
+    if (n >= t.nrows) return;
+    const int row = t.row0 + n;
+    if (kMode == kDense) {
+      scale = args.row_scale[row];
+      to = row;
+    } else {
+      const int id = plan_slot(args, row);
+      if (id >= 0) {
+        scale = args.row_scale[kMode == kUp ? id / args.top_k : row];
+        to = kMode == kUp ? row : id;
+      } else {
+        set_error(args.err, kErrInvalidInput);
+      }
+    }
   };
 
   if (warp < kProducers) {
@@ -307,26 +327,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       float tok_s[kChunks];
       int tok_row[kChunks];
 #pragma unroll
-      for (int i = 0; i < kChunks; ++i) {
-        const int n = 16 * part_c + 64 * i + (lane & 15);
-        tok_s[i] = 0.0f;
-        tok_row[i] = -1;
-        if (n < c.nrows) {
-          const int row = c.row0 + n;
-          if (kMode == kDense) {
-            tok_s[i] = args.row_scale[row];
-            tok_row[i] = row;
-          } else {
-            const int id = plan_slot(args, row);
-            if (id >= 0) {
-              tok_s[i] = args.row_scale[kMode == kUp ? id / args.top_k : row];
-              tok_row[i] = kMode == kUp ? row : id;
-            } else {
-              set_error(args.err, kErrInvalidInput);
-            }
-          }
-        }
-      }
+      for (int i = 0; i < kChunks; ++i) token_at(c, 16 * part_c + 64 * i + (lane & 15), tok_s[i], tok_row[i]);
+      // no scale of the warp's is near the ends of fp32's range: then their products need no look at each
+      bool near = int8_near_scale(s0) && int8_near_scale(s1);
+#pragma unroll
+      for (int i = 0; i < kChunks; ++i) near = near && int8_near_scale(tok_s[i]);
+      near = __all_sync(0xffffffffu, near);
       bool ok = true;
       if (lane == 0) ok = mbar_wait_bounded(&acc_full[buf], (j / C::kAccBufs) & 1, abort_flag);
       ok = __shfl_sync(0xffffffffu, ok, 0);
@@ -337,6 +343,45 @@ __global__ void __launch_bounds__(kThreads, 1)
         break;
       }
       const uint32_t lane_base = tmem + (static_cast<uint32_t>(q * 32) << 16) + buf * C::kAccCols;
+      if (!near) {
+        // rare, so small rather than fast: lane = channel, element stores, the tokens looked up again
+#pragma unroll 1
+        for (int i = 0; i < kChunks; ++i) {
+          const int cb = 16 * part_c + 64 * i;
+          if (cb >= c.N) break;
+          __syncwarp();
+          uint32_t v0[16], v1[16];
+          tmem_load_16(lane_base + cb, v0);
+          if (kBoxes == 2) tmem_load_16(lane_base + kNmax + cb, v1);
+          tmem_load_wait();
+          float sc;
+          int to;
+          token_at(c, cb + (lane & 15), sc, to);
+#pragma unroll
+          for (int p = 0; p < 16; ++p) {
+            const float sx = __shfl_sync(0xffffffffu, sc, p);
+            const int row = __shfl_sync(0xffffffffu, to, p);
+            if (row < 0) continue;
+            float r0 = int8_value(sx, s0, static_cast<int>(v0[p]));
+            const float r1 = kBoxes == 2 ? int8_value(sx, s1, static_cast<int>(v1[p])) : 0.0f;
+            if (kMode == kUp) r0 = silu_mul(r0, r1);
+            const size_t at = static_cast<size_t>(row) * args.out_ld;
+            auto put = [&](int ch, float r) {
+              if (ch >= args.rows_per_expert) return;
+              if (kMode == kDense && args.out_f32)
+                static_cast<float*>(args.out)[at + ch] = r;
+              else
+                static_cast<__nv_bfloat16*>(args.out)[at + ch] = __float2bfloat16_rn(r);
+            };
+            put(ch0, r0);
+            if (kMode != kUp && kBoxes == 2) put(ch1, r1);
+          }
+        }
+        tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(cluster_addr(&acc_empty[buf], 0));
+        continue;
+      }
       if (kMode == kDense && args.out_plain) {
         // fp32 results, or rows that take no 16-byte stores: lane = channel, one store per token and half
 #pragma unroll

@@ -58,6 +58,23 @@ __device__ __forceinline__ uint32_t max_bits(uint32_t top, uint32_t pair) {
   return max(top, max(pair & 0x7fffu, (pair >> 16) & 0x7fffu));
 }
 
+// The value of an integer sum: (sx sw) sum in fp32, three roundings, as long as the scales' product is a normal number.
+// Where it is not (rows or channels near the ends of fp32's range), the result may be one all the same, or 0 where
+// infinity times 0 would be NaN: there the product is taken in fp64, whose range holds it, and rounded once.  Which of
+// the two depends on the two scales alone, so a row's results are the same bits in every kernel and batch.
+static __device__ __noinline__ float int8_value_fp64(float sx, float sw, int sum) {
+  return static_cast<float>(static_cast<double>(sx) * static_cast<double>(sw) * static_cast<double>(sum));
+}
+__device__ __forceinline__ float int8_value(float sx, float sw, int sum) {
+  const float p = sx * sw;
+  if (fabsf(p) >= 0x1p-126f && fabsf(p) < INFINITY) return p * static_cast<float>(sum);
+  return int8_value_fp64(sx, sw, sum);
+}
+// Two scales for which this holds have a normal product, or one of 0: (sx sw) sum is int8_value without its test.
+__device__ __forceinline__ bool int8_near_scale(float s) {
+  return s == 0.0f || (fabsf(s) >= 0x1p-60f && fabsf(s) <= 0x1p60f);
+}
+
 // Eight bf16 values (a 16-byte vector) as eight codes; kPlain: the row has s.c.
 template <bool kPlain>
 __device__ __forceinline__ uint2 codes_of_8(const uint4& v, const RowScale& s) {

@@ -621,3 +621,83 @@ def test_plans_that_reach_beyond_the_buffers(nmax, pair, monkeypatch):
             bad[1] = v
             # the first expert's row 0 keeps its value unless it is one of the second's rows v .. v + 2 too
             run(dict(plan, **{name: bad}), not (name == "expert_offsets" and -3 < v <= 0))
+
+
+# ------------------------------------------------------------------ scales whose product leaves fp32's normal range
+def far_rows(M, cols):
+    """Rows of one value each, so codes of 127 and scales of exactly 2^-117, 1, 2^90 and 0, in turn."""
+    x = torch.tensor([127 * 2.0 ** -117, 127.0, 127 * 2.0 ** 90, 0.0]).repeat(M // 4 + 1)[:M]
+    return x[:, None].expand(M, cols).to(torch.bfloat16).contiguous()
+
+
+def far_weights(rows, cols, seed, scale):
+    """Codes of 64 to 127, so sums of about 2^13.6 cols, and scales of `scale` times 1 to 2; every third channel has
+    sums of 0 (halves of +1 and -1) and the scale 2^60."""
+    g = gen(seed)
+    c = torch.randint(64, 128, (rows, cols), generator=g).to(torch.int8)
+    s = scale * (1.0 + torch.rand(rows, generator=g))
+    c[::3, :cols // 2], c[::3, cols // 2:], s[::3] = 1, -1, 2.0 ** 60
+    return c, s
+
+
+def far_within(got, want, rel):
+    """Relative where the exact value is a normal number of fp32; infinite above, one subnormal step of bf16 below."""
+    got, top = got.detach().cpu().double().numpy(), float(torch.finfo(torch.bfloat16).max)
+    normal = (np.abs(want) >= 2.0 ** -126) & (np.abs(want) <= top)
+    assert normal.any() and (want == 0).any()
+    assert (np.abs(got - want)[normal] <= rel * np.abs(want)[normal]).all()
+    assert (got[np.abs(want) > 1.01 * top] == np.inf).all()
+    assert (np.abs(got - want)[np.abs(want) < 2.0 ** -126] <= 2.0 ** -133).all()
+
+
+@pytest.mark.parametrize("out", [torch.bfloat16, torch.float32], ids=["bf16", "fp32"])
+@pytest.mark.parametrize("M,N,tile", [(1, 40, None), (2, 40, None), (4, 300, None), (20, 136, None), (70, 136, "0"),
+                                      (70, 136, "96"), (300, 520, "256"), (300, 520, "256x1"), (300, 515, "64")])
+def test_linear_scales_far_apart(M, N, tile, out, monkeypatch):
+    """Row scales from 2^-117 to 2^90 against channel scales of 2^-31 (their product has 2 bits left in fp32, the result
+    is a normal number) and 2^60 (their product is infinite, the sum 0): the bars of the other tests hold."""
+    if tile is not None:
+        monkeypatch.setenv("MOE_INT8_TILE", tile)
+    x = far_rows(M, 4096)
+    codes, scales = far_weights(N, 4096, 51, 2.0 ** -31)
+    y = moe.linear_int8(x.to(DEV), codes.to(DEV), scales.to(DEV), out_dtype=out)
+    xq, sx = quantize_ref(x.double().numpy())
+    want = (xq @ codes.double().numpy().T) * sx[:, None] * scales.double().numpy()
+    far_within(y, want, 5 * 2.0 ** -24 + STEP[out])
+    if M > 4:  # the same bits alone as among rows of other magnitudes
+        for m in range(4):
+            assert torch.equal(moe.linear_int8(x[m:m + 1].to(DEV), codes.to(DEV), scales.to(DEV), out_dtype=out)[0], y[m])
+
+
+@pytest.mark.parametrize("nmax,pair", [("32", "0"), ("128", "128"), ("128", "256")])
+@pytest.mark.parametrize("M", [3, 41, 300])
+def test_experts_scales_far_apart(M, nmax, pair, monkeypatch):
+    """The same in the projections: g is of order 1, u about 2^-122 out of scales of 2^-117 and 2^-31."""
+    set_widths(monkeypatch, nmax, pair)
+    shape = moe.Shape(M, 4096, 256, 2, 1, 16)
+    ids = (torch.arange(M)[:, None] % 3 == 1).int()
+    plan = moe.align_block_size(ids.to(DEV), 2, 16)
+    x = torch.full((M, 4096), 127 * 2.0 ** -117).to(torch.bfloat16)
+    gc, gs = far_weights(512, 4096, 52, 2.0 ** 91)
+    uc, us = far_weights(512, 4096, 53, 2.0 ** -31)
+    gs[::3] = 2.0 ** 91
+    gc[::3] = gc[1]
+    dc, ds = far_weights(8192, 256, 54, 2.0 ** -27)
+    iw = moe.Int8Weights(gc.view(2, 256, 4096).to(DEV), uc.view(2, 256, 4096).to(DEV), dc.view(2, 4096, 256).to(DEV),
+                         gs.view(2, 256).to(DEV), us.view(2, 256).to(DEV), ds.view(2, 4096).to(DEV))
+    h = torch.zeros(moe.align_capacity(shape), 256, dtype=torch.bfloat16, device=DEV)
+    moe.grouped_up_swiglu_int8(x.to(DEV), iw, plan, shape, h=h)
+    hin = far_rows(h.shape[0], 256)
+    y = moe.grouped_down_int8(hin.to(DEV), iw, plan, shape)
+    xq, sx = quantize_ref(x.double().numpy())
+    hq, sh = quantize_ref(hin.double().numpy())
+    counts, offs, sid = (plan[k].cpu().numpy() for k in ("expert_counts", "expert_offsets", "sorted_ids"))
+    g64 = lambda q, c, s, e, n, sc: (q @ c.view(2, n, -1)[e].double().numpy().T) * sc[:, None] * s.view(2, n)[e].double().numpy()  # noqa: E731
+    yw = np.zeros((M, 4096))
+    for e in range(2):
+        rows = np.arange(offs[e], offs[e] + counts[e])
+        t = sid[rows]
+        g, u = g64(xq[t], gc, gs, e, 256, sx[t]), g64(xq[t], uc, us, e, 256, sx[t])
+        far_within(h[rows], g / (1.0 + np.exp(-g)) * u, 2.0 ** -8 + (16 + 16 * np.abs(g).max()) * 2.0 ** -24)
+        yw[t] = g64(hq[rows], dc, ds, e, 4096, sh[rows])
+    far_within(y, yw, 2.0 ** -8 + 5 * 2.0 ** -24)
