@@ -375,8 +375,8 @@ MOE_API size_t moe_nvfp4_blob_bytes(moe_shape_t s, int which);
  * product with it is NaN.
  * src: bf16, row r at src + r * ld elements; codes: int8, row r at codes +
  * r * pitch (bytes from cols to the pitch are left as they were); scales: fp32
- * [rows].  Any alignment.  rows, cols >= 1, ld >= cols, pitch >= cols; rows < 2^31,
- * cols <= MOE_INT8_MAX_K. */
+ * [rows].  No alignment beyond the types' own.  rows, cols >= 1, ld >= cols,
+ * pitch >= cols; rows < 2^31, cols <= MOE_INT8_MAX_K. */
 #define MOE_INT8_MAX_K 131072 /* 131072 * 127 * 127 < 2^31: the sums are exact */
 MOE_API moe_status_t moe_quantize_int8(const moe_bf16_t* src, int64_t ld, int64_t rows, int64_t cols, int8_t* codes,
                                        int64_t pitch, float* scales, moe_stream_t stream);
@@ -388,12 +388,13 @@ MOE_API moe_status_t moe_quantize_int8(const moe_bf16_t* src, int64_t ld, int64_
  * int32, the scaling in fp32 (sx * w_scale first; in fp64 where that product is
  * no normal number of fp32, so that only the result's own range counts), rounded
  * to out_dtype (bf16 or fp32) at the end.  The int8 expert projections scale alike.
- * x: bf16, row m at x + m * ldx elements (any alignment, ldx >= K); w: int8
- * [N, K] codes, row n at w + n * ldw, w 16-byte aligned, ldw >= K a multiple of
- * 16 (codes between K and ldw are not read as values); w_scale: fp32 [N]; out:
- * row m at out + m * ldo elements, ldo >= N; ws: moe_linear_int8_workspace_size
- * bytes, 16-byte aligned (0, and ws may be null, where a few tokens take
- * one launch that quantises x itself); err_flag (nullable) as everywhere.
+ * x: bf16, row m at x + m * ldx elements, ldx >= K; w: int8 [N, K] codes, row n
+ * at w + n * ldw, w 16-byte aligned, ldw >= K a multiple of 16 (codes between K
+ * and ldw are not read as values); w_scale: fp32 [N]; out: row m at out + m * ldo
+ * elements, ldo >= N; x, w_scale and out need the alignment of their type only;
+ * ws: moe_linear_int8_workspace_size bytes, 16-byte aligned (0, and ws may be
+ * null, where a few tokens take one launch that quantises x itself); err_flag
+ * (nullable) as everywhere.
  * Accepted: 1 <= M, N <= 2^30 with (M/32 + 1) * (N/128 + 1) < 2^31;
  * 1 <= K <= MOE_INT8_MAX_K; else UNSUPPORTED. */
 MOE_API moe_status_t moe_linear_int8(const moe_bf16_t* x, int64_t ldx, const int8_t* w, int64_t ldw,

@@ -23,6 +23,9 @@ size_t align_up(size_t v, size_t a = kAlign) { return (v + a - 1) / a * a; }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
+// Whether an address is a multiple of `bytes`, a power of two (null is).
+bool aligned(const void* p, size_t bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; }
+
 bool is_pow2(int v) { return v > 0 && (v & (v - 1)) == 0; }
 
 moe_status_t check_shape(const moe_shape_t& s) {
@@ -582,6 +585,10 @@ Int8Layout int8_layout(size_t rows, size_t pitch) {
 Int8Layout int8_up_layout(const moe_shape_t& s) { return int8_layout(s.M, s.H); }
 Int8Layout int8_down_layout(const moe_shape_t& s) { return int8_layout(cap_rows(s), s.I); }
 
+bool int8_plan_aligned(const moe_plan_t& p) {
+  return aligned(p.expert_counts, 4) && aligned(p.expert_offsets, 4) && aligned(p.num_tokens_post_padded, 4);
+}
+
 moe::Int8GemmArgs int8_plan_args(const moe_plan_t* plan, const moe_shape_t& s, int32_t* err) {
   moe::Int8GemmArgs a{};
   a.sorted_ids = plan->sorted_ids;
@@ -800,7 +807,9 @@ moe_status_t check_layer_args(const moe_bf16_t* x, const moe_bf16_t* w_router, c
   if (!aligned16(x) || !aligned16(w_router) || !aligned16(gamma) || !aligned16(out) || !aligned16(w->gate) ||
       !aligned16(w->up) || !aligned16(w->down) || (residual_out && !aligned16(residual_out)))
     return MOE_ERR_INVALID_ARG;
-  if (w->dtype == MOE_W_INT8 && (!w->gate_gs || !w->up_gs || !w->down_gs)) return MOE_ERR_INVALID_ARG;
+  if (w->dtype == MOE_W_INT8 && (!w->gate_gs || !w->up_gs || !w->down_gs || !aligned(w->gate_gs, 4) ||
+                                 !aligned(w->up_gs, 4) || !aligned(w->down_gs, 4)))
+    return MOE_ERR_INVALID_ARG;
   if (!(eps >= 0.0f)) return MOE_ERR_INVALID_ARG;
   return MOE_OK;
 }
@@ -983,7 +992,8 @@ moe_status_t moe_grouped_up_swiglu(const moe_bf16_t* x, const moe_weights_t* w, 
     return run_up_nvfp4(x, w, plan, s, h, ws, err_flag, static_cast<cudaStream_t>(stream));
   }
   if (w->dtype == MOE_W_INT8) {
-    if (!w->gate_gs || !w->up_gs) return MOE_ERR_INVALID_ARG;
+    if (!w->gate_gs || !w->up_gs || !aligned(w->gate_gs, 4) || !aligned(w->up_gs, 4)) return MOE_ERR_INVALID_ARG;
+    if (!int8_plan_aligned(*plan) || !aligned(err_flag, 4)) return MOE_ERR_INVALID_ARG;
     if (!ws || ws_bytes < moe_up_workspace_size(s, MOE_W_INT8) || !aligned16(ws)) return MOE_ERR_WORKSPACE;
     return run_up_int8(x, w, plan, s, h, ws, err_flag, static_cast<cudaStream_t>(stream));
   }
@@ -1025,7 +1035,8 @@ moe_status_t moe_grouped_down(const moe_bf16_t* h, const moe_weights_t* w, const
     return run_down_nvfp4(h, w, plan, s, y, ws, err_flag, static_cast<cudaStream_t>(stream));
   }
   if (w->dtype == MOE_W_INT8) {
-    if (!w->down_gs || !plan->num_tokens_post_padded) return MOE_ERR_INVALID_ARG;
+    if (!w->down_gs || !plan->num_tokens_post_padded || !aligned(w->down_gs, 4)) return MOE_ERR_INVALID_ARG;
+    if (!int8_plan_aligned(*plan) || !aligned(err_flag, 4)) return MOE_ERR_INVALID_ARG;
     if (!ws || ws_bytes < moe_down_workspace_size(s, MOE_W_INT8) || !aligned16(ws)) return MOE_ERR_WORKSPACE;
     return run_down_int8(h, w, plan, s, y, ws, err_flag, static_cast<cudaStream_t>(stream));
   }
@@ -1172,7 +1183,8 @@ moe_status_t moe_route_logits(const void* logits, moe_dtype_t dtype, int64_t ld,
   if (st != MOE_OK) return st;
   if (!logits || !topk_ids || !topk_w) return MOE_ERR_INVALID_ARG;
   if ((dtype != MOE_DT_F32 && dtype != MOE_DT_BF16) || ld < E) return MOE_ERR_INVALID_ARG;
-  if ((reinterpret_cast<uintptr_t>(logits) & (dtype == MOE_DT_F32 ? 3u : 1u)) != 0) return MOE_ERR_INVALID_ARG;
+  if (!aligned(logits, dtype == MOE_DT_F32 ? 4 : 2) || !aligned(bias, 4) || !aligned(topk_ids, 4) || !aligned(topk_w, 4))
+    return MOE_ERR_INVALID_ARG;
   return cuda_status(moe::launch_route_group(logits, dtype == MOE_DT_BF16, ld, bias, M, E, top_k, group_opts(*opts),
                                              topk_ids, topk_w, static_cast<cudaStream_t>(stream)));
 }
@@ -1185,6 +1197,7 @@ moe_status_t moe_route_group(const moe_bf16_t* x, const moe_bf16_t* w_router, co
   if ((st = check_group_route(s.M, s.E, s.top_k, opts)) != MOE_OK) return st;
   if (!x || !w_router || !topk_ids || !topk_w) return MOE_ERR_INVALID_ARG;
   if (!aligned16(x) || !aligned16(w_router)) return MOE_ERR_INVALID_ARG;
+  if (!aligned(bias, 4) || !aligned(topk_ids, 4) || !aligned(topk_w, 4)) return MOE_ERR_INVALID_ARG;
   if (!ws || ws_bytes < moe_route_workspace_size(s) || !aligned16(ws)) return MOE_ERR_WORKSPACE;
   auto cs = static_cast<cudaStream_t>(stream);
   auto* logits = static_cast<float*>(ws);
@@ -1198,6 +1211,7 @@ moe_status_t moe_quantize_int8(const moe_bf16_t* src, int64_t ld, int64_t rows, 
                                int64_t pitch, float* scales, moe_stream_t stream) {
   if (rows < 1 || cols < 1 || rows >= (1ll << 31) || cols > MOE_INT8_MAX_K) return MOE_ERR_UNSUPPORTED;
   if (!src || !codes || !scales || ld < cols || pitch < cols) return MOE_ERR_INVALID_ARG;
+  if (!aligned(src, 2) || !aligned(scales, 4)) return MOE_ERR_INVALID_ARG;
   moe::Int8RowsArgs q{};
   q.src = src;
   q.ld = ld;
@@ -1221,6 +1235,8 @@ moe_status_t moe_linear_int8(const moe_bf16_t* x, int64_t ldx, const int8_t* w, 
   if (!x || !w || !w_scale || !out) return MOE_ERR_INVALID_ARG;
   if (out_dtype != MOE_DT_F32 && out_dtype != MOE_DT_BF16) return MOE_ERR_INVALID_ARG;
   if (ldx < K || ldw < K || ldo < N || ldw % 16 != 0 || !aligned16(w)) return MOE_ERR_INVALID_ARG;
+  if (!aligned(x, 2) || !aligned(w_scale, 4) || !aligned(out, out_dtype == MOE_DT_F32 ? 4 : 2) || !aligned(err_flag, 4))
+    return MOE_ERR_INVALID_ARG;
   const bool few = moe::int8_few_takes(M, N, K);
   if (!few && (!ws || ws_bytes < moe_linear_int8_workspace_size(M, N, K) || !aligned16(ws))) return MOE_ERR_WORKSPACE;
   auto cs = static_cast<cudaStream_t>(stream);

@@ -126,3 +126,38 @@ def test_binding_refusals():
     iw.gate_scales = torch.zeros(8, 127)
     with pytest.raises(ValueError):
         iw.check(S, "gate")
+
+
+def test_addresses_off_their_type_are_refused():
+    """A pointer that is no multiple of its type's size would fault on the GPU: every argument that needs no more
+    alignment than that is looked at (the others are tested above)."""
+    L, odd, half = moe.library(), ctypes.c_void_p(P + 1), ctypes.c_void_p(P + 2)
+    o = ctypes.byref(_GroupOpts(1, 1, 8, 4, 1, 1.0))
+    logits = lambda bias=FAKE, ids=FAKE, w=FAKE: L.moe_route_logits(FAKE, 0, 64, bias, 4, 64, 8, o, ids, w, None)  # noqa: E731
+    s64 = moe.Shape(4, 256, 128, 64, 8, 16).c()
+    group = lambda bias=FAKE, ids=FAKE, w=FAKE: L.moe_route_group(  # noqa: E731
+        FAKE, FAKE, bias, s64, o, ids, w, FAKE, 1 << 20, None)
+    for call in (logits, group):
+        for bad in (odd, half):
+            assert call(bias=bad) == 1 and call(ids=bad) == 1 and call(w=bad) == 1
+    quantize = lambda src=FAKE, sc=FAKE: L.moe_quantize_int8(src, 64, 4, 64, FAKE, 64, sc, None)  # noqa: E731
+    assert quantize(src=odd) == 1 and quantize(sc=odd) == 1 and quantize(sc=half) == 1
+    for M in (1, 40):
+        dense = lambda x=FAKE, sc=FAKE, out=FAKE, dt=1, err=None: L.moe_linear_int8(  # noqa: E731
+            x, 64, FAKE, 64, sc, M, 8, 64, out, 8, dt, FAKE, 1 << 20, err, None)
+        assert dense(x=odd) == 1 and dense(sc=half) == 1 and dense(out=odd) == 1
+        assert dense(out=half, dt=0) == 1 and dense(err=half) == 1
+    s, n = S.c(), 1 << 22
+    up = lambda w, p, err=None: L.moe_grouped_up_swiglu(FAKE, ctypes.byref(w), ctypes.byref(p), s, FAKE, FAKE, n, err, None)  # noqa: E731
+    down = lambda w, p, err=None: L.moe_grouped_down(FAKE, ctypes.byref(w), ctypes.byref(p), s, FAKE, FAKE, n, err, None)  # noqa: E731
+    w, p = _Weights(2, P, P, P, P, P, P), _Plan(P, P, P, P, P)
+    assert up(_Weights(2, P, P, P, P + 2, P, P), p) == 1 and up(_Weights(2, P, P, P, P, P + 2, P), p) == 1
+    assert down(_Weights(2, P, P, P, P, P, P + 2), p) == 1
+    for bad in (_Plan(P, P, P + 2, P, P), _Plan(P, P, P, P + 2, P)):
+        assert up(w, bad) == 1 and down(w, bad) == 1
+    assert down(w, _Plan(P, P, P, P, P + 2)) == 1
+    assert up(w, p, half) == 1 and down(w, p, half) == 1
+    layer = lambda w: L.moe_layer(FAKE, FAKE, None, ctypes.byref(w), FAKE, ctypes.c_float(1e-5), s, FAKE, None, None,  # noqa: E731
+                                  None, FAKE, 1 << 30, None)
+    for i in range(3):
+        assert layer(_Weights(2, P, P, P, *(P + 2 * (i == j) for j in range(3)))) == 1
