@@ -390,7 +390,7 @@ MOE_API moe_status_t moe_quantize_int8(const moe_bf16_t* src, int64_t ld, int64_
  * to out_dtype (bf16 or fp32) at the end.  The int8 expert projections scale alike.
  * x: bf16, row m at x + m * ldx elements, ldx >= K; w: int8 [N, K] codes, row n
  * at w + n * ldw, w 16-byte aligned, ldw >= K a multiple of 16 (codes between K
- * and ldw are not read as values); w_scale: fp32 [N]; out: row m at out + m * ldo
+ * and ldw are not read as values; the last row may end at K); w_scale: fp32 [N]; out: row m at out + m * ldo
  * elements, ldo >= N; x, w_scale and out need the alignment of their type only;
  * ws: moe_linear_int8_workspace_size bytes, 16-byte aligned (0, and ws may be
  * null, where a few tokens take one launch that quantises x itself); err_flag

@@ -60,13 +60,16 @@ __global__ void __launch_bounds__(kThreads, 1) int8_few_kernel(const uint16_t* _
   const int way = warp % ways, mine = warp / ways;
   const int first = lane + 32 * way, step = 32 * ways;  // this lane's chunks
 
-  // the first weights: they wait for nothing (a channel past the last reads the last one's and stores nothing)
+  // the first weights: they wait for nothing (a channel past the last reads the last one's and stores nothing).  The
+  // last row may end at its K codes: of a chunk that it does not fill nothing is loaded here
   uint4 a[kAhead];
   auto fetch = [&](int group, int c0) {
-    const int8_t* row = w + static_cast<int64_t>(min(group * at_once + mine, N - 1)) * ldw;
+    const int n = min(group * at_once + mine, N - 1);
+    const int8_t* row = w + static_cast<int64_t>(n) * ldw;
+    const int whole = n == N - 1 ? K / 16 : chunks;
 #pragma unroll
     for (int i = 0; i < kAhead; ++i)
-      a[i] = c0 + step * i < chunks ? load_weights(row + 16 * static_cast<int64_t>(c0 + step * i)) : make_uint4(0, 0, 0, 0);
+      a[i] = c0 + step * i < whole ? load_weights(row + 16 * static_cast<int64_t>(c0 + step * i)) : make_uint4(0, 0, 0, 0);
   };
   const int groups = (N + at_once - 1) / at_once;
   int group = blockIdx.x;
@@ -147,6 +150,12 @@ __global__ void __launch_bounds__(kThreads, 1) int8_few_kernel(const uint16_t* _
       }
     }
     const int n = group * at_once + mine;
+    if (n == N - 1 && way == 0 && lane < K % 16) {  // the rest of the last row, a code per lane
+      const int k = K / 16 * 16 + lane;
+      const int wk = w[static_cast<int64_t>(n) * ldw + k];
+#pragma unroll
+      for (int m = 0; m < kRows; ++m) acc[m] += wk * static_cast<int8_t>(codes[m * pitch + k]);
+    }
     if (group + static_cast<int>(gridDim.x) < groups) fetch(group + gridDim.x, first);
 #pragma unroll
     for (int m = 0; m < kRows; ++m) acc[m] = __reduce_add_sync(0xffffffffu, acc[m]);

@@ -701,3 +701,23 @@ def test_experts_scales_far_apart(M, nmax, pair, monkeypatch):
         far_within(h[rows], g / (1.0 + np.exp(-g)) * u, 2.0 ** -8 + (16 + 16 * np.abs(g).max()) * 2.0 ** -24)
         yw[t] = g64(hq[rows], dc, ds, e, 4096, sh[rows])
     far_within(y, yw, 2.0 ** -8 + 5 * 2.0 ** -24)
+
+
+@pytest.mark.parametrize("M", [1, 2, 4, 20, 40])
+@pytest.mark.parametrize("N,K", [(1, 1), (1, 15), (1, 17), (3, 33), (40, 1000), (5000, 47), (129, 8201), (2, 16400)])
+def test_linear_last_weight_row_ends_at_its_last_code(M, N, K):
+    """Weights whose storage ends with the last row's K codes: nothing behind them is asked for, and the last channel is
+    that of a padded copy."""
+    pitch = (K + 15) // 16 * 16
+    x = torch.randn(M, K, generator=gen(61)).to(torch.bfloat16).to(DEV)
+    codes, scales = (t.to(DEV) for t in codes_of(N, K, 62))
+    tight = torch.zeros((N - 1) * pitch + K, dtype=torch.int8, device=DEV).as_strided((N, K), (pitch, 1))
+    tight.copy_(codes)
+    assert tight.untyped_storage().nbytes() == (N - 1) * pitch + K
+    padded = torch.full((N + 1, pitch), 99, dtype=torch.int8, device=DEV)[:N, :K]
+    padded.copy_(codes)
+    y = moe.linear_int8(x, tight, scales, out_dtype=torch.float32)
+    assert torch.equal(y, moe.linear_int8(x, padded, scales, out_dtype=torch.float32))
+    xq, sx = quantize_ref(x.double().cpu().numpy())
+    want = (xq @ codes.double().cpu().numpy().T) * sx[:, None] * scales.double().cpu().numpy()
+    within(y, want, 5 * 2.0 ** -24)
