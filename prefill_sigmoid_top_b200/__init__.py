@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import importlib.util
 import os
 import threading
 from dataclasses import dataclass
@@ -158,16 +159,20 @@ def library():
 
 
 def _load_binding():
-    """The loaded _binding.so (built in-tree, like the library, on first use if it is missing)."""
+    """The loaded extension for this interpreter and torch (built in-tree, like the library, on first use if it is
+    missing)."""
     global _fast
     library()
     with _lock:
         if _fast is None:
-            if not os.path.exists(os.path.join(_PKG, "_binding.so")):
-                from . import build as _build
+            from . import build as _build
+            path = _build.binding_path()
+            if not os.path.exists(path):
                 _build.build_binding()
-            from . import _binding
-            _fast = _binding
+            spec = importlib.util.spec_from_file_location(f"{__name__}._binding", path)
+            module = importlib.util.module_from_spec(spec)
+            spec.loader.exec_module(module)
+            _fast = module
     return _fast
 
 

@@ -5,6 +5,7 @@ import concurrent.futures as cf
 import os
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -27,18 +28,21 @@ def _stale(out: str, deps: list[str]) -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
-BINDING = os.path.join(PKG, "_binding.so")
+def binding_path() -> str:
+    """The binding for this interpreter and this torch: it is compiled against the headers of both and fits no others,
+    so each pair has a file of its own and one that was built before an upgrade is not loaded after it."""
+    import torch
+    return os.path.join(PKG, f"_binding.{sysconfig.get_config_var('SOABI')}.torch-{torch.__version__}.so")
 
 
 def build_binding(force: bool = False) -> str:
     """Compile the CPython extension that marshals the short calls (csrc/binding.cpp), against libmoe_b200.so beside it."""
     src, header = os.path.join(CSRC, "binding.cpp"), os.path.join(ROOT, "include", "moe_b200.h")
-    if force or _stale(BINDING, [src, header]):
-        import sysconfig
-
+    path = binding_path()
+    if force or _stale(path, [src, header]):
         import torch
         tdir = os.path.dirname(torch.__file__)
-        tmp = BINDING + f".tmp{os.getpid()}"
+        tmp = path + f".tmp{os.getpid()}"
         subprocess.check_call([
             os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
             f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", sysconfig.get_paths()["include"],
@@ -48,8 +52,8 @@ def build_binding(force: bool = False) -> str:
             "-I", os.path.join(ROOT, "include"), src, "-o", tmp, "-L", PKG, "-l:libmoe_b200.so",
             "-L", os.path.join(tdir, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda",
             "-Wl,-rpath,$ORIGIN"])
-        os.replace(tmp, BINDING)
-    return BINDING
+        os.replace(tmp, path)
+    return path
 
 
 TRACE_LIB = os.path.join(PKG, "libmoe_b200_trace.so")
