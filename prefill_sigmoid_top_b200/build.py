@@ -43,15 +43,21 @@ def build_binding(force: bool = False) -> str:
         import torch
         tdir = os.path.dirname(torch.__file__)
         tmp = path + f".tmp{os.getpid()}"
-        subprocess.check_call([
-            os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+        cxx = os.environ.get("CXX", "g++")
+        cmd = [
+            cxx, "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
             f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", sysconfig.get_paths()["include"],
             "-isystem", os.path.join(tdir, "include"),
             "-isystem", os.path.join(tdir, "include", "torch", "csrc", "api", "include"),
             "-isystem", os.path.join(os.path.dirname(os.path.dirname(NVCC)), "include"),
             "-I", os.path.join(ROOT, "include"), src, "-o", tmp, "-L", PKG, "-l:libmoe_b200.so",
             "-L", os.path.join(tdir, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda",
-            "-Wl,-rpath,$ORIGIN"])
+            "-Wl,-rpath,$ORIGIN"]
+        try:
+            subprocess.check_call(cmd)
+        except (OSError, subprocess.CalledProcessError) as e:
+            raise RuntimeError(f"the Python binding was not built: {cxx} failed on {src} (it takes the headers of Python "
+                               f"and torch, which the C library does not): {e}") from e
         os.replace(tmp, path)
     return path
 
@@ -61,9 +67,10 @@ TRACE_LIB = os.path.join(PKG, "libmoe_b200_trace.so")
 
 def build(force: bool = False, verbose: bool = False, extra_flags: list[str] | None = None,
           trace: bool = False) -> str:
-    """Compile the library; trace=True builds the timeline variant instead (-DMOE_PAIR_TRACE for the
-    2-SM pair GEMMs, -DMOE_LAYER_TRACE for the single-launch layer, into libmoe_b200_trace.so; see
-    pair_trace.py and layer_trace.py), never loaded by the package."""
+    """Compile the library (nvcc alone; build_binding compiles what Python calls it through); trace=True
+    builds the timeline variant instead (-DMOE_PAIR_TRACE for the 2-SM pair GEMMs, -DMOE_LAYER_TRACE for
+    the single-launch layer, into libmoe_b200_trace.so; see pair_trace.py and layer_trace.py), never
+    loaded by the package."""
     build_dir = BUILD + ("_trace" if trace else "")
     lib = TRACE_LIB if trace else LIB
     os.makedirs(build_dir, exist_ok=True)
@@ -89,10 +96,21 @@ def build(force: bool = False, verbose: bool = False, extra_flags: list[str] | N
         tmp = lib + f".tmp{os.getpid()}"
         subprocess.check_call([NVCC, "-gencode", "arch=compute_100a,code=sm_100a", "-shared", *objs, "-o", tmp])
         os.replace(tmp, lib)
-    if not trace:
-        build_binding(force)
     return lib
 
 
+def main(argv: list[str]) -> int:
+    """Both, the library first: a C program needs that alone, so a binding that cannot be built here is reported and
+    leaves it in place."""
+    force, trace = "--force" in argv, "--trace" in argv
+    print(build(force=force, verbose="-v" in argv, trace=trace))
+    if not trace:
+        try:
+            print(build_binding(force))
+        except RuntimeError as e:
+            print(e, file=sys.stderr)
+    return 0
+
+
 if __name__ == "__main__":
-    print(build(force="--force" in sys.argv, verbose="-v" in sys.argv, trace="--trace" in sys.argv))
+    sys.exit(main(sys.argv[1:]))
