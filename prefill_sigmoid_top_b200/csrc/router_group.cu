@@ -30,8 +30,14 @@
 //            rcp.approx within 2^-23; the scaled argument of the exponential adds |z| 2^-23.4 relative)
 //   softmax: relative 2^-19 + |z - max| 2^-23, and p <= e^-|z - max| / denom: below 2^-18 / denom
 //            (exponentials 2^-22, their sum 11 roundings, reciprocal and product 2^-22: less than 2^-19)
-// plus 2^-23 of each sum that follows.  Weights: an exponential and a denominator of such (sigmoid: a sum of K <= 32
-// scores in 5 levels), at most 24 roundings of 2^-24: within 2^-19.  Of bf16 logits, two that are nearer than their spacing are equal: a tie.
+// plus 2^-23 of each sum that follows.  Of bf16 logits, two that are nearer than their spacing are equal: a tie.
+// Weights, in fp32 (in fp64 they and a denominator's exponentials would cost more than the choice), in units of 2^-24:
+//   numerator: expf 4; sigmoid: the sum with 1 and its rcp.approx 1 + 2; softmax: the factor for z - max 1;
+//   denominator, renormalised: numerators in 5 levels of a sum, 5 more;
+//     softmax over all: expf 4; the rounding of z - max, |z - max| at most, 4.5 in the mean over the shares of 1024
+//     experts (all but one 5.4 below it); 6 levels in a lane and 5 over the lanes 11;
+//   rcp.approx 2, two products 2.
+// Sigmoid 7 + 12 + 4 = 23, softmax renormalised 5 + 10 + 4 = 19, over all 5 + 19.5 + 4 = 28.5: within 2^-19 = 32.
 // Keys below the range, -inf among them, share the lowest integer: where one counts in the sum of a group that stays,
 // the token is fp64's.  About 1 token in 1000 of normal logits and a small bias has two
 // neighbours too near (2 in 100 with 1024 experts and K = 32).  Where that is all, the K + 1 listed keys are computed

@@ -721,3 +721,20 @@ def test_linear_last_weight_row_ends_at_its_last_code(M, N, K):
     xq, sx = quantize_ref(x.double().cpu().numpy())
     want = (xq @ codes.double().cpu().numpy().T) * sx[:, None] * scales.double().cpu().numpy()
     within(y, want, 5 * 2.0 ** -24)
+
+
+@pytest.mark.parametrize("nmax,pair", [("32", "0"), ("128", "128"), ("128", "256")])
+@pytest.mark.parametrize("M,E,K,skew", [(300, 1024, 2, 0.3), (90, 1000, 5, 1.0), (1, 1024, 32, 0.0), (700, 100, 1, 1.5)])
+def test_experts_up_to_the_limit(M, E, K, skew, nmax, pair, monkeypatch):
+    """As many experts as are accepted, and counts that are no multiple of 32: the counts and the tile list in shared
+    memory, the search for a tile's expert, experts without a token, the last expert's tokens."""
+    set_widths(monkeypatch, nmax, pair)
+    shape = moe.Shape(M, 256, 128, E, K, 16)
+    ids = random_ids(M, E, K, E + K, skew)
+    ids[0, 0] = E - 1
+    if K > 1:
+        ids[0, 1] = 0
+    x, ids, plan, mats, iw = experts_case(shape, seed=71, ids=ids)
+    assert (plan["expert_counts"] == 0).any() and plan["expert_counts"][-1] > 0
+    check_up(shape, x, plan, mats, iw)
+    check_down(shape, torch.randn(moe.align_capacity(shape), 128, generator=gen(72)).to(torch.bfloat16).to(DEV), plan, mats, iw)

@@ -300,3 +300,21 @@ def test_experts_masked_by_infinities(G, gs, TG, K, part, dtype, scoring):
         for logits, bias in ((zm, None), (zm, b), (z, bm), (zm, bm)):
             check(logits, bias, K, G, TG, group_score, scoring)
             check(logits, bias, K, G, TG, group_score, scoring, renorm=False)
+
+
+@pytest.mark.parametrize("E,top", [(1024, 5.4), (1000, 5.0), (960, 6.0), (300, 4.2)])
+def test_softmax_weights_with_a_wide_denominator(E, top):
+    """One logit and E - 1 of about `top` below it, where the rounding of z - max in the denominator's exponentials counts
+    most.  Units of 2^-24: numerator expf 4 and its correction 1; denominator expf 4, the rounding of differences in
+    [4, 8) 4 (half a step), at most 11 levels of the sum; reciprocal 2, two products 2: 28."""
+    g = torch.Generator().manual_seed(E)
+    z = 3.7 - top + 0.1 * torch.rand(64, E, generator=g)
+    z[torch.arange(64), torch.randint(0, E, (64,), generator=g)] = 3.7
+    z -= torch.rand(64, 1, generator=g)
+    for bias in (None, 0.001 * torch.randn(E, generator=g)):
+        ids, w = moe.route_logits(z.to(DEV), None if bias is None else bias.to(DEV), 8, scoring=moe.SCORE_SOFTMAX,
+                                  renormalize=False)
+        ids_r, w_r = reference(z.numpy(), None if bias is None else bias.numpy(), 8, 1, 1, moe.GROUP_TOP2,
+                               moe.SCORE_SOFTMAX, False, 1.0)
+        assert np.array_equal(ids.cpu().numpy(), ids_r)
+        assert (np.abs(w.cpu().numpy() - w_r) <= 28 * 2.0 ** -24 * w_r).all()
