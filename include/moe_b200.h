@@ -169,8 +169,9 @@ MOE_API moe_status_t moe_route_ex(const moe_bf16_t* x, const moe_bf16_t* w_route
  *           -> lower id;  topk_w[t,k] = w_k * routed_scale with w_k = p_k, or
  *           p_k / sum_j p_j over the K selected (renormalize; 0 if that sum is 0).
  * The selection is that of fp64 arithmetic (p, keys and group scores in fp64,
- * the softmax sum in any order);
- * the weights are within 2^-19 (relative) of exact ones.  A NaN logit counts as
+ * the softmax sum in any order); the weights are exact ones rounded to fp32 once,
+ * within 2^-24 (1 + 2^-5), except a SOFTMAX without renormalize, whose sum over
+ * all experts takes fp32 exponentials: within 2^-20 (relative).  A NaN logit counts as
  * -inf, a NaN key or group score ranks as -inf; with +inf among softmax logits the +inf entries share the scores, and
  * a row of -inf only has scores 0.  The ids are always K different experts of
  * the chosen groups, also where keys are -inf.

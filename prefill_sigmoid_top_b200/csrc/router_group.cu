@@ -23,7 +23,7 @@
 //     stay by one warp maximum each.
 //  4. top_k + 1 rounds of ONE warp maximum (redux) over the lists' first integers; the owner moves its list up.  The
 //     round past the last shows the gap behind the choice.
-//  5. weights from the K logits.
+//  5. weights from the K logits, in fp64.
 // Two keys are in the right order where their integers are 3 or more apart (one is off by less than a step) and that
 // distance exceeds what the keys may be off by:
 //   sigmoid: |p32 - p| <= p (1 - p) (|z| 2^-23.4 + 2^-22) + p (2^-24 + 2^-23) < 1.5 * 2^-22 (ex2.approx is within 2^-22,
@@ -31,13 +31,12 @@
 //   softmax: relative 2^-19 + |z - max| 2^-23, and p <= e^-|z - max| / denom: below 2^-18 / denom
 //            (exponentials 2^-22, their sum 11 roundings, reciprocal and product 2^-22: less than 2^-19)
 // plus 2^-23 of each sum that follows.  Of bf16 logits, two that are nearer than their spacing are equal: a tie.
-// Weights, in fp32 (in fp64 they and a denominator's exponentials would cost more than the choice), in units of 2^-24:
-//   numerator: expf 4; sigmoid: the sum with 1 and its rcp.approx 1 + 2; softmax: the factor for z - max 1;
-//   denominator, renormalised: numerators in 5 levels of a sum, 5 more;
-//     softmax over all: expf 4; the rounding of z - max, |z - max| at most, 4.5 in the mean over the shares of 1024
-//     experts (all but one 5.4 below it); 6 levels in a lane and 5 over the lanes 11;
-//   rcp.approx 2, two products 2.
-// Sigmoid 7 + 12 + 4 = 23, softmax renormalised 5 + 10 + 4 = 19, over all 5 + 19.5 + 4 = 28.5: within 2^-19 = 32.
+// Weights: exponentials of the K chosen logits, their sum and the quotients in fp64 (a few instructions each: far fewer
+// bits are needed than exp() and a division give), rounded to fp32 once: within 2^-24 (1 + 2^-5).  A softmax that is not
+// renormalised has a denominator over all experts, whose exponentials in fp64 would cost more than the choice: they are
+// expf (within 4 units of 2^-24), times a factor for the rounding of z - max (1), summed in fp32 in a lane (up to 6
+// levels) and in fp64 over the lanes: with the last rounding within 12 units, 2^-20.  Weights in fp32 throughout were
+// off by up to 28 units (measured: 1.2) and took 23.5 us instead of 25.0 for 32767 tokens.
 // Keys below the range, -inf among them, share the lowest integer: where one counts in the sum of a group that stays,
 // the token is fp64's.  About 1 token in 1000 of normal logits and a small bias has two
 // neighbours too near (2 in 100 with 1024 experts and K = 32).  Where that is all, the K + 1 listed keys are computed
@@ -83,6 +82,29 @@ __device__ __forceinline__ float rcp_approx(float x) {
   float y;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+
+// e^x for x in [-100, 81], within 2^-31 (relative): x = k ln 2 + r with |r| <= ln 2 / 2, then Taylor's series to r^8 (the
+// next term is below 2^-32).  k leaves the sum with 1.5 * 2^52 as its low word.
+__device__ __forceinline__ double exp_reduced(double x) {
+  constexpr double kRound = 6755399441055744.0;
+  const double t = fma(x, 1.4426950408889634, kRound);
+  const double r = fma(kRound - t, 0.6931471805599453, x);
+  double p = 1.0 / 40320.0;
+  p = fma(p, r, 1.0 / 5040.0);
+  p = fma(p, r, 1.0 / 720.0);
+  p = fma(p, r, 1.0 / 120.0);
+  p = fma(p, r, 1.0 / 24.0);
+  p = fma(p, r, 1.0 / 6.0);
+  p = fma(p, r, 0.5);
+  p = fma(p, r, 1.0);
+  p = fma(p, r, 1.0);
+  return __hiloint2double(__double2hiint(p) + (__double2loint(t) << 20), __double2loint(p));
+}
+// 1 / d for a d in fp32's normal range, within 2^-44: one step of Newton's method from the fp32 reciprocal.
+__device__ __forceinline__ double reciprocal(double d) {
+  const double y = static_cast<double>(rcp_approx(static_cast<float>(d)));
+  return fma(y, fma(-d, y, 1.0), y);
 }
 
 // e^(z - zmax) at the limits: a row whose largest logit is +inf shares among its +inf entries, a row of -inf only has
@@ -312,13 +334,26 @@ __global__ void __launch_bounds__(32 * kWarps) route_group_kernel(const void* __
     for (int i = 0; i < kPer; ++i) v[i] = i < n ? raw_logit<kBf16>(row, e0 + i) : 0.0f;
   }
   float zmax = 0.0f, denom = 1.0f;
+  double denom64 = 1.0;  // of the weights, where they are shares of all experts
   if (softmax) {
     zmax = -INFINITY;
 #pragma unroll
     for (int i = 0; i < kPer; ++i)
       if (kFull || i < n) zmax = fmaxf(zmax, v[i]);
     zmax = from_order_bits(__reduce_max_sync(0xffffffffu, order_bits(zmax)));
-    if (!by_logit || group_sums || !o.renormalize) {
+    if (!o.renormalize) {
+      // the rounding of z - max counts in full in the exponential of a far logit: it goes in as a factor
+      denom64 = tree_sum<kPer>([&](int i) {
+        if (!kFull && i >= n) return 0.0f;
+        const float d = v[i] - zmax, back = d + zmax;
+        const float lost = (v[i] - back) + ((back - d) - zmax);  // z - max = d + lost
+        const float e = expf(d);
+        return e > 0.0f ? fmaf(e, lost, e) : 0.0f;
+      });
+#pragma unroll
+      for (int off = 16; off >= 1; off >>= 1) denom64 += shfl_xor_d(denom64, off);
+      denom = static_cast<float>(denom64);
+    } else if (!by_logit || group_sums) {
       denom = tree_sum<kPer>([&](int i) { return kFull || i < n ? expf(v[i] - zmax) : 0.0f; });
 #pragma unroll
       for (int off = 16; off >= 1; off >>= 1) denom += __shfl_xor_sync(0xffffffffu, denom, off);
@@ -561,28 +596,25 @@ __global__ void __launch_bounds__(32 * kWarps) route_group_kernel(const void* __
   }
 
   // ---- 5. weights
-  float p = 0.0f;
-  if (lane < K) {
-    if (softmax) {
-      // the rounding of z - max counts in full in the exponential of a far logit: it goes in as a factor
-      const float d = zsel - zmax, back = d + zmax;
-      const float lost = (zsel - back) + ((back - d) - zmax);  // z - max = d + lost
-      const float e = expf(d);
-      p = fmaf(e, lost, e);
-    } else {
-      p = rcp_approx(1.0f + expf(-zsel));
+  double p = 0.0;
+  if (lane < K) {  // z >= -80 here (softmax: z - zmax)
+    const double z = static_cast<double>(zsel);
+    const double e = exp_reduced(softmax ? z - static_cast<double>(zmax) : -fmin(z, 100.0));
+    p = softmax ? e : reciprocal(1.0 + e);
+  }
+  double total = denom64;
+  if (o.renormalize) {
+    total = p;
+    if (K > 8) {
+      total += shfl_xor_d(total, 16);
+      total += shfl_xor_d(total, 8);
     }
-  }
-  float total = p;
-  if (K > 8) {
-    total += __shfl_xor_sync(0xffffffffu, total, 16);
-    total += __shfl_xor_sync(0xffffffffu, total, 8);
-  }
 #pragma unroll
-  for (int off = 4; off >= 1; off >>= 1) total += __shfl_xor_sync(0xffffffffu, total, off);
+    for (int off = 4; off >= 1; off >>= 1) total += shfl_xor_d(total, off);
+  }
   if (lane < K) {
     ids[lane] = sel;
-    w[lane] = p * rcp_approx(o.renormalize ? total : denom) * o.routed_scale;
+    w[lane] = static_cast<float>(p * (reciprocal(total) * static_cast<double>(o.routed_scale)));
   }
 }
 

@@ -318,3 +318,39 @@ def test_softmax_weights_with_a_wide_denominator(E, top):
                                moe.SCORE_SOFTMAX, False, 1.0)
         assert np.array_equal(ids.cpu().numpy(), ids_r)
         assert (np.abs(w.cpu().numpy() - w_r) <= 28 * 2.0 ** -24 * w_r).all()
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["fp32", "bf16"])
+@pytest.mark.parametrize("G,gs,TG,K", [(8, 32, 4, 8), (1, 64, 1, 32), (4, 256, 2, 17), (1, 5, 1, 1), (17, 60, 9, 24), (5, 12, 2, 7)])
+@pytest.mark.parametrize("spread", [0.01, 1.5, 12.0])
+def test_weights_are_rounded_once(spread, G, gs, TG, K, dtype):
+    """The weights of sigmoid scores and of a renormalised softmax are those of fp64 with one rounding to fp32: half a
+    step, 2^-24, and 2^-5 of that for the arithmetic before it.  A softmax over all experts: 12 * 2^-24 (exponentials 4,
+    their argument 1, at most 6 levels of an fp32 sum, the rounding 1)."""
+    z, b = rand(500, G * gs, G + K, dtype, spread)
+    for scoring, renorm, units in ((moe.SCORE_SIGMOID, True, 1 + 2.0 ** -5), (moe.SCORE_SIGMOID, False, 1 + 2.0 ** -5),
+                                   (moe.SCORE_SOFTMAX, True, 1 + 2.0 ** -5), (moe.SCORE_SOFTMAX, False, 12)):
+        for bias in (None, b):
+            ids, w = moe.route_logits(z.to(DEV), None if bias is None else bias.to(DEV), K, G, TG, moe.GROUP_TOP2, scoring,
+                                      renorm, 2.5)
+            ids_r, w_r = reference(z.float().numpy(), None if bias is None else bias.numpy(), K, G, TG, moe.GROUP_TOP2,
+                                   scoring, renorm, 2.5)
+            assert np.array_equal(ids.cpu().numpy(), ids_r)
+            w, normal = w.cpu().numpy().astype(np.float64), w_r >= 2.0 ** -126
+            assert (np.abs(w - w_r)[normal] <= units * 2.0 ** -24 * w_r[normal]).all()
+
+
+def test_weights_over_the_range_of_logits():
+    """One expert's score itself, from e^-90 to 1, and pairs of which one is that far below the other.  Scores below
+    2^-126 are subnormal numbers of fp32, 2^-149 apart: there half a step is 2^-150, whatever the value."""
+    z = torch.cat([torch.linspace(-90.0, 40.0, 20011), torch.tensor([-80.0, -80.00001, 0.0, -0.0, 88.0, 100.0, 700.0, 3e38])])
+    _, w = moe.route_logits(z[:, None].to(DEV), None, 1, renormalize=False)
+    want = 1.0 / (1.0 + np.exp(-z.double().numpy()))
+    bar = lambda v: (1 + 2.0 ** -5) * np.maximum(2.0 ** -24 * v, 2.0 ** -150)  # noqa: E731
+    assert (np.abs(w.cpu().numpy()[:, 0] - want) <= bar(want)).all()
+    pair = torch.stack([z[:20011], torch.zeros(20011)], 1)
+    for scoring in (moe.SCORE_SIGMOID, moe.SCORE_SOFTMAX):
+        ids, w = moe.route_logits(pair.to(DEV), None, 2, scoring=scoring)
+        ids_r, w_r = reference(pair.numpy(), None, 2, 1, 1, moe.GROUP_TOP2, scoring, True, 1.0)
+        assert np.array_equal(ids.cpu().numpy(), ids_r)
+        assert (np.abs(w.cpu().numpy() - w_r) <= bar(w_r)).all()
