@@ -621,7 +621,7 @@ __global__ void __launch_bounds__(32 * kWarps) route_group_kernel(const void* __
 template <bool kBf16, int kPer>
 cudaError_t launch_per(const void* logits, int64_t ld, const float* bias, int M, int E, int K, const RouteGroupOpts& o,
                        int32_t* topk_ids, float* topk_w, cudaStream_t stream) {
-  const dim3 grid((M + kWarps - 1) / kWarps);
+  const dim3 grid((M - 1) / kWarps + 1);  // M + kWarps - 1 may pass 2^31
   const int size = kBf16 ? 2 : 4;
   const int vec = kPer * size < 16 ? size : 16;  // bytes of a load
   const bool full = E == 32 * kPer && (o.n_group & (o.n_group - 1)) == 0 && (ld * size) % vec == 0 &&

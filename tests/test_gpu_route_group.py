@@ -354,3 +354,20 @@ def test_weights_over_the_range_of_logits():
         ids_r, w_r = reference(pair.numpy(), None, 2, 1, 1, moe.GROUP_TOP2, scoring, True, 1.0)
         assert np.array_equal(ids.cpu().numpy(), ids_r)
         assert (np.abs(w.cpu().numpy() - w_r) <= bar(w_r)).all()
+
+
+@pytest.mark.parametrize("M", [2 ** 31 - 1, 2 ** 31 - 4])
+def test_as_many_tokens_as_are_accepted(M):
+    """One expert and one choice: M * top_k just below 2^31."""
+    if torch.cuda.mem_get_info()[0] < 40 << 30:
+        pytest.skip("needs 40 GB")
+    z = torch.zeros(M, 1, dtype=torch.bfloat16, device=DEV)
+    z[-1] = 1.0
+    ids = torch.full((M, 1), -7, dtype=torch.int32, device=DEV)
+    w = torch.full((M, 1), -7.0, device=DEV)
+    moe.route_logits(z, None, 1, renormalize=False, topk_ids=ids, topk_w=w)
+    assert not ids.any()
+    assert float(w[-1]) == np.float32(1.0 / (1.0 + np.exp(-1.0)))
+    assert not (w[:-1] != 0.5).any()
+    del z, ids, w
+    torch.cuda.empty_cache()
