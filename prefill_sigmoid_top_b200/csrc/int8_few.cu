@@ -9,11 +9,17 @@
 // products added to an int32 sum).  Codes, scales and sums are those of the other forms, so the results are the same
 // bits.
 //
-// Bound: the chain; then HBM, and with more tokens the shared-memory reads of their codes beside it.  Measured, this
-// form / two launches (us): 2048 x 7168, 1 token 5.0 / 8.7, 2 tokens 6.2 / 10, 4 tokens 8.6 / 9.4, 8 tokens 13.6 / 9.6;
-// 7168 x 7168, 1 token 9.4 / 12.3, 4 tokens 16.3 / 12.5; 40000 x 7168, 1 token 45.5 (6.3 TB/s).  So it is taken for one
-// or two tokens, and for up to four where the weights are at most 16 MB (int8_few_takes).
+// Bound: the chain; then HBM, and with more tokens the shared-memory reads of their codes beside it.  Measured, replayed
+// with the weights in L2, this form / two launches (us): 2048 x 7168, 1 token 5.1 / 8.7, 2 tokens 6.2 / 10, 4 tokens
+// 8.4 / 9.4, 8 tokens 13.6 / 9.6; 7168 x 7168, 4 tokens 16.3 / 12.5.  With other weights each time, as in a model's step:
+// 2048 x 7168, 1 token 6.5, 2 tokens 7.4, 4 tokens 9.3 (8 in two launches 9.8); 7168 x 7168, 1 token 12.9, 2 tokens 14.6
+// (4 in two launches 14.9); 40000 x 7168, 1 token 46 (6.2 TB/s).  So it is taken for one or two tokens, and for up to
+// four where the weights are at most 16 MB (int8_few_takes).
+//
+// The last weight row may end at its K codes: where K is no multiple of 16 its last chunk is taken code by code (a form
+// of its own, since the check and its code cost 0.1 to 0.4 us).
 #include <algorithm>
+#include <type_traits>
 
 #include "int8_rows.cuh"
 #include "kernels.h"
@@ -41,8 +47,8 @@ __device__ __forceinline__ int dot16(const uint4& a, const uint4& b, int c) {
   return __dp4a(static_cast<int>(a.w), static_cast<int>(b.w), c);
 }
 
-// kRows: tokens, rounded up to a power of two (the codes of absent ones are 0).
-template <int kRows>
+// kRows: tokens, rounded up to a power of two (the codes of absent ones are 0).  kRagged: K is no multiple of 16.
+template <int kRows, bool kRagged>
 __global__ void __launch_bounds__(kThreads, 1) int8_few_kernel(const uint16_t* __restrict__ x, int64_t ldx, bool vectors,
                                                                const int8_t* __restrict__ w, int64_t ldw, int ways,
                                                                const Int8GemmArgs args) {
@@ -66,7 +72,7 @@ __global__ void __launch_bounds__(kThreads, 1) int8_few_kernel(const uint16_t* _
   auto fetch = [&](int group, int c0) {
     const int n = min(group * at_once + mine, N - 1);
     const int8_t* row = w + static_cast<int64_t>(n) * ldw;
-    const int whole = n == N - 1 ? K / 16 : chunks;
+    const int whole = kRagged && n == N - 1 ? K / 16 : chunks;
 #pragma unroll
     for (int i = 0; i < kAhead; ++i)
       a[i] = c0 + step * i < whole ? load_weights(row + 16 * static_cast<int64_t>(c0 + step * i)) : make_uint4(0, 0, 0, 0);
@@ -134,6 +140,7 @@ __global__ void __launch_bounds__(kThreads, 1) int8_few_kernel(const uint16_t* _
 
   // ---- channels
   for (; group < groups; group += gridDim.x) {
+    const int n = group * at_once + mine;
     int acc[kRows];
 #pragma unroll
     for (int m = 0; m < kRows; ++m) acc[m] = 0;
@@ -148,13 +155,6 @@ __global__ void __launch_bounds__(kThreads, 1) int8_few_kernel(const uint16_t* _
             acc[m] = dot16(a[i], *reinterpret_cast<const uint4*>(codes + m * pitch + 16 * c), acc[m]);
         }
       }
-    }
-    const int n = group * at_once + mine;
-    if (n == N - 1 && way == 0 && lane < K % 16) {  // the rest of the last row, a code per lane
-      const int k = K / 16 * 16 + lane;
-      const int wk = w[static_cast<int64_t>(n) * ldw + k];
-#pragma unroll
-      for (int m = 0; m < kRows; ++m) acc[m] += wk * static_cast<int8_t>(codes[m * pitch + k]);
     }
     if (group + static_cast<int>(gridDim.x) < groups) fetch(group + gridDim.x, first);
 #pragma unroll
@@ -174,6 +174,9 @@ __global__ void __launch_bounds__(kThreads, 1) int8_few_kernel(const uint16_t* _
 #pragma unroll
         for (int m = 0; m < kRows; ++m) sum = lane == m ? acc[m] : sum;
       }
+      if (kRagged && n == N - 1)  // the rest of the last row
+        for (int k = K / 16 * 16; k < K; ++k)
+          sum += w[static_cast<int64_t>(n) * ldw + k] * static_cast<int8_t>(codes[lane * pitch + k]);
       const float r = int8_value(scale[lane], args.ch_scale0[n], sum);
       const size_t at = static_cast<size_t>(lane) * args.out_ld + n;
       if (args.out_f32)
@@ -185,10 +188,10 @@ __global__ void __launch_bounds__(kThreads, 1) int8_few_kernel(const uint16_t* _
   }
 }
 
-template <int kRows>
+template <int kRows, bool kRagged>
 cudaError_t launch_rows(const uint16_t* x, int64_t ldx, const int8_t* w, int64_t ldw, const Int8GemmArgs& args,
                         int num_sms, cudaStream_t stream) {
-  auto kern = int8_few_kernel<kRows>;
+  auto kern = int8_few_kernel<kRows, kRagged>;
   int dev = 0;
   cudaError_t st = cudaGetDevice(&dev);
   if (st != cudaSuccess) return st;
@@ -221,9 +224,13 @@ bool int8_few_takes(int64_t M, int64_t N, int64_t K) {
 
 cudaError_t launch_int8_few(const uint16_t* x, int64_t ldx, const int8_t* w, int64_t ldw, const Int8GemmArgs& args,
                             int num_sms, cudaStream_t stream) {
-  if (args.M <= 1) return launch_rows<1>(x, ldx, w, ldw, args, num_sms, stream);
-  if (args.M <= 2) return launch_rows<2>(x, ldx, w, ldw, args, num_sms, stream);
-  return launch_rows<4>(x, ldx, w, ldw, args, num_sms, stream);
+  auto rows = [&](auto ragged) {
+    constexpr bool kRagged = decltype(ragged)::value;
+    if (args.M <= 1) return launch_rows<1, kRagged>(x, ldx, w, ldw, args, num_sms, stream);
+    if (args.M <= 2) return launch_rows<2, kRagged>(x, ldx, w, ldw, args, num_sms, stream);
+    return launch_rows<4, kRagged>(x, ldx, w, ldw, args, num_sms, stream);
+  };
+  return args.kdim % 16 != 0 ? rows(std::true_type{}) : rows(std::false_type{});
 }
 
 }  // namespace moe
