@@ -262,8 +262,8 @@ MOE_API size_t moe_up_workspace_size(moe_shape_t s, moe_wdtype_t dtype);
  * err_flag: device int32 (nullable), MOE_ERR_INVALID_INPUT if an id lies
  * outside [0,E) (outputs then unspecified).
  * Limit: M*top_k <= MOE_ROUTED_UP_MAX_SLOTS, else MOE_ERR_UNSUPPORTED;
- * NVFP4 weights: MOE_ERR_UNSUPPORTED.  moe_layer takes this path by itself on
- * decode shapes. */
+ * NVFP4 and int8 weights: MOE_ERR_UNSUPPORTED.  moe_layer takes this path by
+ * itself on decode shapes. */
 #define MOE_ROUTED_UP_MAX_SLOTS 1024
 MOE_API moe_status_t moe_grouped_up_swiglu_routed(const moe_bf16_t* x, const moe_weights_t* w,
                                                   const int32_t* topk_ids, moe_shape_t s, int32_t* sorted_ids,

@@ -606,7 +606,8 @@ moe::Int8GemmArgs int8_plan_args(const moe_plan_t* plan, const moe_shape_t& s, i
 // from 16 tokens per expert: at 20 they cost 2 percent where tokens are spread evenly (up, 32 experts of 7168 x 2048:
 // 157 us against 154) and gain 10 to 20 where they are not (up 159 against 177, down 87 against 98; down of 64 experts
 // of 2048 x 1024 33 against 41), since an expert of more than 32 tokens has its weights read twice by single CTAs; at
-// 12 they lose (up 58 against 51).  MOE_GEMM_PAIR, MOE_GEMM_PERSISTENT and MOE_GEMM_NMAX override as for bf16 (single
+// 12 they lose (up 58 against 51).  The rule sees the mean alone, for which no look at the plan is needed: a few busy
+// experts under a mean below 16 cost single CTAs repeated reads of their weights, from L2, how much was not measured.  MOE_GEMM_PAIR, MOE_GEMM_PERSISTENT and MOE_GEMM_NMAX override as for bf16 (single
 // CTAs take tiles of 32 tokens in any case: of 128 they are slower than pairs at every size).
 int int8_pair_nmax(const moe_shape_t& s) {
   const bool forced = std::getenv("MOE_GEMM_PERSISTENT") != nullptr || std::getenv("MOE_GEMM_NMAX") != nullptr;

@@ -19,10 +19,10 @@
 // of its copies in series); with three: 8192 x 7168 x 7168 314 -> 299 us, prefill up 1467 -> 1403 us, batch up 1128 ->
 // 1102 us.
 //
-// Measured: 8192 x 7168 x 7168 299 us with its quantiser (2.8 Pop/s; 356 us under the power cap of a long run), batch
-// up (512 tokens, 256 experts) 1.12 ms at 6.8 TB/s, skewed prefill (2048 tokens) up 1.42 ms, down 0.80 ms.  Bound: HBM
-// for the experts with few tokens, power and the operand feed for the busy ones (tensor pipe 67% active at
-// 4096 x 7168 x 7168).
+// Measured, replayed alone / as calls in a row, which run under the power cap, with their quantisers: 8192 x 7168 x 7168
+// 301 / 365 us (2.8 / 2.3 Pop/s), batch up (512 tokens, 256 experts) 1.12 / 1.21 ms (6.8 / 6.3 TB/s), skewed prefill
+// (2048 tokens) up 1.41 / 1.70 ms, down 0.80 / 0.96 ms.  Bound: HBM for the experts with few tokens, power and the
+// operand feed for the busy ones (tensor pipe 67% active at 4096 x 7168 x 7168).
 //
 // The launch overlaps the kernel before it (programmatic dependent launch): set-up and the first weight boxes come
 // before the wait for it.  Every mbarrier wait is bounded; a timeout sets the error word and unwinds, and both CTAs

@@ -36,17 +36,18 @@
 // renormalised has a denominator over all experts, whose exponentials in fp64 would cost more than the choice: they are
 // expf (within 4 units of 2^-24), times a factor for the rounding of z - max (1), summed in fp32 in a lane (up to 6
 // levels) and in fp64 over the lanes: with the last rounding within 12 units, 2^-20.  Weights in fp32 throughout were
-// off by up to 28 units (measured: 1.2) and took 23.5 us instead of 25.0 for 32767 tokens.
+// off by up to 28 units (measured: 1.2) and took 21.6 us instead of 23.4 for 32767 tokens.
 // Keys below the range, -inf among them, share the lowest integer: where one counts in the sum of a group that stays,
 // the token is fp64's.  About 1 token in 1000 of normal logits and a small bias has two
 // neighbours too near (2 in 100 with 1024 experts and K = 32).  Where that is all, the K + 1 listed keys are computed
 // exactly, one per lane, and put in order; the rest goes to the fp64 path as a whole, whose 10 to 40 us for one token
 // would otherwise be the tail of every large call.
 //
-// Measured (256 experts in 8 groups, 4 kept, K = 8, sigmoid and bias, fp32): 8 tokens 2.6 us, 32767 tokens 21.6 us
-// (1.6 TB/s; 577 instructions per token, 79% of the issue slots in use; more warps per SM change nothing); 2048 tokens of bf16 logits, softmax,
-// K = 16: 3.9 us; a part of the experts masked by -inf changes nothing (softmax: 32 -> 40 us).  Tried and slower: persistent warps that fetch their next token ahead (35 us), keys and ids in
-// shared memory with two warp reductions per choice (50 us).
+// Measured (256 experts in 8 groups, 4 kept, K = 8, sigmoid and bias, fp32): 8 tokens 2.5 us, 32767 tokens 23.4 us
+// (1.5 TB/s; 630 instructions per token, 53 of them for the weights in fp64, 81% of the issue slots in use; more warps per
+// SM change nothing); 2048 tokens of bf16 logits, softmax, K = 16: 4.3 us; a part of the experts masked by -inf changes
+// nothing (softmax: 32 -> 40 us).  Tried and slower, before the weights were in fp64 (21.6 us): persistent warps that
+// fetch their next token ahead (35 us), keys and ids in shared memory with two warp reductions per choice (50 us).
 #include "common.cuh"
 #include "kernels.h"
 
