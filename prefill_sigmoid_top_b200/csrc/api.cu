@@ -607,8 +607,9 @@ moe::Int8GemmArgs int8_plan_args(const moe_plan_t* plan, const moe_shape_t& s, i
 // 157 us against 154) and gain 10 to 20 where they are not (up 159 against 177, down 87 against 98; down of 64 experts
 // of 2048 x 1024 33 against 41), since an expert of more than 32 tokens has its weights read twice by single CTAs; at
 // 12 they lose (up 58 against 51).  The rule sees the mean alone, for which no look at the plan is needed: a few busy
-// experts under a mean below 16 cost single CTAs repeated reads of their weights, from L2, how much was not measured.  MOE_GEMM_PAIR, MOE_GEMM_PERSISTENT and MOE_GEMM_NMAX override as for bf16 (single
-// CTAs take tiles of 32 tokens in any case: of 128 they are slower than pairs at every size).
+// experts under a mean below 16 cost single CTAs repeated reads of their weights, from L2; how much was not measured.
+// MOE_GEMM_PAIR, MOE_GEMM_PERSISTENT and MOE_GEMM_NMAX override as for bf16 (single CTAs take tiles of 32 tokens in any
+// case: of 128 they are slower than pairs at every size).
 int int8_pair_nmax(const moe_shape_t& s) {
   const bool forced = std::getenv("MOE_GEMM_PERSISTENT") != nullptr || std::getenv("MOE_GEMM_NMAX") != nullptr;
   const bool pairs = forced ? want_persistent(s) : static_cast<long long>(s.M) * s.top_k >= 16ll * s.E;

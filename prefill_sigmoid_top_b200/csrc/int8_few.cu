@@ -74,8 +74,10 @@ __global__ void __launch_bounds__(kThreads, 1) int8_few_kernel(const uint16_t* _
     const int8_t* row = w + static_cast<int64_t>(n) * ldw;
     const int whole = kRagged && n == N - 1 ? K / 16 : chunks;
 #pragma unroll
-    for (int i = 0; i < kAhead; ++i)
-      a[i] = c0 + step * i < whole ? load_weights(row + 16 * static_cast<int64_t>(c0 + step * i)) : make_uint4(0, 0, 0, 0);
+    for (int i = 0; i < kAhead; ++i) {
+      const int c = c0 + step * i;
+      a[i] = c < whole ? load_weights(row + 16 * static_cast<int64_t>(c)) : make_uint4(0, 0, 0, 0);
+    }
   };
   const int groups = (N + at_once - 1) / at_once;
   int group = blockIdx.x;

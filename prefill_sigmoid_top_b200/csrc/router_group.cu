@@ -44,9 +44,9 @@
 // would otherwise be the tail of every large call.
 //
 // Measured (256 experts in 8 groups, 4 kept, K = 8, sigmoid and bias, fp32): 8 tokens 2.5 us, 32767 tokens 23.4 us
-// (1.5 TB/s; 630 instructions per token, 53 of them for the weights in fp64, 81% of the issue slots in use; more warps per
-// SM change nothing); 2048 tokens of bf16 logits, softmax, K = 16: 4.3 us; a part of the experts masked by -inf changes
-// nothing (softmax: 32 -> 40 us).  Tried and slower, before the weights were in fp64 (21.6 us): persistent warps that
+// (1.5 TB/s; 630 instructions per token, 53 of them for the weights in fp64, 81% of the issue slots in use; more warps
+// per SM change nothing); 2048 tokens of bf16 logits, softmax, K = 16: 4.3 us; a part of the experts masked by -inf
+// changes nothing (softmax: 32 -> 40 us).  Tried and slower, before the weights were in fp64 (21.6 us): persistent warps that
 // fetch their next token ahead (35 us), keys and ids in shared memory with two warp reductions per choice (50 us).
 #include "common.cuh"
 #include "kernels.h"
